@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 import numpy as np
@@ -85,6 +86,10 @@ _SIGS = {
     "dls_attention_status": (ctypes.c_int, [vp, vp]),
     "dls_attention_workspace_bytes": (sz, [i32, i32, i32, i32, i32]),
     "dls_attention_decode_noalloc": (ctypes.c_int, [vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, vp, vp]),
+    "dls_qk_norm_rope": (ctypes.c_int, [vp, vp]),
+    "dls_kv_append": (ctypes.c_int, [vp, vp]),
+    "dls_attention_chunk": (ctypes.c_int, [vp, vp]),
+    "dls_attention_chunk_workspace_bytes": (ctypes.c_uint64, [i32]),
     "dls_kquant_packed_bytes": (ctypes.c_uint64, [i32, i32, i32]),
     "dls_kquant_pack": (ctypes.c_int, [i32, vp, i32, i32, vp, vp]),
     "dls_kquant_gemv": (ctypes.c_int, [i32, vp, i32, i32, vp, vp, vp, vp]),
@@ -198,6 +203,175 @@ def attention_decode_noalloc(q, k_pages, v_pages, page_table, lengths, o, n_batc
                                                _ptr(lengths), _ptr(o), n_batch, n_heads, n_kv_heads, head_dim,
                                                page_tokens, max_pages, n_splits, _ptr(status),
                                                _stream_handle(stream)))
+
+
+# --- the paged cache: filling it and attending over it
+
+DLS_F32, DLS_F16, DLS_BF16 = 1, 2, 3
+ROPE_PAIRINGS = {"adjacent": 0, "halves": 1}
+# the header's descriptors, packed in one go (native sizes and alignment)
+_QK_NORM_ROPE = struct.Struct("@4P4q4P8if")
+_KV_APPEND = struct.Struct("@6P4q2P5P12if")
+_ATTENTION_CHUNK = struct.Struct("@8PPQP2q11if")
+_dtypes = {}
+
+
+def _dtype(t, name):
+    if not _dtypes:
+        import torch
+
+        _dtypes.update({torch.float32: DLS_F32, torch.float16: DLS_F16, torch.bfloat16: DLS_BF16})
+    try:
+        return _dtypes[t.dtype]
+    except KeyError:
+        raise ValueError(f"{name}: type {t.dtype} (float32, float16 or bfloat16)") from None
+
+
+def _rows(t, name, n=None, heads=None, hd=None, typ=None):
+    """(pointer, elements between tokens) of a [tokens, heads, head_dim] tensor whose rows are contiguous."""
+    if t.dim() != 3:
+        raise ValueError(f"{name}: shape {tuple(t.shape)} ([tokens, heads, head_dim])")
+    shape, stride = t.shape, t.stride()
+    if (n is not None and shape[0] != n) or (heads is not None and shape[1] != heads) or (hd is not None and shape[2] != hd):
+        raise ValueError(f"{name}: shape {tuple(shape)}, wanted {(n, heads, hd)}")
+    if typ is not None and _dtype(t, name) != typ:
+        raise ValueError(f"{name}: type {t.dtype}")
+    row = shape[1] * shape[2]
+    if (stride[2] != 1 and shape[2] > 1) or (stride[1] != shape[2] and shape[1] > 1):
+        raise ValueError(f"{name}: a token's heads must be contiguous (strides {stride})")
+    return t.data_ptr(), (stride[0] if shape[0] > 1 else row)
+
+
+def _array(t, name, typ, shape):
+    """Pointer of a contiguous tensor of the given type (its name) and shape; None -> 0."""
+    if t is None:
+        return 0
+    if str(t.dtype) != typ or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)}, wanted contiguous {typ} {shape}")
+    return t.data_ptr()
+
+
+def _call(fn, desc, stream, *tensors):
+    """One library call on the tensors' own device (all on one)."""
+    import torch
+
+    device = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and (t.get_device() != device or not t.is_cuda):
+            raise ValueError("all tensors must be on one CUDA device")
+    if torch.cuda.current_device() == device:
+        _check(fn(desc, _stream_handle(stream)))
+    else:
+        with torch.cuda.device(device):
+            _check(fn(desc, _stream_handle(stream)))
+
+
+def _inv_freq(inv_freq):
+    if inv_freq is None:
+        return None, 0, 0
+    a = np.ascontiguousarray(inv_freq, dtype=np.float64)
+    if a.ndim != 1:
+        raise ValueError(f"inv_freq: shape {a.shape} ([rot_dim / 2])")
+    return a, a.ctypes.data, 2 * a.size
+
+
+def _pools(k_pages, v_pages, page_table, cu_q, kv_len):
+    """Shapes of the cache and the batch: (pages, KV heads, page tokens, head_dim, table pointer, entries of a
+    sequence, cu_q and kv_len pointers, sequences)."""
+    if k_pages.dim() != 4 or k_pages.shape != v_pages.shape or k_pages.dtype != v_pages.dtype:
+        raise ValueError(f"k_pages {tuple(k_pages.shape)} {k_pages.dtype}, v_pages {tuple(v_pages.shape)} {v_pages.dtype}: "
+                         "one [pages, kv_heads, page_tokens, head_dim] and type wanted")
+    if not k_pages.is_contiguous() or not v_pages.is_contiguous():
+        raise ValueError("k_pages and v_pages must be contiguous")
+    if page_table.dim() != 2:
+        raise ValueError(f"page_table: shape {tuple(page_table.shape)} ([sequences, pages])")
+    n, most = page_table.shape
+    return (*k_pages.shape, _array(page_table, "page_table", "torch.int32", (n, most)), most,
+            _array(cu_q, "cu_q", "torch.int32", (n + 1,)), _array(kv_len, "kv_len", "torch.int32", (n,)), n)
+
+
+def rope_inv_freq(rot_dim: int, theta: float) -> np.ndarray:
+    """theta^(-2 i / rot_dim), radians per position: the frequencies of the model's own decode path."""
+    return float(theta) ** (-np.arange(0, rot_dim, 2, dtype=np.float64) / rot_dim)
+
+
+def qk_norm_rope(q, k, positions, inv_freq, q_out, k_out, *, q_norm=None, k_norm=None, eps=1e-5, pairing="adjacent",
+                 stream=None):
+    """Per-head RMSNorm (where a norm is given) and rotation of q and k [tokens, heads, head_dim] into q_out and
+    k_out, which may be q and k themselves.  Either pair may be None.  positions: device int32 [tokens]; inv_freq:
+    host float64 [rot_dim / 2], or None for no rotation."""
+    one = q if q is not None else k
+    if one is None or (q is None) != (q_out is None) or (k is None) != (k_out is None):
+        raise ValueError("q with q_out, k with k_out, or both")
+    n, _, hd = one.shape if one.dim() == 3 else (0, 0, 0)
+    typ = _dtype(one, "q")
+    out = _dtype(q_out if q is not None else k_out, "q_out")
+    qp = qs = qop = qos = qh = kp = ks = kop = kos = kh = 0
+    if q is not None:
+        qh = q.shape[1] if q.dim() == 3 else 0
+        qp, qs = _rows(q, "q")
+        qop, qos = _rows(q_out, "q_out", n, qh, hd, out)
+    if k is not None:
+        kh = k.shape[1] if k.dim() == 3 else 0
+        kp, ks = _rows(k, "k", n, None, hd, typ)
+        kop, kos = _rows(k_out, "k_out", n, kh, hd, out)
+    keep, fp, rot = _inv_freq(inv_freq)
+    desc = _QK_NORM_ROPE.pack(qp, kp, qop, kop, qs, ks, qos, kos, _array(q_norm, "q_norm", "torch.float32", (hd,)),
+                              _array(k_norm, "k_norm", "torch.float32", (hd,)),
+                              _array(positions, "positions", "torch.int32", (n,)), fp, n, qh, kh, hd, rot,
+                              ROPE_PAIRINGS[pairing], typ, out, eps)
+    _call(load().dls_qk_norm_rope, desc, stream, one, q_out, k, k_out, q_norm, k_norm, positions)
+
+
+def kv_append(k, v, k_pages, v_pages, page_table, cu_q, kv_len, inv_freq, *, q=None, q_out=None, q_norm=None, k_norm=None,
+              eps=1e-5, pairing="adjacent", status=None, stream=None):
+    """Append a ragged chunk's keys (normed where k_norm is given, rotated by their cache position) and values
+    [tokens, kv_heads, head_dim] to the pages; with q, q_out = q normed and rotated in the same pass, in the
+    cache's type.  cu_q: device int32 [sequences + 1], kv_len: device int32 [sequences], the new tokens counted."""
+    pages, kvh, pt, hd, table, most, cu, kl, seqs = _pools(k_pages, v_pages, page_table, cu_q, kv_len)
+    if (q is None) != (q_out is None):
+        raise ValueError("q with q_out, or neither")
+    typ, kv_type = _dtype(k, "k"), _dtype(k_pages, "k_pages")
+    kp, ks = _rows(k, "k", None, kvh, hd)
+    n = k.shape[0]
+    vptr, vs = _rows(v, "v", n, kvh, hd, typ)
+    qp = qs = qop = qos = qh = 0
+    if q is not None:
+        qp, qs = _rows(q, "q", n, None, hd, typ)
+        qh = q.shape[1]
+        qop, qos = _rows(q_out, "q_out", n, qh, hd, kv_type)
+    keep, fp, rot = _inv_freq(inv_freq)
+    desc = _KV_APPEND.pack(kp, vptr, qp, k_pages.data_ptr(), v_pages.data_ptr(), qop, ks, vs, qs, qos,
+                           _array(k_norm, "k_norm", "torch.float32", (hd,)),
+                           _array(q_norm, "q_norm", "torch.float32", (hd,)), table, cu, kl, fp,
+                           _array(status, "status", "torch.int32", (1,)), n, seqs, qh, kvh, hd, rot,
+                           ROPE_PAIRINGS[pairing], typ, kv_type, pt, pages, most, eps)
+    _call(load().dls_kv_append, desc, stream, k, v, k_pages, v_pages, page_table, cu_q, kv_len, q, q_out, q_norm, k_norm,
+          status)
+
+
+def attention_chunk_workspace_bytes(head_dim: int) -> int:
+    return int(load().dls_attention_chunk_workspace_bytes(head_dim))
+
+
+def attention_chunk(q, k_pages, v_pages, page_table, cu_q, kv_len, o, workspace, *, lse=None, scale=0.0, causal=True,
+                    window=0, status=None, stream=None):
+    """Attention of ragged chunks of new tokens (q, o [tokens, heads, head_dim] in the cache's type) over the paged
+    cache.  workspace: a uint8 tensor of attention_chunk_workspace_bytes(head_dim) zeros, kept from call to call.
+    lse: fp32 [tokens, heads] or None.  scale 0: 1 / sqrt(head_dim)."""
+    pages, kvh, pt, hd, table, most, cu, kl, seqs = _pools(k_pages, v_pages, page_table, cu_q, kv_len)
+    kv_type = _dtype(k_pages, "k_pages")
+    qp, qs = _rows(q, "q", None, None, hd, kv_type)
+    n, heads, _ = q.shape
+    op, os_ = _rows(o, "o", n, heads, hd, kv_type)
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    desc = _ATTENTION_CHUNK.pack(qp, k_pages.data_ptr(), v_pages.data_ptr(), table, cu, kl, op,
+                                 _array(lse, "lse", "torch.float32", (n, heads)), workspace.data_ptr(),
+                                 workspace.numel() * workspace.element_size(),
+                                 _array(status, "status", "torch.int32", (1,)), qs, os_, n, seqs, heads, kvh, hd, pt, pages,
+                                 most, kv_type, int(bool(causal)), window, scale)
+    _call(load().dls_attention_chunk, desc, stream, q, k_pages, v_pages, page_table, cu_q, kv_len, o, workspace, lse, status)
 
 
 DLS_Q4_K = 12

@@ -425,6 +425,147 @@ int dls_kquant_pack(int32_t type, const void* blocks, int32_t rows, int32_t cols
 int dls_kquant_gemv(int32_t type, const void* packed, int32_t rows, int32_t cols, const float* x, float* y,
                     int32_t* status, void* cuda_stream);
 
+/* ---- the paged cache: filling it and attending over it ------------------------ */
+
+/* Standalone operators for callers that run their own projections around a
+ * paged cache of the layout above (pools [n_pages][n_kv_heads][page_tokens]
+ * [head_dim], page tables of int32, negative = no page): norm and rotation
+ * of q and k, the append of a chunk's keys and values, and attention of the
+ * chunk over the pages (SwarmKV page, sections 2 and 3: prefill fills the
+ * cache once and branches continue over it; the engine page, section 4.4:
+ * RoPE, causal softmax with the mask inside the kernel).
+ *
+ * Common to the three calls:
+ *  - Tensors are device memory of the current device, rows (one token's
+ *    heads, contiguous) `*_stride` elements apart, so slices of a fused
+ *    projection's output can be passed as they are.  Pointers are 16-byte
+ *    aligned and strides a multiple of 16 bytes (else DLS_ERR_ARG).
+ *  - A batch is ragged: sequence b's new tokens are rows cu_q[b] ..
+ *    cu_q[b + 1] - 1 (device int32 [n_seqs + 1], not decreasing, cu_q[0] >= 0)
+ *    and kv_len[b] (device int32 [n_seqs]) counts the sequence's cached
+ *    tokens WITH the new ones, so new token i stands at position kv_len[b] -
+ *    (cu_q[b + 1] - cu_q[b]) + i.  Rows outside every sequence (a padded
+ *    batch) may hold anything and are not written.  The lengths stay on the device: a
+ *    captured graph follows them from replay to replay.
+ *  - status: device int32 [1] or NULL.  The call zeroes it on cuda_stream;
+ *    bit 1 is or-ed in for a page-table entry outside [0, n_pages), bit 4
+ *    for lengths that do not fit (cu_q decreasing or outside [0, n_tokens],
+ *    kv_len negative or above page_tokens * max_pages, an append with
+ *    kv_len below the chunk's length) and bit 8 when a bounded wait ran out.  Read it with
+ *    dls_attention_status.  What a flagged entry would have addressed is
+ *    skipped, never accessed.
+ *  - Work is enqueued on cuda_stream (NULL: the default stream); nothing is
+ *    allocated or synchronised.  Errors are in dls_last_error(NULL). */
+
+/* Element types (dls_dtype). */
+typedef enum dls_dtype { DLS_F32 = 1, DLS_F16 = 2, DLS_BF16 = 3 } dls_dtype;
+/* Which elements of a head rotate together: 2i and 2i + 1, as the model's
+ * own decode path, or i and i + rot_dim / 2. */
+typedef enum dls_rope_pairing { DLS_ROPE_ADJACENT = 0, DLS_ROPE_HALVES = 1 } dls_rope_pairing;
+
+/* Per-head RMSNorm and rotation of q and k in one pass over them:
+ *   y = x * rsqrt(mean(x^2) + eps) * norm      (where norm is given)
+ *   pair i of the first rot_dim elements turned by position * inv_freq[i]
+ * in fp32, rounded once to out_type; the elements from rot_dim on are not
+ * turned.  Angles are reduced in 64-bit fixed point, exact in the position
+ * for the full int32 range.  An output may be its own input (in place, same
+ * type and stride), and must not overlap an input otherwise. */
+typedef struct dls_qk_norm_rope_desc {
+  const void* q;            /* in_type [n_tokens][n_heads][head_dim]; unused when n_heads = 0 */
+  const void* k;            /* in_type [n_tokens][n_kv_heads][head_dim]; unused when n_kv_heads = 0 */
+  void* q_out;              /* out_type, the same shapes */
+  void* k_out;
+  int64_t q_stride, k_stride, q_out_stride, k_out_stride; /* elements from one token to the next */
+  const float* q_norm;      /* device fp32 [head_dim], or NULL: no norm */
+  const float* k_norm;
+  const int32_t* positions; /* device [n_tokens], any int32 */
+  const double* inv_freq;   /* HOST [rot_dim / 2], radians per position; read during the call */
+  int32_t n_tokens, n_heads, n_kv_heads;
+  int32_t head_dim;         /* a multiple of 16, 16..256 */
+  int32_t rot_dim;          /* a multiple of 16, 0..head_dim */
+  int32_t pairing;          /* dls_rope_pairing */
+  int32_t in_type, out_type; /* dls_dtype */
+  float eps;                /* >= 0 */
+} dls_qk_norm_rope_desc;
+int dls_qk_norm_rope(const dls_qk_norm_rope_desc* d, void* cuda_stream);
+
+/* Append a ragged chunk's keys and values to the pages of their sequences:
+ * K normed (where k_norm is given), rotated by its cache position and
+ * rounded once to kv_type, V rounded to kv_type.  With q given, q_out =
+ * the normed and rotated q in kv_type, as dls_attention_chunk reads it, in
+ * the same pass.  A token whose page is missing keeps its q_out; its K and
+ * V are dropped and flagged.  Two rows that name the same slot (pages shared
+ * by two sequences that both append) leave one of the two in it. */
+typedef struct dls_kv_append_desc {
+  const void* k;            /* in_type [n_tokens][n_kv_heads][head_dim] */
+  const void* v;
+  const void* q;            /* in_type [n_tokens][n_heads][head_dim], or NULL */
+  void* k_pages;            /* kv_type pools */
+  void* v_pages;
+  void* q_out;              /* kv_type [n_tokens][n_heads][head_dim]; with q */
+  int64_t k_stride, v_stride, q_stride, q_out_stride;
+  const float* k_norm;      /* device fp32 [head_dim], or NULL */
+  const float* q_norm;
+  const int32_t* page_table; /* device [n_seqs][max_pages] */
+  const int32_t* cu_q;
+  const int32_t* kv_len;
+  const double* inv_freq;   /* HOST [rot_dim / 2] */
+  int32_t* status;
+  int32_t n_tokens, n_seqs, n_heads, n_kv_heads;
+  int32_t head_dim, rot_dim, pairing; /* as above */
+  int32_t in_type;          /* dls_dtype */
+  int32_t kv_type;          /* DLS_F16 or DLS_BF16 */
+  int32_t page_tokens;      /* 16, 32, 64, 128 or 256 */
+  int32_t n_pages, max_pages;
+  float eps;
+} dls_kv_append_desc;
+int dls_kv_append(const dls_kv_append_desc* d, void* cuda_stream);
+
+/* Attention of ragged chunks of new tokens over the paged cache: each
+ * query head of each new token over its sequence's keys (its KV head's),
+ *   o = sum_k softmax_k(scale * q . K[k]) V[k]
+ * causal: keys 0 .. the token's own position; else all kv_len keys.  window
+ * w > 0 (causal only): the newest w of them.  One call serves whole prompts,
+ * chunks over a prefix, verify passes, single tokens and any mix.  A row
+ * with no key (kv_len below the chunk's length) gives o = 0 and lse = -inf.
+ * Scores, softmax statistics and sums are fp32; the weights are rounded to
+ * kv_type for the product with V.  Keys at or past kv_len, and before every
+ * window, are never used, whatever their pages hold, and their page-table
+ * entries are not read.  Results do not depend on timing: partial sums are
+ * joined in a fixed order.
+ * workspace: dls_attention_chunk_workspace_bytes(head_dim) bytes, 256-byte
+ * aligned, zeroed before its first call (a call leaves it ready for the
+ * next, of any shape with that head_dim or a smaller one; zero it again after a call that
+ * reported bit 8).  Calls that may overlap on the GPU need one each. */
+typedef struct dls_attention_chunk_desc {
+  const void* q;            /* kv_type [n_tokens][n_heads][head_dim], rotated */
+  const void* k_pages;      /* kv_type pools */
+  const void* v_pages;
+  const int32_t* page_table; /* device [n_seqs][max_pages] */
+  const int32_t* cu_q;
+  const int32_t* kv_len;
+  void* o;                  /* kv_type [n_tokens][n_heads][head_dim] */
+  float* lse;               /* device fp32 [n_tokens][n_heads]: log sum exp of the scaled scores, or NULL */
+  void* workspace;
+  uint64_t workspace_bytes;
+  int32_t* status;
+  int64_t q_stride, o_stride; /* elements from one token to the next */
+  int32_t n_tokens;         /* rows of q and o, padding included */
+  int32_t n_seqs;           /* 0..DLS_MAX_CHUNK_SEQS */
+  int32_t n_heads, n_kv_heads; /* a multiple of n_kv_heads, at most 128 query heads per KV head */
+  int32_t head_dim;         /* a multiple of 16, 16..128 */
+  int32_t page_tokens;      /* 16, 32, 64, 128 or 256 */
+  int32_t n_pages, max_pages;
+  int32_t kv_type;          /* DLS_F16 or DLS_BF16 */
+  int32_t causal;           /* 0 or 1 */
+  int32_t window;           /* 0 = none */
+  float scale;              /* > 0; 0 = 1 / sqrt(head_dim) */
+} dls_attention_chunk_desc;
+#define DLS_MAX_CHUNK_SEQS 4096
+int dls_attention_chunk(const dls_attention_chunk_desc* d, void* cuda_stream);
+/* Workspace bytes (0 for a bad head_dim). */
+uint64_t dls_attention_chunk_workspace_bytes(int32_t head_dim);
+
 /* ---- test and profiling hooks ------------------------------------------------ */
 
 /* Arm a capture of the residual stream after every layer for the next
