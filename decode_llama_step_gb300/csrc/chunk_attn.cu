@@ -1,96 +1,980 @@
-// Attention of ragged chunks of new tokens over the paged cache.
+// Attention of ragged chunks of new tokens over the paged cache, on the
+// 5th-generation tensor cores.
 //
-// Simple form: a warp per (row, query head) walks the row's keys with a
-// running maximum and sum (m, l) and the unnormalised output in registers,
-//   m' = max(m, s);  l = l e^(m - m') + e^(s - m');  o = o e^(m - m') + e^(s - m') v
-// a lane holding the elements lane, lane + 32, ... of the head.
+// Mathematics: for a query row with raw scores s_k = q . K[k] over its keys,
+// c = scale * log2(e) and any reference R, with p_k = 2^(c s_k - R):
+//   o = sum_k p_k V[k] / sum_k p_k,   lse = R ln 2 + ln sum_k p_k
+// One pass over the keys in tiles of 128 keeps (R, l = sum p, O = sum p V);
+// R follows the running maximum, but only when it falls more than 2^8
+// behind, because moving R costs a pass over O (O *= 2^(R - R'), l likewise).
+// Ranges of keys done by different CTAs are joined by the same formula.
+//
+// A tile of work is a KV head and up to 2 * (128 / G) consecutive new tokens
+// of a sequence: two 128-row MMA operands ("slots"), row = token * G + query
+// head of the group, so one K/V tile from the pages serves 256 rows:
+//   S = Q K^T   tcgen05.mma M = 128, N = 128 keys, K = head_dim (fp32 in TMEM)
+//   P = 2^(...) softmax warps, thread = row, written over S as 16-bit TMEM operand
+//   O += P V    M = 128, N = head_dim, K = 128 keys (A from TMEM, V MN-major)
+// While one slot's softmax runs, the tensor core works for the other.  Tiles
+// with rows for one slot only (few new tokens) give both slots the same Q
+// and every second key tile ("split"), joined in the epilogue; with at most
+// 32 rows ("quad") Q is replicated into the four lane quarters of the
+// operand and each softmax warp takes a quarter of the key columns, so a
+// single token's softmax is spread over all eight warps.
+//
+// Work is divided by key tiles, not by sequences: the key tiles of all
+// (KV head, sequence, token tile) in a row are cut into one equal range per
+// CTA, whatever the mix of prompts and single tokens; a tile cut by a range
+// border leaves partial (R, l, O) in the workspace and the last CTA to arrive
+// joins them in range order.  Each CTA finds its range itself from the
+// device-side lengths, so a call is one launch and a captured graph follows
+// the lengths.
+//
+// Warps: 0 copies (TMA), 1 MMA, 2 the CTA's piece list, 4-7 / 8-11 softmax of
+// slot 0 / 1.  Every wait is bounded (2 s) and sets an abort flag.
 #include <cuda_bf16.h>
 #include <math.h>
 
+#include <mutex>
+
 #include "../../include/dls.h"
 #include "kernels.h"
+#include "tc.cuh"
 
 namespace dls {
 
 namespace {
 
+constexpr int BK = 128;          // keys per tile
+constexpr int MAXC = 152;        // CTAs at most (one per SM)
+constexpr int CTHREADS = 384;
+constexpr int CWARPS = CTHREADS / 32;
+constexpr int QDEPTH = 4;        // pieces the list runs ahead
+constexpr int kMinSteps = 2;     // key tiles of a range at least (one per slot of a split tile)
+constexpr float kGrow = 8.f;     // log2 the maximum may exceed the reference by
+constexpr float kShift = 7.f;    // weights are kept as 2^(c s - R + 7): at most 2^15 in fp16, with 7 more binades below
+constexpr uint64_t kWaitNsC = 2000000000ull;
+constexpr int kCounterBytes = 4096;  // int [MAXC][2], at the start of the workspace
+
+enum Mode { PAIR = 0, SPLIT = 1, QUAD = 2, END = 3 };
+
 struct ChunkArgs {
-  const void *q, *k, *v;
   void* o;
   float* lse;
   const int32_t *page_table, *cu_q, *kv_len;
   int32_t* status;
-  long long q_stride, o_stride;
-  int n_tokens, n_seqs, n_heads, n_kv, head_dim;
-  int page_shift, n_pages, max_pages;
+  int* counters;
+  float* partials;
+  long long o_stride;
+  int n_tokens, n_seqs, n_kv, group, head_dim;
+  int page_shift, n_pages, max_pages, pool_rows;
   int causal, window;
-  float scale;
+  int tpq;      // tokens of a slot: 128 / group
+  int tpq_quad; // tokens of a quad tile: 32 / group (0: none)
+  float c;      // scale * log2(e)
 };
 
-__device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
-__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ void from_f(float x, __half* y) { *y = __float2half_rn(x); }
-__device__ __forceinline__ void from_f(float x, __nv_bfloat16* y) { *y = __float2bfloat16_rn(x); }
+// What a CTA does at a time: key tiles [ja, jb) of one tile of work.
+struct Piece {
+  int mode, b, kvh;
+  int row0, n;        // first row (token) in q / o, tokens
+  int pos0, kl, lo;   // position of the first token, cached keys, first key any row may see
+  int ja, jb;
+  int np, idx, c0;    // pieces of the tile, which one this is, CTA of its first one
+};
+
+template <int HDP>
+struct CCfg {
+  static constexpr int KA = HDP / 64;        // 64-wide swizzle atoms along the head dimension
+  static constexpr int kQ = 128 * HDP * 2;   // one slot's Q
+  static constexpr int kKV = BK * HDP * 2;   // one K or V tile
+  static constexpr int NST = HDP == 128 ? 4 : 8;
+  static constexpr int kKVOff = 2 * kQ;
+  static constexpr int kXOff = kKVOff + NST * kKV;  // float [4][32][32]: joins the quarters of a quad tile
+  static constexpr int kMiscOff = kXOff + 4 * 32 * 32 * 4;
+};
+
+struct CMisc {
+  uint64_t full[8], empty[8], s_full[2], p_full[2], o_full[2], o_free[2], q_full, q_empty, x_full, wg[2], pq_full[QDEPTH], pq_empty[QDEPTH];
+  Piece pq[QDEPTH];
+  float xm[128], xl[128];        // slot 1's statistics for slot 0 (split)
+  float qm[4][32], ql[4][32];    // per quarter (quad)
+  long long scan[CWARPS];
+  long long total, range0, range1, per;
+  int b0, t0, off0, kvh0;
+  uint32_t tmem;
+  int abort, last[2];
+};
+
+template <int HDP>
+constexpr int chunk_smem() {
+  return CCfg<HDP>::kMiscOff + (int)sizeof(CMisc) + 1024;
+}
+static_assert(chunk_smem<128>() <= 227 * 1024 && chunk_smem<64>() <= 227 * 1024, "shared memory");
+// a CTA allocates all of tensor memory: a second one must not fit on the SM
+static_assert(2 * chunk_smem<64>() > 227 * 1024, "one CTA per SM");
+// the lengths being planned over lie in the Q and K/V area before its first use
+static_assert(DLS_MAX_CHUNK_SEQS * 16 <= CCfg<64>::kXOff, "plan scratch");
+
+__device__ __forceinline__ bool cwait(uint32_t bar, uint32_t parity, int* abort_flag, bool heed_abort = true) {
+#pragma unroll 1
+  for (int i = 0; i < 32; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_ns();
+#pragma unroll 1
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 15) == 0) {
+      if (heed_abort && *(volatile int*)abort_flag) return false;
+      if (global_ns() - t0 > kWaitNsC) {
+        *(volatile int*)abort_flag = 1;
+        return false;
+      }
+    }
+  }
+}
+
+// The four warps of a softmax group meet (a bounded bar.sync: false after an
+// abort, so no warp waits for one that gave up).
+__device__ __forceinline__ bool wg_sync(uint32_t bar, uint32_t& phase, int lane, int* abort_flag) {
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
+  return __all_sync(0xffffffffu, cwait(bar, phase++ & 1, abort_flag));
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 
 template <typename T>
-__global__ void __launch_bounds__(128) chunk_simple_kernel(const ChunkArgs a) {
-  const int lane = threadIdx.x & 31;
-  const int t = blockIdx.x, h = blockIdx.y * 4 + (threadIdx.x >> 5);
-  if (h >= a.n_heads) return;
-  const long long room = (long long)a.max_pages << a.page_shift;
-  if (a.status && t == 0 && h == 0) {  // one warp looks the lengths over
-    bool bad = a.cu_q[0] < 0 || a.cu_q[a.n_seqs] > a.n_tokens;
-    for (int i = lane; i < a.n_seqs; i += 32)
-      bad |= a.cu_q[i + 1] < a.cu_q[i] || a.kv_len[i] < 0 || a.kv_len[i] > room;
-    if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(a.status, kBadPos);
+struct Kind;
+template <>
+struct Kind<__half> {
+  static constexpr uint32_t kIdesc = 0;
+  static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
+    uint32_t d;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
   }
-  int b = 0;
-  while (b < a.n_seqs && a.cu_q[b + 1] <= t) ++b;
-  if (b >= a.n_seqs) return;
-  const int start = a.cu_q[b], end = a.cu_q[b + 1];
-  int kl = a.kv_len[b];
-  if (t < start) return;
-  if (start < 0 || end > a.n_tokens || kl < 0 || kl > room) return;
-  const long long pos = (long long)kl - end + t;
-  const int hi = a.causal ? (int)(pos + 1 < 0 ? 0 : pos + 1) : kl;
-  const int lo = a.window && pos - a.window + 1 > 0 ? (int)(pos - a.window + 1) : 0;
-  const int hd = a.head_dim, kvh = h / (a.n_heads / a.n_kv);
-  const T* q = static_cast<const T*>(a.q) + (size_t)t * a.q_stride + (size_t)h * hd;
-  float qv[4], ov[4];
+};
+template <>
+struct Kind<__nv_bfloat16> {
+  static constexpr uint32_t kIdesc = (1u << 7) | (1u << 10);  // A and B bf16
+  static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
+    uint32_t d;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+  }
+};
+
+// ---- division of the work -----------------------------------------------------------------
+
+struct Seq {
+  int start, ql, kl;
+  bool bad;
+};
+
+// Sequence b's rows and lengths; ql = 0 where they do not fit.
+__device__ __forceinline__ Seq seq_get(const ChunkArgs& a, int b) {
+  Seq s;
+  s.start = a.cu_q[b];
+  const int end = a.cu_q[b + 1];
+  s.kl = a.kv_len[b];
+  s.bad = s.start < 0 || end < s.start || end > a.n_tokens || s.kl < 0 || s.kl > ((long long)a.max_pages << a.page_shift);
+  s.ql = s.bad ? 0 : end - s.start;
+  return s;
+}
+
+struct Tile {
+  int mode, n, pos0, lo, j0, keys, steps;  // keys: key tiles to do; steps: its weight in the division (at least 1)
+};
+
+__device__ __forceinline__ Tile tile_of(const ChunkArgs& a, int ql, int kl, int t) {
+  Tile x;
+  const int i0 = t * 2 * a.tpq;
+  x.n = min(2 * a.tpq, ql - i0);
+  x.mode = x.n > a.tpq ? PAIR : x.n > a.tpq_quad ? SPLIT : QUAD;
+  x.pos0 = kl - ql + i0;
+  const int hi = a.causal ? min(max(x.pos0 + x.n, 0), kl) : kl;
+  x.lo = a.window && x.pos0 >= a.window ? min(x.pos0 - a.window + 1, hi) : 0;
+  x.j0 = x.lo / BK;
+  x.keys = hi > x.lo ? (hi + BK - 1) / BK - x.j0 : 0;
+  x.steps = max(x.keys, 1);
+  return x;
+}
+
+__device__ __forceinline__ long long block_scan(long long v, long long* sums, long long* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long x = v;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    qv[i] = lane + 32 * i < hd ? to_f(q[lane + 32 * i]) : 0.f;
-    ov[i] = 0.f;
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
   }
-  float m = -INFINITY, l = 0.f;
-  for (int key = lo; key < hi; ++key) {
-    const int page = a.page_table[(size_t)b * a.max_pages + (key >> a.page_shift)];
-    if (page < 0 || page >= a.n_pages) {
-      if (a.status && lane == 0) atomicOr(a.status, kBadPage);
-      continue;
+  if (lane == 31) sums[warp] = x;
+  __syncthreads();
+  long long pre = 0, tot = 0;
+#pragma unroll
+  for (int w = 0; w < CWARPS; ++w) {
+    if (w < warp) pre += sums[w];
+    tot += sums[w];
+  }
+  __syncthreads();
+  *total = tot;
+  return pre + x - v;
+}
+
+// The CTA's range of key tiles and where it begins (all threads).
+__device__ __noinline__ void plan(const ChunkArgs& a, int4* info, CMisc& sh) {
+  const int tid = threadIdx.x, tp = 2 * a.tpq;
+  const int per_s = (a.n_seqs + CTHREADS - 1) / CTHREADS;
+  const int s0 = min(tid * per_s, a.n_seqs), s1 = min(s0 + per_s, a.n_seqs);
+  long long mine = 0, total;
+  bool bad = false;
+  for (int b = s0; b < s1; ++b) {
+    const Seq s = seq_get(a, b);
+    bad |= s.bad;
+    info[b] = make_int4((int)mine, s.ql, s.kl, 0);
+    mine += (s.ql + tp - 1) / tp;
+  }
+  if (bad && blockIdx.x == 0 && a.status) atomicOr(a.status, kBadPos);
+  const long long pre_t = block_scan(mine, sh.scan, &total);
+  for (int b = s0; b < s1; ++b) info[b].x += (int)pre_t;  // the first tile of the sequence
+  __syncthreads();
+  const int n_tiles = (int)total;
+  const int per_t = (n_tiles + CTHREADS - 1) / CTHREADS;
+  const int t0 = min(tid * per_t, n_tiles), t1 = min(t0 + per_t, n_tiles);
+  int b_first = 0;
+  if (t0 < t1) {  // the last sequence whose first tile is not behind t0
+    int lo = 0, hi = a.n_seqs;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (info[mid].x <= t0) lo = mid;
+      else hi = mid;
     }
-    const size_t row =
-        ((((size_t)page * a.n_kv + kvh) << a.page_shift) + (key & ((1 << a.page_shift) - 1))) * (size_t)hd;
-    const T *k = static_cast<const T*>(a.k) + row, *v = static_cast<const T*>(a.v) + row;
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (lane + 32 * i < hd) s = fmaf(qv[i], to_f(k[lane + 32 * i]), s);
-    s = warp_sum(s) * a.scale;
-    const float mn = fmaxf(m, s);
-    const float f = m == -INFINITY ? 0.f : expf(m - mn), p = mn == -INFINITY ? 0.f : expf(s - mn);
-    l = l * f + p;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (lane + 32 * i < hd) ov[i] = ov[i] * f + p * to_f(v[lane + 32 * i]);
-    m = mn;
+    b_first = lo;
   }
-  const float inv = l > 0.f ? 1.0f / l : 0.f;
-  T* o = static_cast<T*>(a.o) + (size_t)t * a.o_stride + (size_t)h * hd;
+  auto walk = [&](long long stop, int* bo, int* to) {  // steps of tiles t0..t1, or the tile that holds step `stop`
+    long long sum = 0;
+    int b = b_first;
+    for (int t = t0; t < t1; ++t) {
+      while (b + 1 < a.n_seqs && info[b + 1].x <= t) ++b;
+      const int4 f = info[b];
+      const int st = tile_of(a, f.y, f.z, t - f.x).steps;
+      if (stop >= 0 && sum + st > stop) {
+        *bo = b;
+        *to = t - f.x;
+        return stop - sum;
+      }
+      sum += st;
+    }
+    return sum;
+  };
+  mine = walk(-1, nullptr, nullptr);
+  const long long pre = block_scan(mine, sh.scan, &total);
+  const long long all = total * a.n_kv;
+  long long per = (all + gridDim.x - 1) / gridDim.x;
+  if (per < kMinSteps) per = kMinSteps;
+  const long long r0 = min(per * blockIdx.x, all), r1 = min(r0 + per, all);
+  if (tid == 0) {
+    sh.total = total;
+    sh.range0 = r0;
+    sh.range1 = r1;
+    sh.per = per;
+  }
+  if (r0 < r1) {
+    const long long at = r0 % total;
+    if (at >= pre && at < pre + mine) {
+      int b, t;
+      sh.off0 = (int)walk(at - pre, &b, &t);
+      sh.b0 = b;
+      sh.t0 = t;
+      sh.kvh0 = (int)(r0 / total);
+    }
+  }
+  __syncthreads();
+}
+
+// Key tiles of a slot inside a piece: first, first + stride, ... (count of them).
+struct Steps {
+  int first, count, stride;
+};
+__device__ __forceinline__ Steps slot_steps(const ChunkArgs& a, const Piece& p, int slot) {
+  Steps s;
+  if (p.mode != PAIR) {
+    s.first = p.ja + slot;
+    s.stride = 2;
+    s.count = (p.jb - p.ja - slot + 1) >> 1;
+    return s;
+  }
+  const int n = min(p.n - slot * a.tpq, a.tpq), pos0 = p.pos0 + slot * a.tpq;
+  const int hi = a.causal ? min(max(pos0 + n, 0), p.kl) : p.kl;
+  const int lo = a.window && pos0 >= a.window ? min(pos0 - a.window + 1, hi) : 0;
+  s.first = max(p.ja, lo / BK);
+  s.stride = 1;
+  s.count = hi > lo ? max(min(p.jb, (hi + BK - 1) / BK) - s.first, 0) : 0;
+  return s;
+}
+
+// Order of a piece's n key tiles in the ring: pair K0 V0 K1 V1 ..., else K0 K1 V0 K2 V1 K3 V2 ...
+__device__ __forceinline__ int ring_v(int mode, int i, int n) { return mode == PAIR ? 2 * i + 1 : n == 1 ? 1 : 2 + i + min(i, n - 2); }
+__device__ __forceinline__ int ring_k(int mode, int i) { return mode == PAIR ? 2 * i : i < 2 ? i : 2 * i - 1; }
+
+// ---- the kernel ----------------------------------------------------------------------------
+
+struct Row {
+  int lo, hi;       // keys of the row
+  bool ok;          // a row of the batch (others are padding of the operand)
+};
+
+// One key tile's softmax for the thread's row: COLS score columns at
+// tS + col0, weights to the packed operand at tS.  `keep` counts the columns'
+// first key.
+template <typename T, int COLS>
+__device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, int quarter, int key0, const Row& row, float c, bool first,
+                                             int hd, float& R, float& l) {
+  constexpr int NB = COLS / 32;
+  uint32_t v[NB][32];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (lane + 32 * i < hd) from_f(ov[i] * inv, &o[lane + 32 * i]);
-  if (a.lse && lane == 0) a.lse[(size_t)t * a.n_heads + h] = l > 0.f ? m + logf(l) : -INFINITY;
+  for (int k = 0; k < NB; ++k) tmem_ld32(tS + (COLS == 32 ? quarter * 32 : 0) + 32 * k, v[k]);
+  tmem_wait_ld();
+  if (__any_sync(0xffffffffu, row.ok && (key0 < row.lo || key0 + COLS > row.hi))) {
+    const int lo = row.lo - key0, hi = row.hi - key0;
+#pragma unroll
+    for (int k = 0; k < NB; ++k)
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (32 * k + i < lo || 32 * k + i >= hi) v[k][i] = 0xff800000u;
+  }
+  float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int k = 0; k < NB; ++k)
+#pragma unroll
+    for (int i = 0; i < 32; ++i) m4[i & 3] = fmaxf(m4[i & 3], __uint_as_float(v[k][i]));
+  const float mc = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * c;
+  const bool grow = mc > R + kGrow;  // R = -inf before the row's first key
+  if (__any_sync(0xffffffffu, grow && row.ok) && !first) {
+    const float f = grow ? ex2(R - mc) : 1.f;
+    l *= f;
+    for (int d = 0; d < hd; d += 16) {
+      uint32_t w[16];
+      tmem_ld16(tO + d, w);
+      tmem_wait_ld();
+#pragma unroll
+      for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * f);
+      tmem_st16(tO + d, w);
+    }
+  }
+  if (grow) R = mc;
+  const float nr = kShift - (R == -INFINITY ? 0.f : R);
+  const f2_t c2 = pk2(c, c), r2 = pk2(nr, nr);
+  f2_t sum[2] = {pk2(0.f, 0.f), pk2(0.f, 0.f)};
+#pragma unroll
+  for (int k = 0; k < NB; ++k) {
+    uint32_t w[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float2 x = upk2(ffma2(pk2(__uint_as_float(v[k][2 * i]), __uint_as_float(v[k][2 * i + 1])), c2, r2));
+      const float a = ex2(x.x), b = ex2(x.y);
+      sum[i & 1] = fadd2(sum[i & 1], pk2(a, b));
+      w[i] = Kind<T>::pack(a, b);
+    }
+    if (COLS == 128) {
+      tmem_st16(tS + 16 * k, w);
+    } else {
+      uint32_t z[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) z[i] = 0;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if (q == quarter) tmem_st16(tS + 16 * q, w);
+        else tmem_st16(tS + 16 * q, z);
+      }
+    }
+  }
+  const float2 s2 = upk2(fadd2(sum[0], sum[1]));
+  l += s2.x + s2.y;
+  tmem_wait_st();
+}
+
+__device__ __forceinline__ float weight(float R, float M) { return R == -INFINITY ? 0.f : ex2(R - M); }
+
+template <int HDP>
+__device__ __forceinline__ float* partial_at(const ChunkArgs& a, int cta, int which, int slot) {
+  return a.partials + (size_t)((cta * 2 + which) * 2 + slot) * (128 * (HDP + 2));  // R [128], l [128], O [128][HDP]
+}
+
+__device__ __forceinline__ float lse_of(float R, float l) {
+  return l > 0.f ? fmaf(R - kShift, 0.6931471805599453f, logf(l)) : -INFINITY;
+}
+
+// Join the partials of a tile's slot (rows 0..nrows-1; 128 threads).
+template <typename T, int HDP>
+__device__ __noinline__ void join(const ChunkArgs& a, int c0, int np, int kvh, int row0, int slot, int nrows, int tw) {
+  const int c4 = a.head_dim / 4;
+  for (int x = tw; x < nrows * c4; x += 128) {
+    const int r = x / c4, d = (x - r * c4) * 4;
+    float M = -INFINITY, L = 0.f;
+    for (int i = 0; i < np; ++i) M = fmaxf(M, __ldcg(partial_at<HDP>(a, c0 + i, i == 0, slot) + r));
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = 0; i < np; ++i) {
+      const float* q = partial_at<HDP>(a, c0 + i, i == 0, slot);
+      const float w = weight(__ldcg(q + r), M);
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(q + 256 + r * HDP + d));
+      L = fmaf(w, __ldcg(q + 128 + r), L);
+      acc.x = fmaf(w, v.x, acc.x), acc.y = fmaf(w, v.y, acc.y), acc.z = fmaf(w, v.z, acc.z), acc.w = fmaf(w, v.w, acc.w);
+    }
+    const float inv = L > 0.f ? 1.f / L : 0.f;
+    const int tok = r / a.group, head = kvh * a.group + r - tok * a.group;
+    const size_t t = (size_t)row0 + tok;
+    *reinterpret_cast<uint2*>(static_cast<T*>(a.o) + t * a.o_stride + (size_t)head * a.head_dim + d) =
+        make_uint2(Kind<T>::pack(acc.x * inv, acc.y * inv), Kind<T>::pack(acc.z * inv, acc.w * inv));
+    if (a.lse && d == 0) a.lse[t * (a.n_kv * a.group) + head] = lse_of(M, L);
+  }
+}
+
+template <typename T, int HDP>
+__global__ void __launch_bounds__(CTHREADS, 1) chunk_kernel(const __grid_constant__ CUtensorMap tm_q,
+                                                            const __grid_constant__ CUtensorMap tm_q4,
+                                                            const __grid_constant__ CUtensorMap tm_k,
+                                                            const __grid_constant__ CUtensorMap tm_v,
+                                                            const __grid_constant__ ChunkArgs a) {
+  using C = CCfg<HDP>;
+  constexpr int NST = C::NST;
+  extern __shared__ uint8_t csm[];
+  const uint32_t raw = smem_u32(csm);
+  const uint32_t pad = (1024u - (raw & 1023u)) & 1023u;
+  const uint32_t qbase = raw + pad, kvbase = qbase + C::kKVOff;
+  CMisc& sh = *reinterpret_cast<CMisc*>(csm + pad + C::kMiscOff);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    for (int i = 0; i < NST; ++i) {
+      mbar_init(smem_u32(&sh.full[i]), 1);
+      mbar_init(smem_u32(&sh.empty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&sh.s_full[i]), 1);
+      mbar_init(smem_u32(&sh.p_full[i]), 4);
+      mbar_init(smem_u32(&sh.o_full[i]), 1);
+      mbar_init(smem_u32(&sh.o_free[i]), 4);
+    }
+    mbar_init(smem_u32(&sh.q_full), 1);
+    mbar_init(smem_u32(&sh.q_empty), 1);
+    mbar_init(smem_u32(&sh.x_full), 4);
+    mbar_init(smem_u32(&sh.wg[0]), 4);
+    mbar_init(smem_u32(&sh.wg[1]), 4);
+    for (int i = 0; i < QDEPTH; ++i) {
+      mbar_init(smem_u32(&sh.pq_full[i]), 1);
+      mbar_init(smem_u32(&sh.pq_empty[i]), 10);
+    }
+    sh.abort = 0;
+    mbar_fence_init();
+    prefetch_tmap(&tm_q);
+    prefetch_tmap(&tm_q4);
+    prefetch_tmap(&tm_k);
+    prefetch_tmap(&tm_v);
+  }
+  plan(a, reinterpret_cast<int4*>(csm + pad), sh);
+  if (sh.range0 >= sh.range1) return;  // uniform: nothing is allocated yet
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&sh.tmem), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  // the plan's scratch (generic proxy) is overwritten by TMA from here on
+  fence_async_smem();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  int* const ab = &sh.abort;
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp == 0) {
+      // ---------------- copies: Q tiles, and K/V tiles piece by piece of a page
+      const int pr = min(1 << a.page_shift, BK);  // keys of a copy
+      const int npc = BK / pr;
+      const uint32_t qbytes = 128u * a.group * a.tpq * C::KA, q4bytes = 4u * 128u * a.group * a.tpq_quad * C::KA;
+      int u = 0, nq = 0;
+      bool ok = true, q_out = false;
+      for (int k = 0; ok; ++k) {
+        if (!(ok = __all_sync(0xffffffffu, cwait(smem_u32(&sh.pq_full[k % QDEPTH]), (k / QDEPTH) & 1, ab)))) break;
+        const Piece p = sh.pq[k % QDEPTH];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sh.pq_empty[k % QDEPTH]));
+        if (p.mode == END) break;
+        const int n = p.jb - p.ja;
+        if (n == 0) continue;
+        if (nq > 0 && !(ok = __all_sync(0xffffffffu, cwait(smem_u32(&sh.q_empty), (nq - 1) & 1, ab)))) break;
+        if (lane == 0) {
+          const uint32_t bar = smem_u32(&sh.q_full);
+          mbar_expect_tx(bar, p.mode == PAIR ? 2 * qbytes : p.mode == SPLIT ? qbytes : q4bytes);
+          const int h0 = p.kvh * a.group;
+          for (int at = 0; at < C::KA; ++at) {
+            const uint32_t d = qbase + at * (128 * 128);
+            if (p.mode == QUAD) {
+              for (int w = 0; w < 4; ++w) tma_load_3d(d + w * (32 * 128), &tm_q4, at * 64, h0, p.row0, bar);
+            } else {
+              tma_load_3d(d, &tm_q, at * 64, h0, p.row0, bar);
+              if (p.mode == PAIR) tma_load_3d(d + C::kQ, &tm_q, at * 64, h0, p.row0 + a.tpq, bar);
+            }
+          }
+        }
+        ++nq;
+        q_out = true;
+        const int32_t* table = a.page_table + (size_t)p.b * a.max_pages;
+        auto tile = [&](int j, bool is_v) {
+          const int s = u % NST;
+          if (u >= NST && !(ok = __all_sync(0xffffffffu, cwait(smem_u32(&sh.empty[s]), ((u / NST) - 1) & 1, ab)))) return;
+          const uint32_t bar = smem_u32(&sh.full[s]), dst = kvbase + s * C::kKV;
+          if (lane == 0) mbar_expect_tx(bar, C::kKV);
+          __syncwarp();
+          if (lane < npc * C::KA) {
+            const int x = lane / C::KA, at = lane % C::KA;
+            const int key = j * BK + x * pr;
+            int y = a.pool_rows;  // past the end of the pool: the copy fills zeros
+            if (key < p.kl && key + pr > p.lo) {
+              const int page = table[key >> a.page_shift];
+              if (page >= 0 && page < a.n_pages)
+                y = ((page * a.n_kv + p.kvh) << a.page_shift) + (key & ((1 << a.page_shift) - 1));
+              else if (a.status)
+                atomicOr(a.status, kBadPage);
+            }
+            tma_load_2d(dst + at * (BK * 128) + x * pr * 128, is_v ? &tm_v : &tm_k, at * 64, y, bar);
+          }
+          ++u;
+        };
+        if (p.mode == PAIR) {
+          for (int j = p.ja; ok && j < p.jb; ++j) {
+            tile(j, false);
+            if (ok) tile(j, true);
+          }
+        } else {
+          tile(p.ja, false);
+          if (ok && n > 1) tile(p.ja + 1, false);
+          for (int i = 0; ok && i < n; ++i) {
+            tile(p.ja + i, true);
+            if (ok && i + 2 < n) tile(p.ja + i + 2, false);
+          }
+        }
+      }
+      // no copy may be in flight when the CTA ends
+      __syncwarp();
+      for (int x = u > NST ? u - NST : 0; x < u; ++x) cwait(smem_u32(&sh.full[x % NST]), (x / NST) & 1, ab, false);
+      if (q_out) cwait(smem_u32(&sh.q_full), (nq - 1) & 1, ab, false);
+      __syncwarp();
+    } else if (warp == 1) {
+      // ---------------- MMA issue
+      if (lane == 0) {
+        const uint32_t id_s = umma_idesc_f16(128, BK) | Kind<T>::kIdesc;
+        const uint32_t id_o = umma_idesc_f16_bmn(128, a.head_dim) | Kind<T>::kIdesc;
+        const int ksteps = a.head_dim / 16;
+        int u0 = 0, nq = 0;        // ring position of the piece, Q tiles seen
+        int np_[2] = {0, 0};       // P tiles consumed, per slot
+        bool ok = true;
+        auto wait_full = [&](int u) { return cwait(smem_u32(&sh.full[u % NST]), (u / NST) & 1, ab); };
+        auto release = [&](int u) { umma_commit(smem_u32(&sh.empty[u % NST])); };
+        for (int k = 0; ok; ++k) {
+          if (!(ok = cwait(smem_u32(&sh.pq_full[k % QDEPTH]), (k / QDEPTH) & 1, ab))) break;
+          const Piece p = sh.pq[k % QDEPTH];
+          mbar_arrive(smem_u32(&sh.pq_empty[k % QDEPTH]));
+          if (p.mode == END) break;
+          const int n = p.jb - p.ja;
+          bool freed[2] = {k == 0, k == 0};  // the previous piece's O has been read
+          auto qk = [&](int slot, int u) {
+            tc_fence_after();
+            const uint32_t q = qbase + (p.mode == PAIR ? slot * C::kQ : 0), kt = kvbase + (u % NST) * C::kKV;
+            for (int ks = 0; ks < ksteps; ++ks) {
+              const uint32_t off = (ks >> 2) * (128 * 128) + (ks & 3) * 32;
+              umma_f16(tmem + slot * 128, umma_desc_k128(q + off), umma_desc_k128(kt + off), id_s, ks != 0);
+            }
+            umma_commit(smem_u32(&sh.s_full[slot]));
+          };
+          auto pv = [&](int slot, int u, bool first) {
+            if (!cwait(smem_u32(&sh.p_full[slot]), np_[slot] & 1, ab)) return false;
+            ++np_[slot];
+            if (!freed[slot]) {
+              if (!cwait(smem_u32(&sh.o_free[slot]), (k - 1) & 1, ab)) return false;
+              freed[slot] = true;
+            }
+            tc_fence_after();
+            const uint32_t vt = kvbase + (u % NST) * C::kKV;
+#pragma unroll
+            for (int ks = 0; ks < BK / 16; ++ks)
+              umma_f16_ta(tmem + 256 + slot * HDP, tmem + slot * 128 + ks * 8, umma_desc_mn128(vt + ks * 16 * 128, BK * 128, 1024), id_o,
+                          !(first && ks == 0));
+            return true;
+          };
+          if (n > 0) {
+            if (!(ok = cwait(smem_u32(&sh.q_full), nq & 1, ab))) break;
+            ++nq;
+            const int u = u0;
+            u0 += 2 * n;
+            if (p.mode == PAIR) {
+              const Steps s0 = slot_steps(a, p, 0), s1 = slot_steps(a, p, 1);
+              auto on = [&](const Steps& s, int j) { return j >= s.first && j < s.first + s.count; };
+              if (!(ok = wait_full(u))) break;
+              if (on(s0, p.ja)) qk(0, u);
+              if (on(s1, p.ja)) qk(1, u);
+              release(u);
+              if (n == 1) umma_commit(smem_u32(&sh.q_empty));
+              for (int j = p.ja; ok && j < p.jb; ++j) {
+                const int i = j - p.ja, uv = u + 2 * i + 1, uk = uv + 1;
+                const bool more = j + 1 < p.jb;
+                if (!(ok = wait_full(uv))) break;
+                if (on(s0, j)) {
+                  if (!(ok = pv(0, uv, j == s0.first))) break;
+                  if (j + 1 == s0.first + s0.count) umma_commit(smem_u32(&sh.o_full[0]));
+                }
+                if (more) {
+                  if (!(ok = wait_full(uk))) break;
+                  if (on(s0, j + 1)) qk(0, uk);
+                }
+                if (on(s1, j)) {
+                  if (!(ok = pv(1, uv, j == s1.first))) break;
+                  if (j + 1 == s1.first + s1.count) umma_commit(smem_u32(&sh.o_full[1]));
+                }
+                release(uv);
+                if (more) {
+                  if (on(s1, j + 1)) qk(1, uk);
+                  release(uk);
+                  if (j + 2 == p.jb) umma_commit(smem_u32(&sh.q_empty));
+                }
+              }
+            } else {
+              for (int i = 0; i < min(n, 2); ++i) {
+                if (!(ok = wait_full(u + i))) break;
+                qk(i, u + i);
+                release(u + i);
+                if (i == n - 1) umma_commit(smem_u32(&sh.q_empty));
+              }
+              for (int i = 0; ok && i < n; ++i) {
+                const int slot = i & 1, uv = u + ring_v(p.mode, i, n);
+                if (!(ok = wait_full(uv))) break;
+                if (!(ok = pv(slot, uv, i < 2))) break;
+                release(uv);
+                if (i + 2 >= n) umma_commit(smem_u32(&sh.o_full[slot]));
+                if (i + 2 < n) {
+                  const int uk = u + ring_k(p.mode, i + 2);
+                  if (!(ok = wait_full(uk))) break;
+                  qk(slot, uk);
+                  release(uk);
+                  if (i + 2 == n - 1) umma_commit(smem_u32(&sh.q_empty));
+                }
+              }
+            }
+          }
+          for (int s = 0; ok && s < 2; ++s)  // every phase of o_free is seen once
+            if (!freed[s]) ok = cwait(smem_u32(&sh.o_free[s]), (k - 1) & 1, ab);
+        }
+      }
+      __syncwarp();
+    } else if (warp == 2) {
+      // ---------------- the CTA's pieces
+      long long pos = sh.range0;
+      const long long end = sh.range1, per = sh.per;
+      int b = sh.b0, t = sh.t0, off = sh.off0, kvh = sh.kvh0;
+      Seq s = seq_get(a, b);
+      bool ok = true;
+      int k = 0;
+      for (;; ++k) {
+        if (k >= QDEPTH && !(ok = __all_sync(0xffffffffu, cwait(smem_u32(&sh.pq_empty[k % QDEPTH]), ((k / QDEPTH) - 1) & 1, ab)))) break;
+        Piece p;
+        if (pos >= end) {
+          p.mode = END;
+        } else {
+          const Tile x = tile_of(a, s.ql, s.kl, t);
+          const int take = (int)min((long long)(x.steps - off), end - pos);
+          const long long p0 = pos - off;
+          p.mode = x.mode;
+          p.b = b;
+          p.kvh = kvh;
+          p.row0 = s.start + t * 2 * a.tpq;
+          p.n = x.n;
+          p.pos0 = x.pos0;
+          p.kl = s.kl;
+          p.lo = x.lo;
+          p.ja = x.j0 + off;
+          p.jb = x.keys ? p.ja + take : p.ja;
+          p.c0 = (int)(p0 / per);
+          p.np = (int)((p0 + x.steps - 1) / per) - p.c0 + 1;
+          p.idx = (int)blockIdx.x - p.c0;
+          pos += take;
+          if (off + take == x.steps) {
+            off = 0;
+            if (++t * 2 * a.tpq >= s.ql && pos < end) {
+              t = 0;
+              do {
+                if (++b == a.n_seqs) b = 0, ++kvh;
+                s = seq_get(a, b);
+              } while (s.ql == 0);
+            }
+          }
+        }
+        if (lane == 0) {
+          sh.pq[k % QDEPTH] = p;
+          mbar_arrive(smem_u32(&sh.pq_full[k % QDEPTH]));
+        }
+        __syncwarp();
+        if (p.mode == END) break;
+      }
+    }
+  } else {
+    // ---------------- softmax and epilogue: slot = warpgroup, thread = row (TMEM lane)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    const int slot = (warp >> 2) - 1, quarter = warp & 3, tw = tid & 127;
+    const uint32_t tl = (uint32_t)(quarter * 32) << 16;
+    const uint32_t tS = tmem + tl + slot * 128, tO = tmem + tl + 256 + slot * HDP;
+    const int hd = a.head_dim, G = a.group;
+    const uint32_t wg = smem_u32(&sh.wg[slot]);
+    uint32_t wph = 0;
+    int u0 = 0, ns = 0, nx = 0;
+    int no[2] = {0, 0};  // phases of o_full passed
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+      if (!(ok = __all_sync(0xffffffffu, cwait(smem_u32(&sh.pq_full[k % QDEPTH]), (k / QDEPTH) & 1, ab)))) break;
+      const Piece p = sh.pq[k % QDEPTH];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sh.pq_empty[k % QDEPTH]));
+      if (p.mode == END) break;
+      const int n = p.jb - p.ja, u = u0;
+      u0 += 2 * n;
+      const Steps st = slot_steps(a, p, slot);
+      const int r = p.mode == QUAD ? lane : tw;
+      const int tok0 = p.mode == PAIR ? slot * a.tpq : 0;
+      const int ntok = p.mode == PAIR ? min(p.n - tok0, a.tpq) : p.n;
+      const int tok = r / G, hg = r - tok * G;
+      Row row;
+      row.ok = tok < ntok;
+      row.lo = 0;
+      row.hi = 0x7fffffff;  // padding rows: never a reason to mask
+      if (row.ok) {
+        const int pos = p.pos0 + tok0 + tok;
+        row.hi = a.causal ? min(max(pos + 1, 0), p.kl) : p.kl;
+        row.lo = a.window && pos >= a.window ? pos - a.window + 1 : 0;
+      }
+      float R = -INFINITY, l = 0.f;
+      for (int i = 0; i < st.count; ++i) {
+        const int j = st.first + i * st.stride;
+        const bool ragged = (j + 1) * BK > p.kl || j * BK < p.lo;
+        if (ragged) {
+          // rows of V that no query may see can hold anything: 0 * NaN would
+          // reach every row through the product
+          const int uv = u + ring_v(p.mode, j - p.ja, n);
+          if (!(ok = __all_sync(0xffffffffu, cwait(smem_u32(&sh.full[uv % NST]), (uv / NST) & 1, ab)))) break;
+          const int key = j * BK + tw;
+          if (key >= p.kl || key < p.lo) {
+            const uint32_t v = kvbase + (uv % NST) * C::kKV + tw * 128;
+            for (int at = 0; at < C::KA; ++at)
+              for (int x = 0; x < 8; ++x) sts128(v + at * (BK * 128) + x * 16, make_uint4(0, 0, 0, 0));
+          }
+          fence_async_smem();
+        }
+        if (!(ok = __all_sync(0xffffffffu, cwait(smem_u32(&sh.s_full[slot]), ns & 1, ab)))) break;
+        ++ns;
+        tc_fence_after();
+        if (p.mode == QUAD) softmax_tile<T, 32>(tS, tO, quarter, j * BK + quarter * 32, row, a.c, i == 0, hd, R, l);
+        else softmax_tile<T, 128>(tS, tO, quarter, j * BK, row, a.c, i == 0, hd, R, l);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sh.p_full[slot]));
+      }
+      if (!ok) break;
+      if (st.count) {
+        if (!(ok = __all_sync(0xffffffffu, cwait(smem_u32(&sh.o_full[slot]), no[slot] & 1, ab)))) break;
+        ++no[slot];
+      }
+      const int nrows = ntok * G;
+      float* const part = p.np > 1 ? partial_at<HDP>(a, blockIdx.x, p.idx == 0, p.mode == PAIR ? slot : 0) : nullptr;
+      const size_t t = (size_t)p.row0 + tok0 + tok;
+      const int head = p.kvh * G + hg;
+      bool use0 = st.count > 0, use1 = false;
+      float w0 = 1.f, w1 = 0.f;
+      const int count1 = slot == 1 ? 0 : slot_steps(a, p, 1).count;
+      if (p.mode != PAIR) {
+        // slot 0 takes slot 1's share
+        if (slot == 1) {
+          // (the last statistics have been read: this piece's P V waited for o_free of the piece before)
+          if (st.count) {
+            sh.xm[tw] = R, sh.xl[tw] = l;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sh.x_full));
+          }
+          continue;
+        }
+        if (count1) {
+          if (!(ok = __all_sync(0xffffffffu, cwait(smem_u32(&sh.x_full), nx & 1, ab) && cwait(smem_u32(&sh.o_full[1]), no[1] & 1, ab)))) break;
+          ++nx;
+          use1 = true;
+          const float R1 = sh.xm[tw], l1 = sh.xl[tw], M = fmaxf(R, R1);
+          w0 = weight(R, M);
+          w1 = weight(R1, M);
+          l = w0 * l + w1 * l1;
+          R = M;
+        }
+      }
+      if (count1) ++no[1];
+      tc_fence_after();
+      const uint32_t tO1 = tO + HDP;  // slot 1's O
+      if (p.mode != QUAD) {
+        float inv = 1.f;
+        if (!part) inv = l > 0.f ? 1.f / l : 0.f;
+        w0 *= inv;
+        w1 *= inv;
+        T* out = static_cast<T*>(a.o) + t * a.o_stride + (size_t)head * hd;
+        for (int d = 0; d < hd; d += 16) {
+          uint32_t v[16], w[16];
+          if (use0) tmem_ld16(tO + d, v);
+          if (use1) tmem_ld16(tO1 + d, w);
+          tmem_wait_ld();
+          float f[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            f[i] = use0 ? __uint_as_float(v[i]) * w0 : 0.f;
+            if (use1) f[i] = fmaf(__uint_as_float(w[i]), w1, f[i]);
+          }
+          if (row.ok) {
+            if (part) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                __stcg(reinterpret_cast<float4*>(part + 256 + tw * HDP + d + 4 * i), make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]));
+            } else {
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+                *reinterpret_cast<uint4*>(out + d + 8 * i) =
+                    make_uint4(Kind<T>::pack(f[8 * i], f[8 * i + 1]), Kind<T>::pack(f[8 * i + 2], f[8 * i + 3]),
+                               Kind<T>::pack(f[8 * i + 4], f[8 * i + 5]), Kind<T>::pack(f[8 * i + 6], f[8 * i + 7]));
+            }
+          }
+        }
+      } else {
+        // join the quarters, 32 output columns at a time
+        sh.qm[quarter][lane] = R;
+        sh.ql[quarter][lane] = l;
+        if (!(ok = wg_sync(wg, wph, lane, ab))) break;
+        float M = -INFINITY, L = 0.f;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) M = fmaxf(M, sh.qm[q][lane]);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) L = fmaf(weight(sh.qm[q][lane], M), sh.ql[q][lane], L);
+        float f = weight(R, M);
+        if (!part) f *= L > 0.f ? 1.f / L : 0.f;
+        w0 *= f;
+        w1 *= f;
+        R = M;
+        l = L;
+        float4* const X = reinterpret_cast<float4*>(csm + pad + C::kXOff);  // [quarter][row][8], chunk ^ (row & 7)
+        for (int d = 0; ok && d < hd; d += 32) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t v[16], w[16];
+            if (use0) tmem_ld16(tO + d + 16 * h, v);
+            if (use1) tmem_ld16(tO1 + d + 16 * h, w);
+            tmem_wait_ld();
+            float g[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              g[i] = use0 ? __uint_as_float(v[i]) * w0 : 0.f;
+              if (use1) g[i] = fmaf(__uint_as_float(w[i]), w1, g[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              X[(quarter * 32 + lane) * 8 + ((4 * h + i) ^ (lane & 7))] = make_float4(g[4 * i], g[4 * i + 1], g[4 * i + 2], g[4 * i + 3]);
+          }
+          if (!(ok = wg_sync(wg, wph, lane, ab))) break;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int rr = (tw + 128 * i) >> 3, ch = tw & 7, dd = d + 4 * ch;
+            if (rr < nrows && dd < hd) {
+              float4 s = X[rr * 8 + (ch ^ (rr & 7))];
+#pragma unroll
+              for (int q = 1; q < 4; ++q) {
+                const float4 y = X[(q * 32 + rr) * 8 + (ch ^ (rr & 7))];
+                s.x += y.x, s.y += y.y, s.z += y.z, s.w += y.w;
+              }
+              if (part) {
+                __stcg(reinterpret_cast<float4*>(part + 256 + rr * HDP + dd), s);
+              } else {
+                const int tk = rr / G;
+                *reinterpret_cast<uint2*>(static_cast<T*>(a.o) + ((size_t)p.row0 + tk) * a.o_stride +
+                                          (size_t)(p.kvh * G + rr - tk * G) * hd + dd) =
+                    make_uint2(Kind<T>::pack(s.x, s.y), Kind<T>::pack(s.z, s.w));
+              }
+            }
+          }
+          ok = wg_sync(wg, wph, lane, ab);
+        }
+        if (!ok) break;
+      }
+      // O is read: the next piece may overwrite it
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(smem_u32(&sh.o_free[slot]));
+        if (p.mode != PAIR) mbar_arrive(smem_u32(&sh.o_free[1]));
+      }
+      if (row.ok && (p.mode != QUAD || quarter == 0)) {
+        if (part) {
+          __stcg(part + r, R);
+          __stcg(part + 128 + r, l);
+        } else if (a.lse) {
+          a.lse[t * (a.n_kv * G) + head] = lse_of(R, l);
+        }
+      }
+      if (part) {
+        // the last piece of the tile to arrive joins them all
+        __threadfence();
+        if (!(ok = wg_sync(wg, wph, lane, ab))) break;
+        if (tw == 0) {
+          int* cnt = a.counters + p.c0 * 2 + slot;
+          const bool last = atomicAdd(cnt, 1) == p.np - 1;
+          if (last) *cnt = 0;  // ready for the next call
+          sh.last[slot] = last;
+        }
+        if (!(ok = wg_sync(wg, wph, lane, ab))) break;
+        if (sh.last[slot]) {
+          __threadfence();
+          join<T, HDP>(a, p.c0, p.np, p.kvh, p.row0 + tok0, slot, nrows, tw);
+        }
+      }
+    }
+    if (!ok && a.status && lane == 0) atomicOr(a.status, kTimeout);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+using ChunkFn = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const CUtensorMap, const ChunkArgs);
+
+// SMs of the current device, with the kernels' attributes set on it; 0 on an error.
+int device_ready(cudaError_t* err) {
+  static std::mutex mu;
+  static int sms[64];
+  int dev = 0;
+  if ((*err = cudaGetDevice(&dev)) != cudaSuccess) return 0;
+  if (dev < 0 || dev >= 64) {
+    *err = cudaErrorInvalidDevice;
+    return 0;
+  }
+  std::lock_guard<std::mutex> g(mu);
+  if (sms[dev]) return sms[dev];
+  int n = 0;
+  if ((*err = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return 0;
+  const ChunkFn f[2] = {chunk_kernel<__half, 128>, chunk_kernel<__nv_bfloat16, 128>};
+  const ChunkFn h[2] = {chunk_kernel<__half, 64>, chunk_kernel<__nv_bfloat16, 64>};
+  for (int i = 0; i < 2; ++i) {
+    if ((*err = cudaFuncSetAttribute(f[i], cudaFuncAttributeMaxDynamicSharedMemorySize, chunk_smem<128>())) != cudaSuccess) return 0;
+    if ((*err = cudaFuncSetAttribute(h[i], cudaFuncAttributeMaxDynamicSharedMemorySize, chunk_smem<64>())) != cudaSuccess) return 0;
+  }
+  return sms[dev] = n;
 }
 
 bool rows_ok(const void* p, long long stride, long long width) {
@@ -103,7 +987,8 @@ bool rows_ok(const void* p, long long stride, long long width) {
 
 extern "C" uint64_t dls_attention_chunk_workspace_bytes(int32_t head_dim) {
   if (head_dim < 16 || head_dim > 128 || head_dim % 16) return 0;
-  return 256;
+  const uint64_t hdp = head_dim <= 64 ? 64 : 128;
+  return dls::kCounterBytes + (uint64_t)dls::MAXC * 4 * 128 * (hdp + 2) * sizeof(float);
 }
 
 extern "C" int dls_attention_chunk(const dls_attention_chunk_desc* d, void* cuda_stream) {
@@ -116,7 +1001,7 @@ extern "C" int dls_attention_chunk(const dls_attention_chunk_desc* d, void* cuda
   if (d->kv_type != DLS_F16 && d->kv_type != DLS_BF16) return report_error(DLS_ERR_ARG, "attention_chunk: kv_type=%d", d->kv_type);
   if (d->n_kv_heads < 1 || d->n_heads < 1 || d->n_heads % d->n_kv_heads || d->n_heads / d->n_kv_heads > 128 || d->n_heads > 65536)
     return report_error(DLS_ERR_ARG, "attention_chunk: n_heads=%d n_kv_heads=%d (groups of at most 128)", d->n_heads, d->n_kv_heads);
-  if (d->n_tokens < 0 || d->n_seqs < 0 || d->n_seqs > DLS_MAX_CHUNK_SEQS || d->n_pages < 1 || d->max_pages < 1 ||
+  if (d->n_tokens < 0 || d->n_tokens > 1 << 30 || d->n_seqs < 0 || d->n_seqs > DLS_MAX_CHUNK_SEQS || d->n_pages < 1 || d->max_pages < 1 ||
       (long long)d->max_pages * pt > 0x7fffffff - 1024)
     return report_error(DLS_ERR_ARG, "attention_chunk: n_tokens=%d n_seqs=%d (at most %d) n_pages=%d max_pages=%d", d->n_tokens, d->n_seqs,
                         DLS_MAX_CHUNK_SEQS, d->n_pages, d->max_pages);
@@ -138,22 +1023,39 @@ extern "C" int dls_attention_chunk(const dls_attention_chunk_desc* d, void* cuda
   if (!d->workspace || (reinterpret_cast<uintptr_t>(d->workspace) & 255) || d->workspace_bytes < dls_attention_chunk_workspace_bytes(hd))
     return report_error(DLS_ERR_ARG, "attention_chunk: workspace=%p bytes=%llu (256-byte aligned, at least %llu)", d->workspace,
                         (unsigned long long)d->workspace_bytes, (unsigned long long)dls_attention_chunk_workspace_bytes(hd));
-  ChunkArgs a{};
-  a.q = d->q, a.k = d->k_pages, a.v = d->v_pages, a.o = d->o, a.lse = d->lse;
-  a.page_table = d->page_table, a.cu_q = d->cu_q, a.kv_len = d->kv_len, a.status = d->status;
-  a.q_stride = d->q_stride, a.o_stride = d->o_stride;
-  a.n_tokens = d->n_tokens, a.n_seqs = d->n_seqs, a.n_heads = d->n_heads, a.n_kv = d->n_kv_heads, a.head_dim = hd;
-  a.page_shift = pt == 16 ? 4 : pt == 32 ? 5 : pt == 64 ? 6 : pt == 128 ? 7 : 8;
-  a.n_pages = d->n_pages, a.max_pages = d->max_pages;
-  a.causal = d->causal, a.window = d->window;
-  a.scale = d->scale > 0.f ? d->scale : 1.0f / sqrtf((float)hd);
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
   cudaError_t e = cudaSuccess;
+  const int sms = device_ready(&e);
+  if (e != cudaSuccess) return report_error(DLS_ERR_CUDA, "attention_chunk: cuda=%s", cudaGetErrorString(e));
+  ChunkArgs a{};
+  a.o = d->o, a.lse = d->lse;
+  a.page_table = d->page_table, a.cu_q = d->cu_q, a.kv_len = d->kv_len, a.status = d->status;
+  a.counters = static_cast<int*>(d->workspace);
+  a.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(d->workspace) + kCounterBytes);
+  a.o_stride = d->o_stride;
+  a.n_tokens = d->n_tokens, a.n_seqs = d->n_seqs, a.n_kv = d->n_kv_heads, a.group = d->n_heads / d->n_kv_heads, a.head_dim = hd;
+  a.page_shift = pt == 16 ? 4 : pt == 32 ? 5 : pt == 64 ? 6 : pt == 128 ? 7 : 8;
+  a.n_pages = d->n_pages, a.max_pages = d->max_pages, a.pool_rows = d->n_pages * d->n_kv_heads * pt;
+  a.causal = d->causal, a.window = d->window;
+  a.tpq = 128 / a.group, a.tpq_quad = 32 / a.group;
+  a.c = (d->scale > 0.f ? d->scale : 1.0f / sqrtf((float)hd)) * 1.4426950408889634f;
+  const CUtensorMapDataType dt = d->kv_type == DLS_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const uint32_t pr = pt < BK ? pt : BK;
+  CUtensorMap tq, tq4, tk, tv;
+  const uint64_t dims[3] = {(uint64_t)hd, (uint64_t)d->n_heads, (uint64_t)d->n_tokens};
+  const uint64_t strides[2] = {(uint64_t)hd * 2, (uint64_t)d->q_stride * 2};
+  const uint32_t box[3] = {64, (uint32_t)a.group, (uint32_t)a.tpq}, box4[3] = {64, (uint32_t)a.group, (uint32_t)(a.tpq_quad ? a.tpq_quad : 1)};
+  if (!make_tmap_3d(&tq, dt, d->q, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_tmap_3d(&tq4, dt, d->q, dims, strides, box4, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_tmap_2d(&tk, dt, d->k_pages, hd, a.pool_rows, hd * 2, 64, pr, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_tmap_2d(&tv, dt, d->v_pages, hd, a.pool_rows, hd * 2, 64, pr, CU_TENSOR_MAP_SWIZZLE_128B))
+    return report_error(DLS_ERR_CUDA, "attention_chunk: tensor map (head_dim=%d n_heads=%d n_tokens=%d)", hd, d->n_heads, d->n_tokens);
   if (a.status) e = cudaMemsetAsync(a.status, 0, sizeof(int32_t), s);
   if (e == cudaSuccess) {
-    const dim3 grid(d->n_tokens, (d->n_heads + 3) / 4);
-    if (d->kv_type == DLS_F16) chunk_simple_kernel<__half><<<grid, 128, 0, s>>>(a);
-    else chunk_simple_kernel<__nv_bfloat16><<<grid, 128, 0, s>>>(a);
+    const bool half = d->kv_type == DLS_F16;
+    const ChunkFn f = hd <= 64 ? (half ? chunk_kernel<__half, 64> : chunk_kernel<__nv_bfloat16, 64>)
+                               : (half ? chunk_kernel<__half, 128> : chunk_kernel<__nv_bfloat16, 128>);
+    f<<<sms < MAXC ? sms : MAXC, CTHREADS, hd <= 64 ? chunk_smem<64>() : chunk_smem<128>(), s>>>(tq, tq4, tk, tv, a);
     e = cudaGetLastError();
   }
   if (e != cudaSuccess) return report_error(DLS_ERR_CUDA, "attention_chunk: cuda=%s", cudaGetErrorString(e));

@@ -321,6 +321,9 @@ cudaError_t launch_pattn(const float* q, float* o, const KvView& kv, const int32
 // 2-D tiled tensor map (row-major, dim0 contiguous; strides in bytes)
 bool make_tmap_2d(CUtensorMap* m, CUtensorMapDataType dt, const void* base, uint64_t dim0, uint64_t dim1,
                   uint64_t stride1, uint32_t box0, uint32_t box1, CUtensorMapSwizzle sw);
+// the same with three dimensions (strides of dimensions 1 and 2)
+bool make_tmap_3d(CUtensorMap* m, CUtensorMapDataType dt, const void* base, const uint64_t (&dim)[3],
+                  const uint64_t (&stride)[2], const uint32_t (&box3)[3], CUtensorMapSwizzle sw);
 
 // ---- prefill attention on the tensor cores ---------------------------------------
 
