@@ -760,10 +760,14 @@ __global__ void __launch_bounds__(CTHREADS, 1) chunk_kernel(const __grid_constan
       float R = -INFINITY, l = 0.f;
       for (int i = 0; i < st.count; ++i) {
         const int j = st.first + i * st.stride;
-        const bool ragged = (j + 1) * BK > p.kl || j * BK < p.lo;
-        if (ragged) {
+        if (!(ok = __all_sync(0xffffffffu, cwait(smem_u32(&sh.s_full[slot]), ns & 1, ab)))) break;
+        ++ns;
+        tc_fence_after();
+        if ((j + 1) * BK > p.kl || j * BK < p.lo) {
           // rows of V that no query may see can hold anything: 0 * NaN would
-          // reach every row through the product
+          // reach every row through the product.  (This wait comes after
+          // s_full: the MMA warp has then consumed the stage's previous
+          // tile, so the barrier is at most one phase behind.)
           const int uv = u + ring_v(p.mode, j - p.ja, n);
           if (!(ok = __all_sync(0xffffffffu, cwait(smem_u32(&sh.full[uv % NST]), (uv / NST) & 1, ab)))) break;
           const int key = j * BK + tw;
@@ -774,9 +778,6 @@ __global__ void __launch_bounds__(CTHREADS, 1) chunk_kernel(const __grid_constan
           }
           fence_async_smem();
         }
-        if (!(ok = __all_sync(0xffffffffu, cwait(smem_u32(&sh.s_full[slot]), ns & 1, ab)))) break;
-        ++ns;
-        tc_fence_after();
         if (p.mode == QUAD) softmax_tile<T, 32>(tS, tO, quarter, j * BK + quarter * 32, row, a.c, i == 0, hd, R, l);
         else softmax_tile<T, 128>(tS, tO, quarter, j * BK, row, a.c, i == 0, hd, R, l);
         tc_fence_before();

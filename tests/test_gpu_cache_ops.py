@@ -583,3 +583,19 @@ def test_a_graph_follows_the_lengths(gpu_lib):
         torch.cuda.synchronize()
         close_attend(B, o, None, attend64(B, q, heads, hd ** -0.5, True, 0), heads)
         assert bool((o[B.starts[-1]:] == 7).all())
+
+
+@pytest.mark.parametrize("heads,kvh,hd,page,typ", [(32, 8, 128, 32, "f16"), (16, 2, 128, 64, "bf16"), (8, 8, 64, 16, "f16")])
+def test_attention_chunk_many_tiles_of_each_range(gpu_lib, heads, kvh, hd, page, typ):
+    """Several tiles of several key tiles in each CTA's range, each with a partly filled last page, repeated: copies run
+    ahead of the products from tile to tile."""
+    B = Batch([(5, 4101), (1, 3661), (3, 4009), (4, 1803), (1, 2951), (4, 3718), (5, 2122), (1, 2767), (60, 3001)], kvh, hd, page,
+              TYPES[typ], 16)
+    B.fill()
+    q = (2 * torch.randn(B.rows, heads, hd, generator=B.g, device="cuda")).to(B.typ)
+    o, first, lse, ws = torch.empty_like(q), torch.empty_like(q), torch.empty(B.rows, heads, device="cuda"), workspace(hd)
+    dls.attention_chunk(q, B.k, B.v, B.table, B.cu_q, B.kv_len, first, ws)
+    for _ in range(20):
+        dls.attention_chunk(q, B.k, B.v, B.table, B.cu_q, B.kv_len, o, ws, lse=lse)
+        assert torch.equal(o, first)
+    close_attend(B, o, lse, attend64(B, q, heads, hd ** -0.5, True, 0), heads)
