@@ -54,6 +54,7 @@ constexpr int kMinSteps = 2;     // key tiles of a range at least (one per slot 
 constexpr float kGrow = 8.f;     // log2 the maximum may exceed the reference by
 constexpr float kShift = 7.f;    // weights are kept as 2^(c s - R + 7): at most 2^15 in fp16, with 7 more binades below
 constexpr uint64_t kWaitNsC = 2000000000ull;
+constexpr int kPCol = 64;         // the weights' columns in a slot's S (packed: 64 of them)
 constexpr int kCounterBytes = 4096;  // int [MAXC][2], at the start of the workspace
 
 enum Mode { PAIR = 0, SPLIT = 1, QUAD = 2, END = 3 };
@@ -329,73 +330,111 @@ struct Row {
   bool ok;          // a row of the batch (others are padding of the operand)
 };
 
-// One key tile's softmax for the thread's row: COLS score columns at
-// tS + col0, weights to the packed operand at tS.  `keep` counts the columns'
-// first key.
-template <typename T, int COLS>
-__device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, int quarter, int key0, const Row& row, float c, bool first,
-                                             int hd, float& R, float& l) {
-  constexpr int NB = COLS / 32;
-  uint32_t v[NB][32];
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// Scores of keys key0 .. key0 + N - 1 outside the row's range become -inf.
+template <int N>
+__device__ __forceinline__ void mask_keys(uint32_t (&v)[N], int key0, const Row& row) {
+  const int lo = row.lo - key0, hi = row.hi - key0;
 #pragma unroll
-  for (int k = 0; k < NB; ++k) tmem_ld32(tS + (COLS == 32 ? quarter * 32 : 0) + 32 * k, v[k]);
-  tmem_wait_ld();
-  if (__any_sync(0xffffffffu, row.ok && (key0 < row.lo || key0 + COLS > row.hi))) {
-    const int lo = row.lo - key0, hi = row.hi - key0;
+  for (int i = 0; i < N; ++i)
+    if (i < lo || i >= hi) v[i] = 0xff800000u;
+}
+
+template <int N>
+__device__ __forceinline__ float max_of(const uint32_t (&v)[N], float m) {
+  float m4[4] = {m, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-    for (int k = 0; k < NB; ++k)
+  for (int i = 0; i < N; i += 8)
 #pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (32 * k + i < lo || 32 * k + i >= hi) v[k][i] = 0xff800000u;
-  }
-  float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-  for (int k = 0; k < NB; ++k)
-#pragma unroll
-    for (int i = 0; i < 32; ++i) m4[i & 3] = fmaxf(m4[i & 3], __uint_as_float(v[k][i]));
-  const float mc = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * c;
+    for (int k = 0; k < 4; ++k) m4[k] = max3(m4[k], __uint_as_float(v[i + 2 * k]), __uint_as_float(v[i + 2 * k + 1]));
+  return fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+}
+
+// Move the row's reference to mc (= c * new maximum) where that is more than
+// 2^kGrow above it; O and l follow.  The S tile being there means that every
+// product before it is complete, so O is at rest until the weights are handed
+// over.
+__device__ __forceinline__ void follow_max(float mc, const Row& row, bool first, uint32_t tO, int hd, float& R, float& l) {
   const bool grow = mc > R + kGrow;  // R = -inf before the row's first key
-  if (__any_sync(0xffffffffu, grow && row.ok) && !first) {
+  if (!first && __any_sync(0xffffffffu, grow && row.ok)) {
     const float f = grow ? ex2(R - mc) : 1.f;
     l *= f;
+#pragma unroll 1
     for (int d = 0; d < hd; d += 16) {
       uint32_t w[16];
-      tmem_ld16(tO + d, w);
-      tmem_wait_ld();
+      tmem_read(tO + d, w);
 #pragma unroll
       for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * f);
       tmem_st16(tO + d, w);
     }
   }
   if (grow) R = mc;
+}
+
+// Weights of scores v[at .. at + 31], rounded to the operand's type, and their sum.
+template <typename T, int N>
+__device__ __forceinline__ void weights32(const uint32_t (&v)[N], int at, f2_t c2, f2_t r2, uint32_t (&w)[16], f2_t (&sum)[2]) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float2 x = upk2(ffma2(pk2(__uint_as_float(v[at + 2 * i]), __uint_as_float(v[at + 2 * i + 1])), c2, r2));
+    const float a = ex2(x.x), b = ex2(x.y);
+    sum[i & 1] = fadd2(sum[i & 1], pk2(a, b));
+    w[i] = Kind<T>::pack(a, b);
+  }
+}
+
+// One key tile's softmax for the thread's row: 128 score columns at tS, the
+// weights to the packed operand at tS + kPCol, over scores that are in
+// registers by then.
+template <typename T>
+__device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, int key0, const Row& row, float c, bool first, int hd, float& R,
+                                             float& l) {
+  const bool ragged = __any_sync(0xffffffffu, row.ok && (key0 < row.lo || key0 + BK > row.hi));
+  uint32_t v[128];
+  tmem_read(tS, v);
+  if (ragged) mask_keys(v, key0, row);
+  follow_max(max_of(v, -INFINITY) * c, row, first, tO, hd, R, l);
   const float nr = kShift - (R == -INFINITY ? 0.f : R);
   const f2_t c2 = pk2(c, c), r2 = pk2(nr, nr);
   f2_t sum[2] = {pk2(0.f, 0.f), pk2(0.f, 0.f)};
 #pragma unroll
-  for (int k = 0; k < NB; ++k) {
+  for (int k = 0; k < 4; ++k) {
     uint32_t w[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float2 x = upk2(ffma2(pk2(__uint_as_float(v[k][2 * i]), __uint_as_float(v[k][2 * i + 1])), c2, r2));
-      const float a = ex2(x.x), b = ex2(x.y);
-      sum[i & 1] = fadd2(sum[i & 1], pk2(a, b));
-      w[i] = Kind<T>::pack(a, b);
-    }
-    if (COLS == 128) {
-      tmem_st16(tS + 16 * k, w);
-    } else {
-      uint32_t z[16];
-#pragma unroll
-      for (int i = 0; i < 16; ++i) z[i] = 0;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        if (q == quarter) tmem_st16(tS + 16 * q, w);
-        else tmem_st16(tS + 16 * q, z);
-      }
-    }
+    weights32<T>(v, 32 * k, c2, r2, w, sum);
+    tmem_st16(tS + kPCol + 16 * k, w);
   }
   const float2 s2 = upk2(fadd2(sum[0], sum[1]));
   l += s2.x + s2.y;
+  tmem_wait_st();
+}
+
+// The same for a quad tile: the warp's quarter of the columns, zero weights in
+// the others of its rows.
+template <typename T>
+__device__ __forceinline__ void softmax_quad(uint32_t tS, uint32_t tO, int quarter, int key0, const Row& row, float c, bool first, int hd,
+                                             float& R, float& l) {
+  uint32_t v[32], w[16];
+  tmem_read(tS + 32 * quarter, v);
+  if (__any_sync(0xffffffffu, row.ok && (key0 < row.lo || key0 + 32 > row.hi))) mask_keys(v, key0, row);
+  follow_max(max_of(v, -INFINITY) * c, row, first, tO, hd, R, l);
+  const float nr = kShift - (R == -INFINITY ? 0.f : R);
+  f2_t sum[2] = {pk2(0.f, 0.f), pk2(0.f, 0.f)};
+  weights32<T>(v, 0, pk2(c, c), pk2(nr, nr), w, sum);
+  const float2 s2 = upk2(fadd2(sum[0], sum[1]));
+  l += s2.x + s2.y;
+  uint32_t z[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) z[i] = 0;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    if (q == quarter) tmem_st16(tS + kPCol + 16 * q, w);
+    else tmem_st16(tS + kPCol + 16 * q, z);
+  }
   tmem_wait_st();
 }
 
@@ -493,7 +532,7 @@ __global__ void __launch_bounds__(CTHREADS, 1) chunk_kernel(const __grid_constan
   int* const ab = &sh.abort;
 
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == 0) {
       // ---------------- copies: Q tiles, and K/V tiles piece by piece of a page
       const int pr = min(1 << a.page_shift, BK);  // keys of a copy
@@ -568,49 +607,61 @@ __global__ void __launch_bounds__(CTHREADS, 1) chunk_kernel(const __grid_constan
       if (q_out) cwait(smem_u32(&sh.q_full), (nq - 1) & 1, ab, false);
       __syncwarp();
     } else if (warp == 1) {
-      // ---------------- MMA issue
-      if (lane == 0) {
+      // ---------------- MMA issue (the whole warp, converged: see umma_f16_warp)
+      {
         const uint32_t id_s = umma_idesc_f16(128, BK) | Kind<T>::kIdesc;
         const uint32_t id_o = umma_idesc_f16_bmn(128, a.head_dim) | Kind<T>::kIdesc;
         const int ksteps = a.head_dim / 16;
         int u0 = 0, nq = 0;        // ring position of the piece, Q tiles seen
         int np_[2] = {0, 0};       // P tiles consumed, per slot
         bool ok = true;
-        auto wait_full = [&](int u) { return cwait(smem_u32(&sh.full[u % NST]), (u / NST) & 1, ab); };
-        auto release = [&](int u) { umma_commit(smem_u32(&sh.empty[u % NST])); };
+        auto wait = [&](uint64_t& bar, int phase) { return __all_sync(0xffffffffu, cwait(smem_u32(&bar), phase & 1, ab)) != 0; };
+        auto wait_full = [&](int u) { return wait(sh.full[u % NST], u / NST); };
+        auto release = [&](int u) { umma_commit_warp(smem_u32(&sh.empty[u % NST])); };
         for (int k = 0; ok; ++k) {
-          if (!(ok = cwait(smem_u32(&sh.pq_full[k % QDEPTH]), (k / QDEPTH) & 1, ab))) break;
+          if (!(ok = wait(sh.pq_full[k % QDEPTH], k / QDEPTH))) break;
           const Piece p = sh.pq[k % QDEPTH];
-          mbar_arrive(smem_u32(&sh.pq_empty[k % QDEPTH]));
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&sh.pq_empty[k % QDEPTH]));
+          __syncwarp();
           if (p.mode == END) break;
           const int n = p.jb - p.ja;
           bool freed[2] = {k == 0, k == 0};  // the previous piece's O has been read
           auto qk = [&](int slot, int u) {
             tc_fence_after();
             const uint32_t q = qbase + (p.mode == PAIR ? slot * C::kQ : 0), kt = kvbase + (u % NST) * C::kKV;
-            for (int ks = 0; ks < ksteps; ++ks) {
-              const uint32_t off = (ks >> 2) * (128 * 128) + (ks & 3) * 32;
-              umma_f16(tmem + slot * 128, umma_desc_k128(q + off), umma_desc_k128(kt + off), id_s, ks != 0);
+            if (ksteps == HDP / 16) {
+#pragma unroll
+              for (int ks = 0; ks < HDP / 16; ++ks) {
+                const uint32_t off = (ks >> 2) * (128 * 128) + (ks & 3) * 32;
+                umma_f16_warp(tmem + slot * 128, umma_desc_k128(q + off), umma_desc_k128(kt + off), id_s, ks != 0);
+              }
+            } else {
+#pragma unroll 1
+              for (int ks = 0; ks < ksteps; ++ks) {
+                const uint32_t off = (ks >> 2) * (128 * 128) + (ks & 3) * 32;
+                umma_f16_warp(tmem + slot * 128, umma_desc_k128(q + off), umma_desc_k128(kt + off), id_s, ks != 0);
+              }
             }
-            umma_commit(smem_u32(&sh.s_full[slot]));
+            umma_commit_warp(smem_u32(&sh.s_full[slot]));
           };
           auto pv = [&](int slot, int u, bool first) {
-            if (!cwait(smem_u32(&sh.p_full[slot]), np_[slot] & 1, ab)) return false;
+            if (!wait(sh.p_full[slot], np_[slot])) return false;
             ++np_[slot];
             if (!freed[slot]) {
-              if (!cwait(smem_u32(&sh.o_free[slot]), (k - 1) & 1, ab)) return false;
+              if (!wait(sh.o_free[slot], k - 1)) return false;
               freed[slot] = true;
             }
             tc_fence_after();
             const uint32_t vt = kvbase + (u % NST) * C::kKV;
 #pragma unroll
             for (int ks = 0; ks < BK / 16; ++ks)
-              umma_f16_ta(tmem + 256 + slot * HDP, tmem + slot * 128 + ks * 8, umma_desc_mn128(vt + ks * 16 * 128, BK * 128, 1024), id_o,
+              umma_f16_ta_warp(tmem + 256 + slot * HDP, tmem + slot * 128 + kPCol + ks * 8, umma_desc_mn128(vt + ks * 16 * 128, BK * 128, 1024), id_o,
                           !(first && ks == 0));
             return true;
           };
           if (n > 0) {
-            if (!(ok = cwait(smem_u32(&sh.q_full), nq & 1, ab))) break;
+            if (!(ok = wait(sh.q_full, nq))) break;
             ++nq;
             const int u = u0;
             u0 += 2 * n;
@@ -621,14 +672,14 @@ __global__ void __launch_bounds__(CTHREADS, 1) chunk_kernel(const __grid_constan
               if (on(s0, p.ja)) qk(0, u);
               if (on(s1, p.ja)) qk(1, u);
               release(u);
-              if (n == 1) umma_commit(smem_u32(&sh.q_empty));
+              if (n == 1) umma_commit_warp(smem_u32(&sh.q_empty));
               for (int j = p.ja; ok && j < p.jb; ++j) {
                 const int i = j - p.ja, uv = u + 2 * i + 1, uk = uv + 1;
                 const bool more = j + 1 < p.jb;
                 if (!(ok = wait_full(uv))) break;
                 if (on(s0, j)) {
                   if (!(ok = pv(0, uv, j == s0.first))) break;
-                  if (j + 1 == s0.first + s0.count) umma_commit(smem_u32(&sh.o_full[0]));
+                  if (j + 1 == s0.first + s0.count) umma_commit_warp(smem_u32(&sh.o_full[0]));
                 }
                 if (more) {
                   if (!(ok = wait_full(uk))) break;
@@ -636,13 +687,13 @@ __global__ void __launch_bounds__(CTHREADS, 1) chunk_kernel(const __grid_constan
                 }
                 if (on(s1, j)) {
                   if (!(ok = pv(1, uv, j == s1.first))) break;
-                  if (j + 1 == s1.first + s1.count) umma_commit(smem_u32(&sh.o_full[1]));
+                  if (j + 1 == s1.first + s1.count) umma_commit_warp(smem_u32(&sh.o_full[1]));
                 }
                 release(uv);
                 if (more) {
                   if (on(s1, j + 1)) qk(1, uk);
                   release(uk);
-                  if (j + 2 == p.jb) umma_commit(smem_u32(&sh.q_empty));
+                  if (j + 2 == p.jb) umma_commit_warp(smem_u32(&sh.q_empty));
                 }
               }
             } else {
@@ -650,26 +701,26 @@ __global__ void __launch_bounds__(CTHREADS, 1) chunk_kernel(const __grid_constan
                 if (!(ok = wait_full(u + i))) break;
                 qk(i, u + i);
                 release(u + i);
-                if (i == n - 1) umma_commit(smem_u32(&sh.q_empty));
+                if (i == n - 1) umma_commit_warp(smem_u32(&sh.q_empty));
               }
               for (int i = 0; ok && i < n; ++i) {
                 const int slot = i & 1, uv = u + ring_v(p.mode, i, n);
                 if (!(ok = wait_full(uv))) break;
                 if (!(ok = pv(slot, uv, i < 2))) break;
                 release(uv);
-                if (i + 2 >= n) umma_commit(smem_u32(&sh.o_full[slot]));
+                if (i + 2 >= n) umma_commit_warp(smem_u32(&sh.o_full[slot]));
                 if (i + 2 < n) {
                   const int uk = u + ring_k(p.mode, i + 2);
                   if (!(ok = wait_full(uk))) break;
                   qk(slot, uk);
                   release(uk);
-                  if (i + 2 == n - 1) umma_commit(smem_u32(&sh.q_empty));
+                  if (i + 2 == n - 1) umma_commit_warp(smem_u32(&sh.q_empty));
                 }
               }
             }
           }
           for (int s = 0; ok && s < 2; ++s)  // every phase of o_free is seen once
-            if (!freed[s]) ok = cwait(smem_u32(&sh.o_free[s]), (k - 1) & 1, ab);
+            if (!freed[s]) ok = wait(sh.o_free[s], k - 1);
         }
       }
       __syncwarp();
@@ -725,7 +776,7 @@ __global__ void __launch_bounds__(CTHREADS, 1) chunk_kernel(const __grid_constan
     }
   } else {
     // ---------------- softmax and epilogue: slot = warpgroup, thread = row (TMEM lane)
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     const int slot = (warp >> 2) - 1, quarter = warp & 3, tw = tid & 127;
     const uint32_t tl = (uint32_t)(quarter * 32) << 16;
     const uint32_t tS = tmem + tl + slot * 128, tO = tmem + tl + 256 + slot * HDP;
@@ -737,9 +788,8 @@ __global__ void __launch_bounds__(CTHREADS, 1) chunk_kernel(const __grid_constan
     bool ok = true;
     for (int k = 0; ok; ++k) {
       if (!(ok = __all_sync(0xffffffffu, cwait(smem_u32(&sh.pq_full[k % QDEPTH]), (k / QDEPTH) & 1, ab)))) break;
-      const Piece p = sh.pq[k % QDEPTH];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sh.pq_empty[k % QDEPTH]));
+      // read where it lies (registers are short here); handed back at the end of the piece
+      const Piece& p = sh.pq[k % QDEPTH];
       if (p.mode == END) break;
       const int n = p.jb - p.ja, u = u0;
       u0 += 2 * n;
@@ -778,8 +828,8 @@ __global__ void __launch_bounds__(CTHREADS, 1) chunk_kernel(const __grid_constan
           }
           fence_async_smem();
         }
-        if (p.mode == QUAD) softmax_tile<T, 32>(tS, tO, quarter, j * BK + quarter * 32, row, a.c, i == 0, hd, R, l);
-        else softmax_tile<T, 128>(tS, tO, quarter, j * BK, row, a.c, i == 0, hd, R, l);
+        if (p.mode == QUAD) softmax_quad<T>(tS, tO, quarter, j * BK + quarter * 32, row, a.c, i == 0, hd, R, l);
+        else softmax_tile<T>(tS, tO, j * BK, row, a.c, i == 0, hd, R, l);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&sh.p_full[slot]));
@@ -805,6 +855,8 @@ __global__ void __launch_bounds__(CTHREADS, 1) chunk_kernel(const __grid_constan
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&sh.x_full));
           }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&sh.pq_empty[k % QDEPTH]));
           continue;
         }
         if (count1) {
@@ -828,10 +880,9 @@ __global__ void __launch_bounds__(CTHREADS, 1) chunk_kernel(const __grid_constan
         w1 *= inv;
         T* out = static_cast<T*>(a.o) + t * a.o_stride + (size_t)head * hd;
         for (int d = 0; d < hd; d += 16) {
-          uint32_t v[16], w[16];
-          if (use0) tmem_ld16(tO + d, v);
-          if (use1) tmem_ld16(tO1 + d, w);
-          tmem_wait_ld();
+          uint32_t v[16] = {}, w[16] = {};
+          if (use0) tmem_read(tO + d, v);
+          if (use1) tmem_read(tO1 + d, w);
           float f[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
@@ -872,10 +923,9 @@ __global__ void __launch_bounds__(CTHREADS, 1) chunk_kernel(const __grid_constan
         for (int d = 0; ok && d < hd; d += 32) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            uint32_t v[16], w[16];
-            if (use0) tmem_ld16(tO + d + 16 * h, v);
-            if (use1) tmem_ld16(tO1 + d + 16 * h, w);
-            tmem_wait_ld();
+            uint32_t v[16] = {}, w[16] = {};
+            if (use0) tmem_read(tO + d + 16 * h, v);
+            if (use1) tmem_read(tO1 + d + 16 * h, w);
             float g[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
@@ -942,6 +992,8 @@ __global__ void __launch_bounds__(CTHREADS, 1) chunk_kernel(const __grid_constan
           join<T, HDP>(a, p.c0, p.np, p.kvh, p.row0 + tok0, slot, nrows, tw);
         }
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sh.pq_empty[k % QDEPTH]));
     }
     if (!ok && a.status && lane == 0) atomicOr(a.status, kTimeout);
   }
