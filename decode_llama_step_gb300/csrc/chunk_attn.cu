@@ -96,7 +96,7 @@ struct CCfg {
 };
 
 struct CMisc {
-  uint64_t full[8], empty[8], s_full[2], p_full[2], o_full[2], o_free[2], q_full, q_empty, x_full, wg[2], pq_full[QDEPTH], pq_empty[QDEPTH];
+  uint64_t full[8], empty[8], s_full[2], p_full[2][2], o_full[2], o_free[2], q_full, q_empty, x_full, wg[2], pq_full[QDEPTH], pq_empty[QDEPTH];
   Piece pq[QDEPTH];
   float xm[128], xl[128];        // slot 1's statistics for slot 0 (split)
   float qm[4][32], ql[4][32];    // per quarter (quad)
@@ -118,22 +118,23 @@ static_assert(2 * chunk_smem<64>() > 227 * 1024, "one CTA per SM");
 static_assert(DLS_MAX_CHUNK_SEQS * 16 <= CCfg<64>::kXOff, "plan scratch");
 
 __device__ __forceinline__ bool cwait(uint32_t bar, uint32_t parity, int* abort_flag, bool heed_abort = true) {
+  uint64_t t0 = 0;
 #pragma unroll 1
-  for (int i = 0; i < 32; ++i)
-    if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = global_ns();
-#pragma unroll 1
-  for (uint32_t i = 1;; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 15) == 0) {
-      if (heed_abort && *(volatile int*)abort_flag) return false;
-      if (global_ns() - t0 > kWaitNsC) {
-        *(volatile int*)abort_flag = 1;
-        return false;
-      }
+  for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i) {
+    if (i & 63) continue;
+    if (heed_abort && *(volatile int*)abort_flag) return false;
+    const uint64_t t = global_ns();
+    if (!t0) t0 = t;
+    if (t - t0 > kWaitNsC) {
+      *(volatile int*)abort_flag = 1;
+      return false;
     }
   }
+  return true;
 }
+
+// A value that is the same in every lane, as one the compiler knows to be.
+__device__ __forceinline__ int uniform(int x) { return (int)__reduce_max_sync(0xffffffffu, (unsigned)x); }
 
 // The four warps of a softmax group meet (a bounded bar.sync: false after an
 // abort, so no warp waits for one that gave up).
@@ -376,6 +377,14 @@ __device__ __forceinline__ void follow_max(float mc, const Row& row, bool first,
   if (grow) R = mc;
 }
 
+// The warp's weights stored so far are visible to the tensor core.
+__device__ __forceinline__ void hand_over(uint32_t bar, int lane) {
+  tmem_wait_st();
+  tc_fence_before();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
+}
+
 // Weights of scores v[at .. at + 31], rounded to the operand's type, and their sum.
 template <typename T, int N>
 __device__ __forceinline__ void weights32(const uint32_t (&v)[N], int at, f2_t c2, f2_t r2, uint32_t (&w)[16], f2_t (&sum)[2]) {
@@ -393,7 +402,7 @@ __device__ __forceinline__ void weights32(const uint32_t (&v)[N], int at, f2_t c
 // registers by then.
 template <typename T>
 __device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, int key0, const Row& row, float c, bool first, int hd, float& R,
-                                             float& l) {
+                                             float& l, uint32_t p_half, int lane) {
   const bool ragged = __any_sync(0xffffffffu, row.ok && (key0 < row.lo || key0 + BK > row.hi));
   uint32_t v[128];
   tmem_read(tS, v);
@@ -407,10 +416,10 @@ __device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, int key0,
     uint32_t w[16];
     weights32<T>(v, 32 * k, c2, r2, w, sum);
     tmem_st16(tS + kPCol + 16 * k, w);
+    if (k == 1) hand_over(p_half, lane);
   }
   const float2 s2 = upk2(fadd2(sum[0], sum[1]));
   l += s2.x + s2.y;
-  tmem_wait_st();
 }
 
 // The same for a quad tile: the warp's quarter of the columns, zero weights in
@@ -435,7 +444,6 @@ __device__ __forceinline__ void softmax_quad(uint32_t tS, uint32_t tO, int quart
     if (q == quarter) tmem_st16(tS + kPCol + 16 * q, w);
     else tmem_st16(tS + kPCol + 16 * q, z);
   }
-  tmem_wait_st();
 }
 
 __device__ __forceinline__ float weight(float R, float M) { return R == -INFINITY ? 0.f : ex2(R - M); }
@@ -497,7 +505,8 @@ __global__ void __launch_bounds__(CTHREADS, 1) chunk_kernel(const __grid_constan
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&sh.s_full[i]), 1);
-      mbar_init(smem_u32(&sh.p_full[i]), 4);
+      mbar_init(smem_u32(&sh.p_full[i][0]), 4);
+      mbar_init(smem_u32(&sh.p_full[i][1]), 4);
       mbar_init(smem_u32(&sh.o_full[i]), 1);
       mbar_init(smem_u32(&sh.o_free[i]), 4);
     }
@@ -608,120 +617,123 @@ __global__ void __launch_bounds__(CTHREADS, 1) chunk_kernel(const __grid_constan
       __syncwarp();
     } else if (warp == 1) {
       // ---------------- MMA issue (the whole warp, converged: see umma_f16_warp)
-      {
-        const uint32_t id_s = umma_idesc_f16(128, BK) | Kind<T>::kIdesc;
-        const uint32_t id_o = umma_idesc_f16_bmn(128, a.head_dim) | Kind<T>::kIdesc;
-        const int ksteps = a.head_dim / 16;
-        int u0 = 0, nq = 0;        // ring position of the piece, Q tiles seen
-        int np_[2] = {0, 0};       // P tiles consumed, per slot
-        bool ok = true;
-        auto wait = [&](uint64_t& bar, int phase) { return __all_sync(0xffffffffu, cwait(smem_u32(&bar), phase & 1, ab)) != 0; };
-        auto wait_full = [&](int u) { return wait(sh.full[u % NST], u / NST); };
-        auto release = [&](int u) { umma_commit_warp(smem_u32(&sh.empty[u % NST])); };
-        for (int k = 0; ok; ++k) {
-          if (!(ok = wait(sh.pq_full[k % QDEPTH], k / QDEPTH))) break;
-          const Piece p = sh.pq[k % QDEPTH];
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&sh.pq_empty[k % QDEPTH]));
-          __syncwarp();
-          if (p.mode == END) break;
-          const int n = p.jb - p.ja;
-          bool freed[2] = {k == 0, k == 0};  // the previous piece's O has been read
-          auto qk = [&](int slot, int u) {
-            tc_fence_after();
-            const uint32_t q = qbase + (p.mode == PAIR ? slot * C::kQ : 0), kt = kvbase + (u % NST) * C::kKV;
-            if (ksteps == HDP / 16) {
+      const uint32_t id_s = umma_idesc_f16(128, BK) | Kind<T>::kIdesc;
+      const uint32_t id_o = umma_idesc_f16_bmn(128, a.head_dim) | Kind<T>::kIdesc;
+      const int ksteps = a.head_dim / 16;
+      int u0 = 0, nq = 0;        // ring position of the piece, Q tiles seen
+      int np0 = 0, np1 = 0;      // weights consumed, per slot
+      bool ok = true;
+      auto wait = [&](uint64_t& bar, int phase) { return __all_sync(0xffffffffu, cwait(smem_u32(&bar), phase & 1, ab)) != 0; };
+      auto wait_full = [&](int u) { return wait(sh.full[u % NST], u / NST); };
+      auto release = [&](int u) { umma_commit_warp(smem_u32(&sh.empty[u % NST])); };
+      auto qk = [&](int slot, uint32_t q, int u) {
+        const uint32_t kt = kvbase + (u % NST) * C::kKV;
+        tc_fence_after();
+        if (ksteps == HDP / 16) {
 #pragma unroll
-              for (int ks = 0; ks < HDP / 16; ++ks) {
-                const uint32_t off = (ks >> 2) * (128 * 128) + (ks & 3) * 32;
-                umma_f16_warp(tmem + slot * 128, umma_desc_k128(q + off), umma_desc_k128(kt + off), id_s, ks != 0);
-              }
-            } else {
+          for (int ks = 0; ks < HDP / 16; ++ks) {
+            const uint32_t off = (ks >> 2) * (128 * 128) + (ks & 3) * 32;
+            umma_f16_warp(tmem + slot * 128, umma_desc_k128(q + off), umma_desc_k128(kt + off), id_s, ks != 0);
+          }
+        } else {
 #pragma unroll 1
-              for (int ks = 0; ks < ksteps; ++ks) {
-                const uint32_t off = (ks >> 2) * (128 * 128) + (ks & 3) * 32;
-                umma_f16_warp(tmem + slot * 128, umma_desc_k128(q + off), umma_desc_k128(kt + off), id_s, ks != 0);
-              }
-            }
-            umma_commit_warp(smem_u32(&sh.s_full[slot]));
-          };
-          auto pv = [&](int slot, int u, bool first) {
-            if (!wait(sh.p_full[slot], np_[slot])) return false;
-            ++np_[slot];
-            if (!freed[slot]) {
-              if (!wait(sh.o_free[slot], k - 1)) return false;
-              freed[slot] = true;
-            }
-            tc_fence_after();
-            const uint32_t vt = kvbase + (u % NST) * C::kKV;
+          for (int ks = 0; ks < ksteps; ++ks) {
+            const uint32_t off = (ks >> 2) * (128 * 128) + (ks & 3) * 32;
+            umma_f16_warp(tmem + slot * 128, umma_desc_k128(q + off), umma_desc_k128(kt + off), id_s, ks != 0);
+          }
+        }
+        umma_commit_warp(smem_u32(&sh.s_full[slot]));
+      };
+      // the weights arrive in two halves (64 keys each); the first product of
+      // a piece waits until the piece before has read the slot's O
+      auto pv = [&](int slot, int phase, int u, bool first, int k) {
+        if (!wait(sh.p_full[slot][0], phase)) return false;
+        if (first && k > 0 && !wait(sh.o_free[slot], k - 1)) return false;
+        tc_fence_after();
+        const uint32_t vt = kvbase + (u % NST) * C::kKV, tp = tmem + slot * 128 + kPCol, to = tmem + 256 + slot * HDP;
 #pragma unroll
-            for (int ks = 0; ks < BK / 16; ++ks)
-              umma_f16_ta_warp(tmem + 256 + slot * HDP, tmem + slot * 128 + kPCol + ks * 8, umma_desc_mn128(vt + ks * 16 * 128, BK * 128, 1024), id_o,
-                          !(first && ks == 0));
-            return true;
-          };
-          if (n > 0) {
-            if (!(ok = wait(sh.q_full, nq))) break;
-            ++nq;
-            const int u = u0;
-            u0 += 2 * n;
-            if (p.mode == PAIR) {
-              const Steps s0 = slot_steps(a, p, 0), s1 = slot_steps(a, p, 1);
-              auto on = [&](const Steps& s, int j) { return j >= s.first && j < s.first + s.count; };
-              if (!(ok = wait_full(u))) break;
-              if (on(s0, p.ja)) qk(0, u);
-              if (on(s1, p.ja)) qk(1, u);
-              release(u);
-              if (n == 1) umma_commit_warp(smem_u32(&sh.q_empty));
-              for (int j = p.ja; ok && j < p.jb; ++j) {
-                const int i = j - p.ja, uv = u + 2 * i + 1, uk = uv + 1;
-                const bool more = j + 1 < p.jb;
-                if (!(ok = wait_full(uv))) break;
-                if (on(s0, j)) {
-                  if (!(ok = pv(0, uv, j == s0.first))) break;
-                  if (j + 1 == s0.first + s0.count) umma_commit_warp(smem_u32(&sh.o_full[0]));
-                }
-                if (more) {
-                  if (!(ok = wait_full(uk))) break;
-                  if (on(s0, j + 1)) qk(0, uk);
-                }
-                if (on(s1, j)) {
-                  if (!(ok = pv(1, uv, j == s1.first))) break;
-                  if (j + 1 == s1.first + s1.count) umma_commit_warp(smem_u32(&sh.o_full[1]));
-                }
-                release(uv);
-                if (more) {
-                  if (on(s1, j + 1)) qk(1, uk);
-                  release(uk);
-                  if (j + 2 == p.jb) umma_commit_warp(smem_u32(&sh.q_empty));
-                }
+        for (int ks = 0; ks < BK / 32; ++ks)
+          umma_f16_ta_warp(to, tp + ks * 8, umma_desc_mn128(vt + ks * 16 * 128, BK * 128, 1024), id_o, !(first && ks == 0));
+        if (!wait(sh.p_full[slot][1], phase)) return false;
+        tc_fence_after();
+#pragma unroll
+        for (int ks = BK / 32; ks < BK / 16; ++ks)
+          umma_f16_ta_warp(to, tp + ks * 8, umma_desc_mn128(vt + ks * 16 * 128, BK * 128, 1024), id_o, true);
+        return true;
+      };
+      for (int k = 0; ok; ++k) {
+        if (!(ok = wait(sh.pq_full[k % QDEPTH], k / QDEPTH))) break;
+        const Piece& p = sh.pq[k % QDEPTH];
+        const int mode = uniform(p.mode);
+        if (mode == END) break;
+        const int n = uniform(p.jb - p.ja);
+        const Steps s0 = slot_steps(a, p, 0), s1 = slot_steps(a, p, 1);
+        const int f0 = uniform(s0.first - p.ja), f1 = uniform(s1.first - p.ja), c0 = uniform(s0.count), c1 = uniform(s1.count);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sh.pq_empty[k % QDEPTH]));
+        __syncwarp();
+        if (n > 0) {
+          if (!(ok = wait(sh.q_full, nq))) break;
+          ++nq;
+          const int u = u0;
+          u0 += 2 * n;
+          if (mode == PAIR) {
+            const int e0 = f0 + c0, e1 = f1 + c1;  // slot s works on key tiles f .. e - 1
+            if (!(ok = wait_full(u))) break;
+            if (f0 == 0 && c0) qk(0, qbase, u);
+            if (f1 == 0 && c1) qk(1, qbase + C::kQ, u);
+            release(u);
+            if (n == 1) umma_commit_warp(smem_u32(&sh.q_empty));
+            for (int i = 0; i < n; ++i) {
+              const int uv = u + 2 * i + 1, uk = uv + 1;
+              const bool more = i + 1 < n;
+              if (!(ok = wait_full(uv))) break;
+              if (i >= f0 && i < e0) {
+                if (!(ok = pv(0, np0++, uv, i == f0, k))) break;
+                if (i + 1 == e0) umma_commit_warp(smem_u32(&sh.o_full[0]));
               }
-            } else {
-              for (int i = 0; i < min(n, 2); ++i) {
-                if (!(ok = wait_full(u + i))) break;
-                qk(i, u + i);
-                release(u + i);
-                if (i == n - 1) umma_commit_warp(smem_u32(&sh.q_empty));
+              if (more) {
+                if (!(ok = wait_full(uk))) break;
+                if (i + 1 >= f0 && i + 1 < e0) qk(0, qbase, uk);
               }
-              for (int i = 0; ok && i < n; ++i) {
-                const int slot = i & 1, uv = u + ring_v(p.mode, i, n);
-                if (!(ok = wait_full(uv))) break;
-                if (!(ok = pv(slot, uv, i < 2))) break;
-                release(uv);
-                if (i + 2 >= n) umma_commit_warp(smem_u32(&sh.o_full[slot]));
-                if (i + 2 < n) {
-                  const int uk = u + ring_k(p.mode, i + 2);
-                  if (!(ok = wait_full(uk))) break;
-                  qk(slot, uk);
-                  release(uk);
-                  if (i + 2 == n - 1) umma_commit_warp(smem_u32(&sh.q_empty));
-                }
+              if (i >= f1 && i < e1) {
+                if (!(ok = pv(1, np1++, uv, i == f1, k))) break;
+                if (i + 1 == e1) umma_commit_warp(smem_u32(&sh.o_full[1]));
+              }
+              release(uv);
+              if (more) {
+                if (i + 1 >= f1 && i + 1 < e1) qk(1, qbase + C::kQ, uk);
+                release(uk);
+                if (i + 2 == n) umma_commit_warp(smem_u32(&sh.q_empty));
+              }
+            }
+          } else {
+            // two key tiles (one per slot) a turn
+            for (int i = 0; i < 2 && i < n; ++i) {
+              if (!(ok = wait_full(u + i))) break;
+              qk(i, qbase, u + i);
+              release(u + i);
+              if (i == n - 1) umma_commit_warp(smem_u32(&sh.q_empty));
+            }
+            for (int i = 0; ok && i < n; ++i) {
+              const int slot = i & 1, uv = u + ring_v(mode, i, n);
+              if (!(ok = wait_full(uv))) break;
+              if (!(ok = pv(slot, slot ? np1++ : np0++, uv, i < 2, k))) break;
+              release(uv);
+              if (i + 2 >= n) umma_commit_warp(smem_u32(&sh.o_full[slot]));
+              if (i + 2 < n) {
+                const int uk = u + ring_k(mode, i + 2);
+                if (!(ok = wait_full(uk))) break;
+                qk(slot, qbase, uk);
+                release(uk);
+                if (i + 2 == n - 1) umma_commit_warp(smem_u32(&sh.q_empty));
               }
             }
           }
-          for (int s = 0; ok && s < 2; ++s)  // every phase of o_free is seen once
-            if (!freed[s]) ok = wait(sh.o_free[s], k - 1);
         }
+        // every phase of o_free is passed, in order
+        if (ok && k > 0 && c0 == 0) ok = wait(sh.o_free[0], k - 1);
+        if (ok && k > 0 && c1 == 0) ok = wait(sh.o_free[1], k - 1);
       }
       __syncwarp();
     } else if (warp == 2) {
@@ -828,11 +840,15 @@ __global__ void __launch_bounds__(CTHREADS, 1) chunk_kernel(const __grid_constan
           }
           fence_async_smem();
         }
-        if (p.mode == QUAD) softmax_quad<T>(tS, tO, quarter, j * BK + quarter * 32, row, a.c, i == 0, hd, R, l);
-        else softmax_tile<T>(tS, tO, j * BK, row, a.c, i == 0, hd, R, l);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sh.p_full[slot]));
+        const uint32_t h0 = smem_u32(&sh.p_full[slot][0]), h1 = smem_u32(&sh.p_full[slot][1]);
+        if (p.mode == QUAD) {
+          softmax_quad<T>(tS, tO, quarter, j * BK + quarter * 32, row, a.c, i == 0, hd, R, l);
+          hand_over(h0, lane);
+          if (lane == 0) mbar_arrive(h1);
+        } else {
+          softmax_tile<T>(tS, tO, j * BK, row, a.c, i == 0, hd, R, l, h0, lane);
+          hand_over(h1, lane);
+        }
       }
       if (!ok) break;
       if (st.count) {
