@@ -55,6 +55,7 @@ constexpr float kGrow = 8.f;     // log2 the maximum may exceed the reference by
 constexpr float kShift = 7.f;    // weights are kept as 2^(c s - R + 7): at most 2^15 in fp16, with 7 more binades below
 constexpr uint64_t kWaitNsC = 2000000000ull;
 constexpr int kPCol = 64;         // the weights' columns in a slot's S (packed: 64 of them)
+constexpr int kJoinCap = 1024;     // (piece, row) statistics of a slot that a join keeps in shared memory
 constexpr int kCounterBytes = 4096;  // int [MAXC][2], at the start of the workspace
 
 enum Mode { PAIR = 0, SPLIT = 1, QUAD = 2, END = 3 };
@@ -92,7 +93,8 @@ struct CCfg {
   static constexpr int NST = HDP == 128 ? 4 : 8;
   static constexpr int kKVOff = 2 * kQ;
   static constexpr int kXOff = kKVOff + NST * kKV;  // float [4][32][32]: joins the quarters of a quad tile
-  static constexpr int kMiscOff = kXOff + 4 * 32 * 32 * 4;
+  static constexpr int kJOff = kXOff + 4 * 32 * 32 * 4;  // statistics being joined: slot 0's in X, slot 1's here
+  static constexpr int kMiscOff = kJOff + 2 * kJoinCap * 4;
 };
 
 struct CMisc {
@@ -111,6 +113,7 @@ template <int HDP>
 constexpr int chunk_smem() {
   return CCfg<HDP>::kMiscOff + (int)sizeof(CMisc) + 1024;
 }
+static_assert(2 * kJoinCap * 4 <= 4 * 32 * 32 * 4, "join area");
 static_assert(chunk_smem<128>() <= 227 * 1024 && chunk_smem<64>() <= 227 * 1024, "shared memory");
 // a CTA allocates all of tensor memory: a second one must not fit on the SM
 static_assert(2 * chunk_smem<64>() > 227 * 1024, "one CTA per SM");
@@ -450,37 +453,78 @@ __device__ __forceinline__ float weight(float R, float M) { return R == -INFINIT
 
 template <int HDP>
 __device__ __forceinline__ float* partial_at(const ChunkArgs& a, int cta, int which, int slot) {
-  return a.partials + (size_t)((cta * 2 + which) * 2 + slot) * (128 * (HDP + 2));  // R [128], l [128], O [128][HDP]
+  return a.partials + (size_t)((cta * 2 + which) * 2 + slot) * (128 * (HDP + 2));  // R [128], l [128], O [HDP / 4][128][4]
 }
 
 __device__ __forceinline__ float lse_of(float R, float l) {
   return l > 0.f ? fmaf(R - kShift, 0.6931471805599453f, logf(l)) : -INFINITY;
 }
 
-// Join the partials of a tile's slot (rows 0..nrows-1; 128 threads).
+// Join the partials of a tile's slot (rows 0..nrows-1; the slot's 128
+// threads).  The statistics of all pieces go to shared memory first, so that
+// the long loop has nothing but independent loads of O, which lie row by row
+// for four columns at a time: lanes read neighbours.
 template <typename T, int HDP>
-__device__ __noinline__ void join(const ChunkArgs& a, int c0, int np, int kvh, int row0, int slot, int nrows, int tw) {
-  const int c4 = a.head_dim / 4;
-  for (int x = tw; x < nrows * c4; x += 128) {
-    const int r = x / c4, d = (x - r * c4) * 4;
+__device__ __noinline__ bool join(const ChunkArgs& a, int c0, int np, int kvh, int row0, int slot, int nrows, int tw, float* area,
+                                  uint32_t wg, uint32_t& wph, int* ab) {
+  float *sw = area, *sl = area + kJoinCap;
+  const bool fits = np * nrows <= kJoinCap;
+  const int lane = tw & 31, c8 = a.head_dim / 8;
+  if (fits) {
+    for (int x = tw; x < np * nrows; x += 128) {
+      const int i = x / nrows;
+      const float* q = partial_at<HDP>(a, c0 + i, i == 0, slot) + (x - i * nrows);
+      sw[x] = __ldcg(q);
+      sl[x] = __ldcg(q + 128);
+    }
+    if (!wg_sync(wg, wph, lane, ab)) return false;
+  }
+  for (int r = tw; r < nrows; r += 128) {
+    if (!fits) break;
     float M = -INFINITY, L = 0.f;
-    for (int i = 0; i < np; ++i) M = fmaxf(M, __ldcg(partial_at<HDP>(a, c0 + i, i == 0, slot) + r));
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < np; ++i) M = fmaxf(M, sw[i * nrows + r]);
+    for (int i = 0; i < np; ++i) {
+      const float w = weight(sw[i * nrows + r], M);
+      L = fmaf(w, sl[i * nrows + r], L);
+      sw[i * nrows + r] = w;
+    }
+    sl[r] = L > 0.f ? 1.f / L : 0.f;
+    if (a.lse) {
+      const int tok = r / a.group;
+      a.lse[((size_t)row0 + tok) * (a.n_kv * a.group) + kvh * a.group + r - tok * a.group] = lse_of(M, L);
+    }
+  }
+  if (fits && !wg_sync(wg, wph, lane, ab)) return false;
+  for (int x = tw; x < nrows * c8; x += 128) {
+    const int d = x / nrows, r = x - d * nrows;
+    const int tok = r / a.group, head = kvh * a.group + r - tok * a.group;
+    const size_t t = (size_t)row0 + tok;
+    float M = -INFINITY, L = 0.f;
+    if (!fits)
+      for (int i = 0; i < np; ++i) M = fmaxf(M, __ldcg(partial_at<HDP>(a, c0 + i, i == 0, slot) + r));
+    float4 u = make_float4(0.f, 0.f, 0.f, 0.f), v = u;
 #pragma unroll 4
     for (int i = 0; i < np; ++i) {
       const float* q = partial_at<HDP>(a, c0 + i, i == 0, slot);
-      const float w = weight(__ldcg(q + r), M);
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(q + 256 + r * HDP + d));
-      L = fmaf(w, __ldcg(q + 128 + r), L);
-      acc.x = fmaf(w, v.x, acc.x), acc.y = fmaf(w, v.y, acc.y), acc.z = fmaf(w, v.z, acc.z), acc.w = fmaf(w, v.w, acc.w);
+      float w;
+      if (fits) {
+        w = sw[i * nrows + r];
+      } else {
+        w = weight(__ldcg(q + r), M);
+        L = fmaf(w, __ldcg(q + 128 + r), L);
+      }
+      const float4 y = __ldcg(reinterpret_cast<const float4*>(q + 256) + 2 * d * 128 + r);
+      const float4 z = __ldcg(reinterpret_cast<const float4*>(q + 256) + (2 * d + 1) * 128 + r);
+      u.x = fmaf(w, y.x, u.x), u.y = fmaf(w, y.y, u.y), u.z = fmaf(w, y.z, u.z), u.w = fmaf(w, y.w, u.w);
+      v.x = fmaf(w, z.x, v.x), v.y = fmaf(w, z.y, v.y), v.z = fmaf(w, z.z, v.z), v.w = fmaf(w, z.w, v.w);
     }
-    const float inv = L > 0.f ? 1.f / L : 0.f;
-    const int tok = r / a.group, head = kvh * a.group + r - tok * a.group;
-    const size_t t = (size_t)row0 + tok;
-    *reinterpret_cast<uint2*>(static_cast<T*>(a.o) + t * a.o_stride + (size_t)head * a.head_dim + d) =
-        make_uint2(Kind<T>::pack(acc.x * inv, acc.y * inv), Kind<T>::pack(acc.z * inv, acc.w * inv));
-    if (a.lse && d == 0) a.lse[t * (a.n_kv * a.group) + head] = lse_of(M, L);
+    const float inv = fits ? sl[r] : L > 0.f ? 1.f / L : 0.f;
+    *reinterpret_cast<uint4*>(static_cast<T*>(a.o) + t * a.o_stride + (size_t)head * a.head_dim + 8 * d) =
+        make_uint4(Kind<T>::pack(u.x * inv, u.y * inv), Kind<T>::pack(u.z * inv, u.w * inv), Kind<T>::pack(v.x * inv, v.y * inv),
+                   Kind<T>::pack(v.z * inv, v.w * inv));
+    if (!fits && a.lse && d == 0) a.lse[t * (a.n_kv * a.group) + head] = lse_of(M, L);
   }
+  return true;
 }
 
 template <typename T, int HDP>
@@ -629,18 +673,14 @@ __global__ void __launch_bounds__(CTHREADS, 1) chunk_kernel(const __grid_constan
       auto qk = [&](int slot, uint32_t q, int u) {
         const uint32_t kt = kvbase + (u % NST) * C::kKV;
         tc_fence_after();
-        if (ksteps == HDP / 16) {
-#pragma unroll
-          for (int ks = 0; ks < HDP / 16; ++ks) {
-            const uint32_t off = (ks >> 2) * (128 * 128) + (ks & 3) * 32;
-            umma_f16_warp(tmem + slot * 128, umma_desc_k128(q + off), umma_desc_k128(kt + off), id_s, ks != 0);
-          }
-        } else {
+        const uint64_t qd = umma_desc_k128(q), kd = umma_desc_k128(kt);
+        int ks = 0;
 #pragma unroll 1
-          for (int ks = 0; ks < ksteps; ++ks) {
-            const uint32_t off = (ks >> 2) * (128 * 128) + (ks & 3) * 32;
-            umma_f16_warp(tmem + slot * 128, umma_desc_k128(q + off), umma_desc_k128(kt + off), id_s, ks != 0);
-          }
+        for (; ks + 4 <= ksteps; ks += 4) umma_f16_warp4(tmem + slot * 128, qd + ks * 256, kd + ks * 256, id_s, ks != 0);
+#pragma unroll 1
+        for (; ks < ksteps; ++ks) {
+          const uint32_t off = (ks >> 2) * 1024 + (ks & 3) * 2;
+          umma_f16_warp(tmem + slot * 128, qd + off, kd + off, id_s, ks != 0);
         }
         umma_commit_warp(smem_u32(&sh.s_full[slot]));
       };
@@ -651,14 +691,11 @@ __global__ void __launch_bounds__(CTHREADS, 1) chunk_kernel(const __grid_constan
         if (first && k > 0 && !wait(sh.o_free[slot], k - 1)) return false;
         tc_fence_after();
         const uint32_t vt = kvbase + (u % NST) * C::kKV, tp = tmem + slot * 128 + kPCol, to = tmem + 256 + slot * HDP;
-#pragma unroll
-        for (int ks = 0; ks < BK / 32; ++ks)
-          umma_f16_ta_warp(to, tp + ks * 8, umma_desc_mn128(vt + ks * 16 * 128, BK * 128, 1024), id_o, !(first && ks == 0));
+        const uint64_t vd = umma_desc_mn128(vt, BK * 128, 1024);
+        umma_f16_ta_warp4(to, tp, vd, id_o, !first);
         if (!wait(sh.p_full[slot][1], phase)) return false;
         tc_fence_after();
-#pragma unroll
-        for (int ks = BK / 32; ks < BK / 16; ++ks)
-          umma_f16_ta_warp(to, tp + ks * 8, umma_desc_mn128(vt + ks * 16 * 128, BK * 128, 1024), id_o, true);
+        umma_f16_ta_warp4(to, tp + 32, vd + 512, id_o, true);
         return true;
       };
       for (int k = 0; ok; ++k) {
@@ -909,7 +946,7 @@ __global__ void __launch_bounds__(CTHREADS, 1) chunk_kernel(const __grid_constan
             if (part) {
 #pragma unroll
               for (int i = 0; i < 4; ++i)
-                __stcg(reinterpret_cast<float4*>(part + 256 + tw * HDP + d + 4 * i), make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]));
+                __stcg(reinterpret_cast<float4*>(part + 256) + (d / 4 + i) * 128 + tw, make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]));
             } else {
 #pragma unroll
               for (int i = 0; i < 2; ++i)
@@ -964,7 +1001,7 @@ __global__ void __launch_bounds__(CTHREADS, 1) chunk_kernel(const __grid_constan
                 s.x += y.x, s.y += y.y, s.z += y.z, s.w += y.w;
               }
               if (part) {
-                __stcg(reinterpret_cast<float4*>(part + 256 + rr * HDP + dd), s);
+                __stcg(reinterpret_cast<float4*>(part + 256) + dd / 4 * 128 + rr, s);
               } else {
                 const int tk = rr / G;
                 *reinterpret_cast<uint2*>(static_cast<T*>(a.o) + ((size_t)p.row0 + tk) * a.o_stride +
@@ -1005,7 +1042,8 @@ __global__ void __launch_bounds__(CTHREADS, 1) chunk_kernel(const __grid_constan
         if (!(ok = wg_sync(wg, wph, lane, ab))) break;
         if (sh.last[slot]) {
           __threadfence();
-          join<T, HDP>(a, p.c0, p.np, p.kvh, p.row0 + tok0, slot, nrows, tw);
+          float* area = reinterpret_cast<float*>(csm + pad + (slot ? C::kJOff : C::kXOff));
+          if (!(ok = join<T, HDP>(a, p.c0, p.np, p.kvh, p.row0 + tok0, slot, nrows, tw, area, wg, wph, ab))) break;
         }
       }
       __syncwarp();
