@@ -73,8 +73,13 @@ struct ChunkArgs {
   int causal, window;
   int tpq;      // tokens of a slot: 128 / group
   int tpq_quad; // tokens of a quad tile: 32 / group (0: none)
+  unsigned inv_group;  // ceil(2^16 / group): r / group = r * inv_group >> 16 for r < 128
   float c;      // scale * log2(e)
+  int small_plan;  // few sequences and tiles: one warp plans
 };
+
+// Token of a slot's row r (0..127).
+__device__ __forceinline__ int token_of(const ChunkArgs& a, int r) { return (int)((unsigned)r * a.inv_group >> 16); }
 
 // What a CTA does at a time: key tiles [ja, jb) of one tile of work.
 struct Piece {
@@ -98,13 +103,14 @@ struct CCfg {
 };
 
 struct CMisc {
-  uint64_t full[8], empty[8], s_full[2], p_full[2][2], o_full[2], o_free[2], q_full, q_empty, x_full, wg[2], pq_full[QDEPTH], pq_empty[QDEPTH];
+  uint64_t full[8], empty[8], s_full[2], p_full[2][2], o_full[2], o_free[2], q_full, q_empty, x_full, pq_full[QDEPTH], pq_empty[QDEPTH];
   Piece pq[QDEPTH];
   float xm[128], xl[128];        // slot 1's statistics for slot 0 (split)
   float qm[4][32], ql[4][32];    // per quarter (quad)
   long long scan[CWARPS];
-  long long total, range0, range1, per;
+  long long range0, range1, per;
   int b0, t0, off0, kvh0;
+  int start0, ql0, kl0;          // sequence b0
   uint32_t tmem;
   int abort, last[2];
 };
@@ -139,12 +145,19 @@ __device__ __forceinline__ bool cwait(uint32_t bar, uint32_t parity, int* abort_
 // A value that is the same in every lane, as one the compiler knows to be.
 __device__ __forceinline__ int uniform(int x) { return (int)__reduce_max_sync(0xffffffffu, (unsigned)x); }
 
-// The four warps of a softmax group meet (a bounded bar.sync: false after an
-// abort, so no warp waits for one that gave up).
-__device__ __forceinline__ bool wg_sync(uint32_t bar, uint32_t& phase, int lane, int* abort_flag) {
-  __syncwarp();
-  if (lane == 0) mbar_arrive(bar);
-  return __all_sync(0xffffffffu, cwait(bar, phase++ & 1, abort_flag));
+// The four warps of a softmax group meet; with a vote, all learn whether all
+// are well.  A plain hardware barrier: a warp whose wait ran out goes on to
+// the end of its piece without waiting, so that nobody is left here, and the
+// group stops together at the vote that begins the next piece.
+__device__ __forceinline__ void wg_sync(int slot) { named_bar(1 + slot, 128); }
+__device__ __forceinline__ bool wg_all(int slot, bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.and.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)ok), "r"(1 + slot)
+      : "memory");
+  return r != 0;
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -231,75 +244,146 @@ __device__ __forceinline__ long long block_scan(long long v, long long* sums, lo
   return pre + x - v;
 }
 
-// The CTA's range of key tiles and where it begins (all threads).
+// Quotient of non-negative values, out of line (64-bit division is long).
+__device__ __noinline__ long long quotient(long long x, long long y) {
+  return (x | y) >> 32 ? x / y : (long long)((unsigned)x / (unsigned)y);
+}
+
+// The CTA's range of key tiles and where it begins (all threads).  Short
+// loops, not unrolled: every CTA runs this once, and what it costs is
+// instruction fetches and latencies.
 __device__ __noinline__ void plan(const ChunkArgs& a, int4* info, CMisc& sh) {
   const int tid = threadIdx.x, tp = 2 * a.tpq;
   const int per_s = (a.n_seqs + CTHREADS - 1) / CTHREADS;
   const int s0 = min(tid * per_s, a.n_seqs), s1 = min(s0 + per_s, a.n_seqs);
   long long mine = 0, total;
   bool bad = false;
+#pragma unroll 1
   for (int b = s0; b < s1; ++b) {
     const Seq s = seq_get(a, b);
     bad |= s.bad;
-    info[b] = make_int4((int)mine, s.ql, s.kl, 0);
+    info[b] = make_int4((int)mine, s.ql, s.kl, s.start);
     mine += (s.ql + tp - 1) / tp;
   }
   if (bad && blockIdx.x == 0 && a.status) atomicOr(a.status, kBadPos);
-  const long long pre_t = block_scan(mine, sh.scan, &total);
-  for (int b = s0; b < s1; ++b) info[b].x += (int)pre_t;  // the first tile of the sequence
+  const int before = (int)block_scan(mine, sh.scan, &total);
+#pragma unroll 1
+  for (int b = s0; b < s1; ++b) info[b].x += before;  // the first tile of the sequence
   __syncthreads();
   const int n_tiles = (int)total;
   const int per_t = (n_tiles + CTHREADS - 1) / CTHREADS;
   const int t0 = min(tid * per_t, n_tiles), t1 = min(t0 + per_t, n_tiles);
-  int b_first = 0;
-  if (t0 < t1) {  // the last sequence whose first tile is not behind t0
-    int lo = 0, hi = a.n_seqs;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (info[mid].x <= t0) lo = mid;
-      else hi = mid;
-    }
-    b_first = lo;
+  int lo = 0, hi = t0 < t1 ? a.n_seqs : 1;
+#pragma unroll 1
+  while (hi - lo > 1) {  // the last sequence whose first tile is not behind t0
+    const int mid = (lo + hi) >> 1;
+    if (info[mid].x <= t0) lo = mid;
+    else hi = mid;
   }
-  auto walk = [&](long long stop, int* bo, int* to) {  // steps of tiles t0..t1, or the tile that holds step `stop`
+  // first pass: the steps of tiles t0 .. t1 - 1; second: the tile that holds
+  // the range's first step, in the thread whose tiles do
+  long long pre = 0, stop = -1, r0 = 0, head = 0;
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
     long long sum = 0;
-    int b = b_first;
+    int b = lo;
+#pragma unroll 1
     for (int t = t0; t < t1; ++t) {
+#pragma unroll 1
       while (b + 1 < a.n_seqs && info[b + 1].x <= t) ++b;
       const int4 f = info[b];
       const int st = tile_of(a, f.y, f.z, t - f.x).steps;
       if (stop >= 0 && sum + st > stop) {
-        *bo = b;
-        *to = t - f.x;
-        return stop - sum;
+        sh.off0 = (int)(stop - sum);
+        sh.b0 = b;
+        sh.t0 = t - f.x;
+        sh.kvh0 = (int)head;
+        sh.start0 = f.w;
+        sh.ql0 = f.y;
+        sh.kl0 = f.z;
+        break;
       }
       sum += st;
     }
-    return sum;
-  };
-  mine = walk(-1, nullptr, nullptr);
-  const long long pre = block_scan(mine, sh.scan, &total);
-  const long long all = total * a.n_kv;
-  long long per = (all + gridDim.x - 1) / gridDim.x;
-  if (per < kMinSteps) per = kMinSteps;
-  const long long r0 = min(per * blockIdx.x, all), r1 = min(r0 + per, all);
-  if (tid == 0) {
-    sh.total = total;
-    sh.range0 = r0;
-    sh.range1 = r1;
-    sh.per = per;
-  }
-  if (r0 < r1) {
-    const long long at = r0 % total;
-    if (at >= pre && at < pre + mine) {
-      int b, t;
-      sh.off0 = (int)walk(at - pre, &b, &t);
-      sh.b0 = b;
-      sh.t0 = t;
-      sh.kvh0 = (int)(r0 / total);
+    if (pass) break;
+    pre = block_scan(sum, sh.scan, &total);
+    const long long all = total * a.n_kv, per = max(quotient(all + gridDim.x - 1, gridDim.x), (long long)kMinSteps);
+    r0 = min(per * blockIdx.x, all);
+    const long long r1 = min(r0 + per, all);
+    if (tid == 0) {
+      sh.range0 = r0;
+      sh.range1 = r1;
+      sh.per = per;
     }
+    if (r0 >= r1) break;  // (uniform)
+    head = quotient(r0, total);
+    const long long at = r0 - head * total;
+    if (at < pre || at >= pre + sum) break;  // another thread's
+    stop = at - pre;
   }
   __syncthreads();
+}
+
+// The same by one warp, without a barrier, for few sequences and tiles: the
+// other warps are at their posts meanwhile.  A lane takes consecutive
+// sequences.  Returns the range; where it begins goes to the last arguments.
+__device__ __forceinline__ void plan_warp(const ChunkArgs& a, int lane, long long& r0, long long& r1, long long& per, int& b0, int& t0,
+                                          int& off0, int& kvh0, Seq& seq0) {
+  const int per_s = (a.n_seqs + 31) / 32, tp = 2 * a.tpq;
+  const int s0 = min(lane * per_s, a.n_seqs), s1 = min(s0 + per_s, a.n_seqs);
+  unsigned pre = 0, total = 0, stop = 0;
+  bool seek = false;
+  int from = 0;
+  b0 = t0 = off0 = kvh0 = 0;
+  seq0 = {};
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+    unsigned sum = 0;
+    bool bad = false, found = false;
+#pragma unroll 1
+    for (int b = s0; b < s1 && !found; ++b) {
+      const Seq s = seq_get(a, b);
+      bad |= s.bad;
+#pragma unroll 1
+      for (int t = 0; t * tp < s.ql; ++t) {
+        const unsigned st = tile_of(a, s.ql, s.kl, t).steps;
+        if (seek && sum + st > stop) {
+          b0 = b, t0 = t, off0 = (int)(stop - sum), seq0 = s;
+          found = true;
+          break;
+        }
+        sum += st;
+      }
+    }
+    if (pass) break;
+    if (bad && blockIdx.x == 0 && a.status) atomicOr(a.status, kBadPos);
+    pre = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned y = __shfl_up_sync(0xffffffffu, pre, o);
+      if (lane >= o) pre += y;
+    }
+    total = __shfl_sync(0xffffffffu, pre, 31);
+    pre -= sum;
+    const long long all = (long long)total * a.n_kv;
+    per = max(quotient(all + gridDim.x - 1, gridDim.x), (long long)kMinSteps);
+    r0 = min(per * blockIdx.x, all);
+    r1 = min(r0 + per, all);
+    if (r0 >= r1) return;
+    kvh0 = (int)quotient(r0, total);
+    stop = (unsigned)(r0 - (long long)kvh0 * total);
+    seek = stop >= pre && stop - pre < sum;
+    stop -= pre;
+    from = __ffs(__ballot_sync(0xffffffffu, seek)) - 1;
+    if (!seek) break;
+  }
+  __syncwarp();
+  b0 = __shfl_sync(0xffffffffu, b0, from);
+  t0 = __shfl_sync(0xffffffffu, t0, from);
+  off0 = __shfl_sync(0xffffffffu, off0, from);
+  seq0.start = __shfl_sync(0xffffffffu, seq0.start, from);
+  seq0.ql = __shfl_sync(0xffffffffu, seq0.ql, from);
+  seq0.kl = __shfl_sync(0xffffffffu, seq0.kl, from);
 }
 
 // Key tiles of a slot inside a piece: first, first + stride, ... (count of them).
@@ -325,6 +409,16 @@ __device__ __forceinline__ Steps slot_steps(const ChunkArgs& a, const Piece& p, 
 
 // Order of a piece's n key tiles in the ring: pair K0 V0 K1 V1 ..., else K0 K1 V0 K2 V1 K3 V2 ...
 __device__ __forceinline__ int ring_v(int mode, int i, int n) { return mode == PAIR ? 2 * i + 1 : n == 1 ? 1 : 2 + i + min(i, n - 2); }
+struct RingUse {
+  int tile;
+  bool is_v;
+};
+__device__ __forceinline__ RingUse ring_use(int mode, int x, int n) {  // the inverse of ring_k and ring_v
+  if (mode == PAIR || n == 1) return {x >> 1, (x & 1) != 0};
+  if (x < 2) return {x, false};
+  if (x < 2 * n - 2) return {(x & 1) ? (x >> 1) + 1 : (x >> 1) - 1, !(x & 1)};
+  return {x - n, true};
+}
 __device__ __forceinline__ int ring_k(int mode, int i) { return mode == PAIR ? 2 * i : i < 2 ? i : 2 * i - 1; }
 
 // ---- the kernel ----------------------------------------------------------------------------
@@ -340,12 +434,11 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
-// Scores of keys key0 .. key0 + N - 1 outside the row's range become -inf.
-template <int N>
-__device__ __forceinline__ void mask_keys(uint32_t (&v)[N], int key0, const Row& row) {
+// Scores of keys key0 .. key0 + 31 outside the row's range become -inf.
+__device__ __forceinline__ void mask_keys(uint32_t (&v)[32], int key0, const Row& row) {
   const int lo = row.lo - key0, hi = row.hi - key0;
 #pragma unroll
-  for (int i = 0; i < N; ++i)
+  for (int i = 0; i < 32; ++i)
     if (i < lo || i >= hi) v[i] = 0xff800000u;
 }
 
@@ -406,10 +499,21 @@ __device__ __forceinline__ void weights32(const uint32_t (&v)[N], int at, f2_t c
 template <typename T>
 __device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, int key0, const Row& row, float c, bool first, int hd, float& R,
                                              float& l, uint32_t p_half, int lane) {
-  const bool ragged = __any_sync(0xffffffffu, row.ok && (key0 < row.lo || key0 + BK > row.hi));
+  if (__any_sync(0xffffffffu, row.ok && (key0 < row.lo || key0 + BK > row.hi))) {
+    // the masked columns are written back first, 32 at a time: tiles like this
+    // come once a piece or so, and 128 comparisons in line cost their fetches
+#pragma unroll 1
+    for (int d = 0; d < BK; d += 32) {
+      if (!__any_sync(0xffffffffu, row.ok && (key0 + d < row.lo || key0 + d + 32 > row.hi))) continue;
+      uint32_t w[32];
+      tmem_read(tS + d, w);
+      mask_keys(w, key0 + d, row);
+      tmem_write(tS + d, w);
+    }
+    tmem_wait_st();
+  }
   uint32_t v[128];
   tmem_read(tS, v);
-  if (ragged) mask_keys(v, key0, row);
   follow_max(max_of(v, -INFINITY) * c, row, first, tO, hd, R, l);
   const float nr = kShift - (R == -INFINITY ? 0.f : R);
   const f2_t c2 = pk2(c, c), r2 = pk2(nr, nr);
@@ -465,24 +569,39 @@ __device__ __forceinline__ float lse_of(float R, float l) {
 // the long loop has nothing but independent loads of O, which lie row by row
 // for four columns at a time: lanes read neighbours.
 template <typename T, int HDP>
-__device__ __noinline__ bool join(const ChunkArgs& a, int c0, int np, int kvh, int row0, int slot, int nrows, int tw, float* area,
-                                  uint32_t wg, uint32_t& wph, int* ab) {
+__device__ __noinline__ void join(const ChunkArgs& a, int c0, int np, int kvh, int row0, int slot, int nrows, int tw, float* area) {
   float *sw = area, *sl = area + kJoinCap;
   const bool fits = np * nrows <= kJoinCap;
-  const int lane = tw & 31, c8 = a.head_dim / 8;
+  const int c8 = a.head_dim / 8;
+  const bool few = nrows * c8 <= 128;  // a value or none per thread
+  float4 y0[8], y1[8];                 // then the first pieces' values are fetched along with the statistics
+  int few_r = 0, few_d = 0;
+  if (few) {
+    few_d = min(tw, nrows * c8 - 1) / nrows, few_r = min(tw, nrows * c8 - 1) - few_d * nrows;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float4* q = reinterpret_cast<const float4*>(partial_at<HDP>(a, c0 + min(i, np - 1), min(i, np - 1) == 0, slot) + 256) +
+                        2 * few_d * 128 + few_r;
+      y0[i] = __ldcg(q), y1[i] = __ldcg(q + 128);
+    }
+  }
+  const unsigned inv_rows = ((1u << 20) + nrows - 1) / nrows;  // x / nrows = x * inv_rows >> 20 for x < 2048 (nrows <= 128)
   if (fits) {
+#pragma unroll 2
     for (int x = tw; x < np * nrows; x += 128) {
-      const int i = x / nrows;
+      const int i = (int)((unsigned)x * inv_rows >> 20);
       const float* q = partial_at<HDP>(a, c0 + i, i == 0, slot) + (x - i * nrows);
       sw[x] = __ldcg(q);
       sl[x] = __ldcg(q + 128);
     }
-    if (!wg_sync(wg, wph, lane, ab)) return false;
+    wg_sync(slot);
   }
-  for (int r = tw; r < nrows; r += 128) {
-    if (!fits) break;
+  if (fits && tw < nrows) {
+    const int r = tw;
     float M = -INFINITY, L = 0.f;
+#pragma unroll 2
     for (int i = 0; i < np; ++i) M = fmaxf(M, sw[i * nrows + r]);
+#pragma unroll 2
     for (int i = 0; i < np; ++i) {
       const float w = weight(sw[i * nrows + r], M);
       L = fmaf(w, sl[i * nrows + r], L);
@@ -490,41 +609,92 @@ __device__ __noinline__ bool join(const ChunkArgs& a, int c0, int np, int kvh, i
     }
     sl[r] = L > 0.f ? 1.f / L : 0.f;
     if (a.lse) {
-      const int tok = r / a.group;
+      const int tok = token_of(a, r);
       a.lse[((size_t)row0 + tok) * (a.n_kv * a.group) + kvh * a.group + r - tok * a.group] = lse_of(M, L);
     }
   }
-  if (fits && !wg_sync(wg, wph, lane, ab)) return false;
-  for (int x = tw; x < nrows * c8; x += 128) {
-    const int d = x / nrows, r = x - d * nrows;
-    const int tok = r / a.group, head = kvh * a.group + r - tok * a.group;
-    const size_t t = (size_t)row0 + tok;
-    float M = -INFINITY, L = 0.f;
-    if (!fits)
-      for (int i = 0; i < np; ++i) M = fmaxf(M, __ldcg(partial_at<HDP>(a, c0 + i, i == 0, slot) + r));
-    float4 u = make_float4(0.f, 0.f, 0.f, 0.f), v = u;
-#pragma unroll 4
-    for (int i = 0; i < np; ++i) {
-      const float* q = partial_at<HDP>(a, c0 + i, i == 0, slot);
-      float w;
-      if (fits) {
-        w = sw[i * nrows + r];
-      } else {
-        w = weight(__ldcg(q + r), M);
-        L = fmaf(w, __ldcg(q + 128 + r), L);
-      }
-      const float4 y = __ldcg(reinterpret_cast<const float4*>(q + 256) + 2 * d * 128 + r);
-      const float4 z = __ldcg(reinterpret_cast<const float4*>(q + 256) + (2 * d + 1) * 128 + r);
-      u.x = fmaf(w, y.x, u.x), u.y = fmaf(w, y.y, u.y), u.z = fmaf(w, y.z, u.z), u.w = fmaf(w, y.w, u.w);
-      v.x = fmaf(w, z.x, v.x), v.y = fmaf(w, z.y, v.y), v.z = fmaf(w, z.z, v.z), v.w = fmaf(w, z.w, v.w);
-    }
-    const float inv = fits ? sl[r] : L > 0.f ? 1.f / L : 0.f;
-    *reinterpret_cast<uint4*>(static_cast<T*>(a.o) + t * a.o_stride + (size_t)head * a.head_dim + 8 * d) =
+  if (fits) wg_sync(slot);
+  auto put = [&](int r, int d, const float4& u, const float4& v, float inv) {
+    const int tok = token_of(a, r), head = kvh * a.group + r - tok * a.group;
+    *reinterpret_cast<uint4*>(static_cast<T*>(a.o) + ((size_t)row0 + tok) * a.o_stride + (size_t)head * a.head_dim + 8 * d) =
         make_uint4(Kind<T>::pack(u.x * inv, u.y * inv), Kind<T>::pack(u.z * inv, u.w * inv), Kind<T>::pack(v.x * inv, v.y * inv),
                    Kind<T>::pack(v.z * inv, v.w * inv));
-    if (!fits && a.lse && d == 0) a.lse[t * (a.n_kv * a.group) + head] = lse_of(M, L);
+  };
+  auto add = [](float4& u, float w, const float4& y) {
+    u.x = fmaf(w, y.x, u.x), u.y = fmaf(w, y.y, u.y), u.z = fmaf(w, y.z, u.z), u.w = fmaf(w, y.w, u.w);
+  };
+  const int total = nrows * c8;  // at most 2048
+  const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (!fits) {  // many pieces of many rows: statistics again for every value
+#pragma unroll 1
+    for (int x = tw; x < total; x += 128) {
+      const int d = x / nrows, r = x - d * nrows;
+      float M = -INFINITY, L = 0.f;
+#pragma unroll 4
+      for (int i = 0; i < np; ++i) M = fmaxf(M, __ldcg(partial_at<HDP>(a, c0 + i, i == 0, slot) + r));
+      float4 u = zero, v = zero;
+#pragma unroll 2
+      for (int i = 0; i < np; ++i) {
+        const float* q = partial_at<HDP>(a, c0 + i, i == 0, slot);
+        const float w = weight(__ldcg(q + r), M);
+        L = fmaf(w, __ldcg(q + 128 + r), L);
+        add(u, w, __ldcg(reinterpret_cast<const float4*>(q + 256) + 2 * d * 128 + r));
+        add(v, w, __ldcg(reinterpret_cast<const float4*>(q + 256) + (2 * d + 1) * 128 + r));
+      }
+      put(r, d, u, v, L > 0.f ? 1.f / L : 0.f);
+      if (a.lse && d == 0) {
+        const int tok = token_of(a, r);
+        a.lse[((size_t)row0 + tok) * (a.n_kv * a.group) + kvh * a.group + r - tok * a.group] = lse_of(M, L);
+      }
+    }
+    return;
   }
-  return true;
+  // the time is the latency of the loads: eight values of eight columns in
+  // flight (a thread's items are 128 apart), or four pieces of one
+  if (total > 128) {
+#pragma unroll 1
+    for (int x0 = tw; x0 < total; x0 += 128 * 8) {
+      int at[8];
+      float4 u[8], v[8];
+#pragma unroll
+      for (int y = 0; y < 8; ++y) {
+        const int x = min(x0 + 128 * y, total - 1), d = (int)((unsigned)x * inv_rows >> 20);
+        at[y] = 2 * d * 128 + x - d * nrows;  // (d, row)
+        u[y] = v[y] = zero;
+      }
+#pragma unroll 1
+      for (int i = 0; i < np; ++i) {
+        const float4* q = reinterpret_cast<const float4*>(partial_at<HDP>(a, c0 + i, i == 0, slot) + 256);
+#pragma unroll
+        for (int y = 0; y < 8; ++y) y0[y] = __ldcg(q + at[y]), y1[y] = __ldcg(q + at[y] + 128);
+#pragma unroll
+        for (int y = 0; y < 8; ++y) {
+          const float w = sw[i * nrows + (at[y] & 127)];
+          add(u[y], w, y0[y]);
+          add(v[y], w, y1[y]);
+        }
+      }
+#pragma unroll
+      for (int y = 0; y < 8; ++y)
+        if (x0 + 128 * y < total) put(at[y] & 127, at[y] >> 8, u[y], v[y], sl[at[y] & 127]);
+    }
+  } else if (tw < total) {
+    float4 u = zero, v = zero;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float w = i < np ? sw[i * nrows + few_r] : 0.f;
+      add(u, w, y0[i]);
+      add(v, w, y1[i]);
+    }
+#pragma unroll 4
+    for (int i = 8; i < np; ++i) {
+      const float4* q = reinterpret_cast<const float4*>(partial_at<HDP>(a, c0 + i, false, slot) + 256) + 2 * few_d * 128 + few_r;
+      const float w = sw[i * nrows + few_r];
+      add(u, w, __ldcg(q));
+      add(v, w, __ldcg(q + 128));
+    }
+    put(few_r, few_d, u, v, sl[few_r]);
+  }
 }
 
 template <typename T, int HDP>
@@ -542,7 +712,8 @@ __global__ void __launch_bounds__(CTHREADS, 1) chunk_kernel(const __grid_constan
   CMisc& sh = *reinterpret_cast<CMisc*>(csm + pad + C::kMiscOff);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-  if (tid == 0) {
+  // set up by warps 1 and 2 while the others begin on the plan
+  if (tid == 64) {
     for (int i = 0; i < NST; ++i) {
       mbar_init(smem_u32(&sh.full[i]), 1);
       mbar_init(smem_u32(&sh.empty[i]), 1);
@@ -557,28 +728,29 @@ __global__ void __launch_bounds__(CTHREADS, 1) chunk_kernel(const __grid_constan
     mbar_init(smem_u32(&sh.q_full), 1);
     mbar_init(smem_u32(&sh.q_empty), 1);
     mbar_init(smem_u32(&sh.x_full), 4);
-    mbar_init(smem_u32(&sh.wg[0]), 4);
-    mbar_init(smem_u32(&sh.wg[1]), 4);
     for (int i = 0; i < QDEPTH; ++i) {
       mbar_init(smem_u32(&sh.pq_full[i]), 1);
       mbar_init(smem_u32(&sh.pq_empty[i]), 10);
     }
     sh.abort = 0;
     mbar_fence_init();
+  }
+  if (tid == 96) {
     prefetch_tmap(&tm_q);
     prefetch_tmap(&tm_q4);
     prefetch_tmap(&tm_k);
     prefetch_tmap(&tm_v);
   }
-  plan(a, reinterpret_cast<int4*>(csm + pad), sh);
-  if (sh.range0 >= sh.range1) return;  // uniform: nothing is allocated yet
   if (warp == 1) {
     tmem_alloc(smem_u32(&sh.tmem), 512);
     tmem_relinquish();
   }
+  if (!a.small_plan) {
+    plan(a, reinterpret_cast<int4*>(csm + pad), sh);
+    // its scratch (generic proxy) is overwritten by TMA from here on
+    fence_async_smem();
+  }
   tc_fence_before();
-  // the plan's scratch (generic proxy) is overwritten by TMA from here on
-  fence_async_smem();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
@@ -640,18 +812,10 @@ __global__ void __launch_bounds__(CTHREADS, 1) chunk_kernel(const __grid_constan
           }
           ++u;
         };
-        if (p.mode == PAIR) {
-          for (int j = p.ja; ok && j < p.jb; ++j) {
-            tile(j, false);
-            if (ok) tile(j, true);
-          }
-        } else {
-          tile(p.ja, false);
-          if (ok && n > 1) tile(p.ja + 1, false);
-          for (int i = 0; ok && i < n; ++i) {
-            tile(p.ja + i, true);
-            if (ok && i + 2 < n) tile(p.ja + i + 2, false);
-          }
+#pragma unroll 1
+        for (int x = 0; ok && x < 2 * n; ++x) {
+          const RingUse r = ring_use(p.mode, x, n);
+          tile(p.ja + r.tile, r.is_v);
         }
       }
       // no copy may be in flight when the CTA ends
@@ -721,6 +885,7 @@ __global__ void __launch_bounds__(CTHREADS, 1) chunk_kernel(const __grid_constan
             if (f1 == 0 && c1) qk(1, qbase + C::kQ, u);
             release(u);
             if (n == 1) umma_commit_warp(smem_u32(&sh.q_empty));
+#pragma unroll 1
             for (int i = 0; i < n; ++i) {
               const int uv = u + 2 * i + 1, uk = uv + 1;
               const bool more = i + 1 < n;
@@ -746,12 +911,14 @@ __global__ void __launch_bounds__(CTHREADS, 1) chunk_kernel(const __grid_constan
             }
           } else {
             // two key tiles (one per slot) a turn
+#pragma unroll 1
             for (int i = 0; i < 2 && i < n; ++i) {
               if (!(ok = wait_full(u + i))) break;
               qk(i, qbase, u + i);
               release(u + i);
               if (i == n - 1) umma_commit_warp(smem_u32(&sh.q_empty));
             }
+#pragma unroll 1
             for (int i = 0; ok && i < n; ++i) {
               const int slot = i & 1, uv = u + ring_v(mode, i, n);
               if (!(ok = wait_full(uv))) break;
@@ -775,10 +942,16 @@ __global__ void __launch_bounds__(CTHREADS, 1) chunk_kernel(const __grid_constan
       __syncwarp();
     } else if (warp == 2) {
       // ---------------- the CTA's pieces
-      long long pos = sh.range0;
-      const long long end = sh.range1, per = sh.per;
-      int b = sh.b0, t = sh.t0, off = sh.off0, kvh = sh.kvh0;
-      Seq s = seq_get(a, b);
+      long long pos, end, per;
+      int b, t, off, kvh;
+      Seq s;
+      if (a.small_plan) {
+        plan_warp(a, lane, pos, end, per, b, t, off, kvh, s);
+      } else {
+        pos = sh.range0, end = sh.range1, per = sh.per;
+        b = sh.b0, t = sh.t0, off = sh.off0, kvh = sh.kvh0;
+        s.start = sh.start0, s.ql = sh.ql0, s.kl = sh.kl0;
+      }
       bool ok = true;
       int k = 0;
       for (;; ++k) {
@@ -800,14 +973,15 @@ __global__ void __launch_bounds__(CTHREADS, 1) chunk_kernel(const __grid_constan
           p.lo = x.lo;
           p.ja = x.j0 + off;
           p.jb = x.keys ? p.ja + take : p.ja;
-          p.c0 = (int)(p0 / per);
-          p.np = (int)((p0 + x.steps - 1) / per) - p.c0 + 1;
+          p.c0 = (int)quotient(p0, per);
+          p.np = (int)quotient(p0 + x.steps - 1, per) - p.c0 + 1;
           p.idx = (int)blockIdx.x - p.c0;
           pos += take;
           if (off + take == x.steps) {
             off = 0;
             if (++t * 2 * a.tpq >= s.ql && pos < end) {
               t = 0;
+#pragma unroll 1
               do {
                 if (++b == a.n_seqs) b = 0, ++kvh;
                 s = seq_get(a, b);
@@ -830,13 +1004,12 @@ __global__ void __launch_bounds__(CTHREADS, 1) chunk_kernel(const __grid_constan
     const uint32_t tl = (uint32_t)(quarter * 32) << 16;
     const uint32_t tS = tmem + tl + slot * 128, tO = tmem + tl + 256 + slot * HDP;
     const int hd = a.head_dim, G = a.group;
-    const uint32_t wg = smem_u32(&sh.wg[slot]);
-    uint32_t wph = 0;
     int u0 = 0, ns = 0, nx = 0;
     int no[2] = {0, 0};  // phases of o_full passed
     bool ok = true;
-    for (int k = 0; ok; ++k) {
-      if (!(ok = __all_sync(0xffffffffu, cwait(smem_u32(&sh.pq_full[k % QDEPTH]), (k / QDEPTH) & 1, ab)))) break;
+    for (int k = 0;; ++k) {
+      ok = ok && cwait(smem_u32(&sh.pq_full[k % QDEPTH]), (k / QDEPTH) & 1, ab);
+      if (!(ok = wg_all(slot, ok))) break;
       // read where it lies (registers are short here); handed back at the end of the piece
       const Piece& p = sh.pq[k % QDEPTH];
       if (p.mode == END) break;
@@ -846,7 +1019,7 @@ __global__ void __launch_bounds__(CTHREADS, 1) chunk_kernel(const __grid_constan
       const int r = p.mode == QUAD ? lane : tw;
       const int tok0 = p.mode == PAIR ? slot * a.tpq : 0;
       const int ntok = p.mode == PAIR ? min(p.n - tok0, a.tpq) : p.n;
-      const int tok = r / G, hg = r - tok * G;
+      const int tok = token_of(a, r), hg = r - tok * G;
       Row row;
       row.ok = tok < ntok;
       row.lo = 0;
@@ -859,7 +1032,7 @@ __global__ void __launch_bounds__(CTHREADS, 1) chunk_kernel(const __grid_constan
       float R = -INFINITY, l = 0.f;
       for (int i = 0; i < st.count; ++i) {
         const int j = st.first + i * st.stride;
-        if (!(ok = __all_sync(0xffffffffu, cwait(smem_u32(&sh.s_full[slot]), ns & 1, ab)))) break;
+        ok = __all_sync(0xffffffffu, ok && cwait(smem_u32(&sh.s_full[slot]), ns & 1, ab));
         ++ns;
         tc_fence_after();
         if ((j + 1) * BK > p.kl || j * BK < p.lo) {
@@ -868,7 +1041,7 @@ __global__ void __launch_bounds__(CTHREADS, 1) chunk_kernel(const __grid_constan
           // s_full: the MMA warp has then consumed the stage's previous
           // tile, so the barrier is at most one phase behind.)
           const int uv = u + ring_v(p.mode, j - p.ja, n);
-          if (!(ok = __all_sync(0xffffffffu, cwait(smem_u32(&sh.full[uv % NST]), (uv / NST) & 1, ab)))) break;
+          ok = __all_sync(0xffffffffu, ok && cwait(smem_u32(&sh.full[uv % NST]), (uv / NST) & 1, ab));
           const int key = j * BK + tw;
           if (key >= p.kl || key < p.lo) {
             const uint32_t v = kvbase + (uv % NST) * C::kKV + tw * 128;
@@ -887,9 +1060,8 @@ __global__ void __launch_bounds__(CTHREADS, 1) chunk_kernel(const __grid_constan
           hand_over(h1, lane);
         }
       }
-      if (!ok) break;
       if (st.count) {
-        if (!(ok = __all_sync(0xffffffffu, cwait(smem_u32(&sh.o_full[slot]), no[slot] & 1, ab)))) break;
+        ok = __all_sync(0xffffffffu, ok && cwait(smem_u32(&sh.o_full[slot]), no[slot] & 1, ab));
         ++no[slot];
       }
       const int nrows = ntok * G;
@@ -913,7 +1085,7 @@ __global__ void __launch_bounds__(CTHREADS, 1) chunk_kernel(const __grid_constan
           continue;
         }
         if (count1) {
-          if (!(ok = __all_sync(0xffffffffu, cwait(smem_u32(&sh.x_full), nx & 1, ab) && cwait(smem_u32(&sh.o_full[1]), no[1] & 1, ab)))) break;
+          ok = __all_sync(0xffffffffu, ok && cwait(smem_u32(&sh.x_full), nx & 1, ab) && cwait(smem_u32(&sh.o_full[1]), no[1] & 1, ab));
           ++nx;
           use1 = true;
           const float R1 = sh.xm[tw], l1 = sh.xl[tw], M = fmaxf(R, R1);
@@ -931,36 +1103,55 @@ __global__ void __launch_bounds__(CTHREADS, 1) chunk_kernel(const __grid_constan
         if (!part) inv = l > 0.f ? 1.f / l : 0.f;
         w0 *= inv;
         w1 *= inv;
-        T* out = static_cast<T*>(a.o) + t * a.o_stride + (size_t)head * hd;
-        for (int d = 0; d < hd; d += 16) {
-          uint32_t v[16] = {}, w[16] = {};
-          if (use0) tmem_read(tO + d, v);
-          if (use1) tmem_read(tO1 + d, w);
-          float f[16];
+        // 64 bytes of each row at a time through shared memory, so that a store
+        // covers 8 rows x 64 bytes (a lane storing its own row: 32 rows x 16,
+        // 32 cycles a store); partials lie column by column and need none
+        const uint32_t stage = qbase + (slot ? C::kJOff : C::kXOff) + quarter * 2048;
+#pragma unroll 1
+        for (int d = 0; d < hd; d += 32) {
+          float f[32];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            f[i] = use0 ? __uint_as_float(v[i]) * w0 : 0.f;
-            if (use1) f[i] = fmaf(__uint_as_float(w[i]), w1, f[i]);
-          }
-          if (row.ok) {
-            if (part) {
+          for (int h = 0; h < 2; ++h) {
+            uint32_t v[16] = {}, w[16] = {};
+            if (use0) tmem_read(tO + d + 16 * h, v);  // (a column past head_dim is allocated, and not stored)
+            if (use1) tmem_read(tO1 + d + 16 * h, w);
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                __stcg(reinterpret_cast<float4*>(part + 256) + (d / 4 + i) * 128 + tw, make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]));
-            } else {
-#pragma unroll
-              for (int i = 0; i < 2; ++i)
-                *reinterpret_cast<uint4*>(out + d + 8 * i) =
-                    make_uint4(Kind<T>::pack(f[8 * i], f[8 * i + 1]), Kind<T>::pack(f[8 * i + 2], f[8 * i + 3]),
-                               Kind<T>::pack(f[8 * i + 4], f[8 * i + 5]), Kind<T>::pack(f[8 * i + 6], f[8 * i + 7]));
+            for (int i = 0; i < 16; ++i) {
+              f[16 * h + i] = use0 ? __uint_as_float(v[i]) * w0 : 0.f;
+              if (use1) f[16 * h + i] = fmaf(__uint_as_float(w[i]), w1, f[16 * h + i]);
             }
+          }
+          if (part) {
+            if (row.ok)
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                if (d + 4 * i < hd)
+                  __stcg(reinterpret_cast<float4*>(part + 256) + (d / 4 + i) * 128 + tw,
+                         make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]));
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              sts128(stage + lane * 64 + ((i ^ (lane >> 1 & 3)) << 4),
+                     make_uint4(Kind<T>::pack(f[8 * i], f[8 * i + 1]), Kind<T>::pack(f[8 * i + 2], f[8 * i + 3]),
+                                Kind<T>::pack(f[8 * i + 4], f[8 * i + 5]), Kind<T>::pack(f[8 * i + 6], f[8 * i + 7])));
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int x = 8 * i + (lane >> 2), ch = lane & 3, rr = quarter * 32 + x;  // row of the warp, 16-byte chunk
+              const uint4 y = lds128(stage + x * 64 + ((ch ^ (x >> 1 & 3)) << 4));
+              const int tk = token_of(a, rr);
+              if (tk < ntok && d + 8 * ch < hd)
+                *reinterpret_cast<uint4*>(static_cast<T*>(a.o) + ((size_t)p.row0 + tok0 + tk) * a.o_stride +
+                                          (size_t)(p.kvh * G + rr - tk * G) * hd + d + 8 * ch) = y;
+            }
+            __syncwarp();
           }
         }
       } else {
         // join the quarters, 32 output columns at a time
         sh.qm[quarter][lane] = R;
         sh.ql[quarter][lane] = l;
-        if (!(ok = wg_sync(wg, wph, lane, ab))) break;
+        wg_sync(slot);
         float M = -INFINITY, L = 0.f;
 #pragma unroll
         for (int q = 0; q < 4; ++q) M = fmaxf(M, sh.qm[q][lane]);
@@ -972,47 +1163,52 @@ __global__ void __launch_bounds__(CTHREADS, 1) chunk_kernel(const __grid_constan
         w1 *= f;
         R = M;
         l = L;
-        float4* const X = reinterpret_cast<float4*>(csm + pad + C::kXOff);  // [quarter][row][8], chunk ^ (row & 7)
-        for (int d = 0; ok && d < hd; d += 32) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
+        // [quarter][row][chunk of 4 columns], chunk ^ (row & 7); as many columns a turn as the rows leave room for
+        float4* const X = reinterpret_cast<float4*>(csm + pad + C::kXOff);
+        const int rs = nrows <= 8 ? 3 : nrows <= 16 ? 4 : 5, cs = 8 - rs;  // log2 of rows and chunks a quarter holds
+#pragma unroll 1
+        for (int d = 0; d < hd; d += 4 << cs) {
+          const int cols = min(4 << cs, hd - d);
+#pragma unroll 1
+          for (int h = 0; h < cols; h += 16) {
             uint32_t v[16] = {}, w[16] = {};
-            if (use0) tmem_read(tO + d + 16 * h, v);
-            if (use1) tmem_read(tO1 + d + 16 * h, w);
-            float g[16];
+            if (use0) tmem_read(tO + d + h, v);
+            if (use1) tmem_read(tO1 + d + h, w);
+            if (row.ok) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              g[i] = use0 ? __uint_as_float(v[i]) * w0 : 0.f;
-              if (use1) g[i] = fmaf(__uint_as_float(w[i]), w1, g[i]);
+              for (int i = 0; i < 4; ++i) {
+                float g[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  g[e] = use0 ? __uint_as_float(v[4 * i + e]) * w0 : 0.f;
+                  if (use1) g[e] = fmaf(__uint_as_float(w[4 * i + e]), w1, g[e]);
+                }
+                X[(((quarter << rs) + lane) << cs) + ((h / 4 + i) ^ (lane & 7))] = make_float4(g[0], g[1], g[2], g[3]);
+              }
             }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              X[(quarter * 32 + lane) * 8 + ((4 * h + i) ^ (lane & 7))] = make_float4(g[4 * i], g[4 * i + 1], g[4 * i + 2], g[4 * i + 3]);
           }
-          if (!(ok = wg_sync(wg, wph, lane, ab))) break;
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int rr = (tw + 128 * i) >> 3, ch = tw & 7, dd = d + 4 * ch;
-            if (rr < nrows && dd < hd) {
-              float4 s = X[rr * 8 + (ch ^ (rr & 7))];
+          wg_sync(slot);
+          for (int x = tw; x < nrows << cs; x += 128) {
+            const int rr = x >> cs, ch = x & ((1 << cs) - 1), dd = d + 4 * ch;
+            if (dd < hd) {
+              float4 s = X[(rr << cs) + (ch ^ (rr & 7))];
 #pragma unroll
               for (int q = 1; q < 4; ++q) {
-                const float4 y = X[(q * 32 + rr) * 8 + (ch ^ (rr & 7))];
+                const float4 y = X[(((q << rs) + rr) << cs) + (ch ^ (rr & 7))];
                 s.x += y.x, s.y += y.y, s.z += y.z, s.w += y.w;
               }
               if (part) {
                 __stcg(reinterpret_cast<float4*>(part + 256) + dd / 4 * 128 + rr, s);
               } else {
-                const int tk = rr / G;
+                const int tk = token_of(a, rr);
                 *reinterpret_cast<uint2*>(static_cast<T*>(a.o) + ((size_t)p.row0 + tk) * a.o_stride +
                                           (size_t)(p.kvh * G + rr - tk * G) * hd + dd) =
                     make_uint2(Kind<T>::pack(s.x, s.y), Kind<T>::pack(s.z, s.w));
               }
             }
           }
-          ok = wg_sync(wg, wph, lane, ab);
+          wg_sync(slot);
         }
-        if (!ok) break;
       }
       // O is read: the next piece may overwrite it
       tc_fence_before();
@@ -1031,19 +1227,20 @@ __global__ void __launch_bounds__(CTHREADS, 1) chunk_kernel(const __grid_constan
       }
       if (part) {
         // the last piece of the tile to arrive joins them all
-        __threadfence();
-        if (!(ok = wg_sync(wg, wph, lane, ab))) break;
+        // (one thread's acquire-release orders the group's accesses: the group meets around it)
+        wg_sync(slot);
         if (tw == 0) {
           int* cnt = a.counters + p.c0 * 2 + slot;
-          const bool last = atomicAdd(cnt, 1) == p.np - 1;
+          int seen;
+          asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(seen) : "l"(cnt) : "memory");
+          const bool last = seen == p.np - 1;
           if (last) *cnt = 0;  // ready for the next call
           sh.last[slot] = last;
         }
-        if (!(ok = wg_sync(wg, wph, lane, ab))) break;
+        wg_sync(slot);
         if (sh.last[slot]) {
-          __threadfence();
           float* area = reinterpret_cast<float*>(csm + pad + (slot ? C::kJOff : C::kXOff));
-          if (!(ok = join<T, HDP>(a, p.c0, p.np, p.kvh, p.row0 + tok0, slot, nrows, tw, area, wg, wph, ab))) break;
+          join<T, HDP>(a, p.c0, p.np, p.kvh, p.row0 + tok0, slot, nrows, tw, area);
         }
       }
       __syncwarp();
@@ -1144,8 +1341,10 @@ extern "C" int dls_attention_chunk(const dls_attention_chunk_desc* d, void* cuda
   a.page_shift = pt == 16 ? 4 : pt == 32 ? 5 : pt == 64 ? 6 : pt == 128 ? 7 : 8;
   a.n_pages = d->n_pages, a.max_pages = d->max_pages, a.pool_rows = d->n_pages * d->n_kv_heads * pt;
   a.causal = d->causal, a.window = d->window;
-  a.tpq = 128 / a.group, a.tpq_quad = 32 / a.group;
+  a.tpq = 128 / a.group, a.tpq_quad = 32 / a.group, a.inv_group = (65536 + a.group - 1) / a.group;
   a.c = (d->scale > 0.f ? d->scale : 1.0f / sqrtf((float)hd)) * 1.4426950408889634f;
+  // a lane of the planning warp walks at most 4 sequences and 8 more tiles; its sums fit 32 bits
+  a.small_plan = d->n_seqs <= 128 && d->n_tokens <= 8 * 2 * a.tpq && (long long)d->max_pages * pt <= 1 << 24;
   const CUtensorMapDataType dt = d->kv_type == DLS_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const uint32_t pr = pt < BK ? pt : BK;
   CUtensorMap tq, tq4, tk, tv;
