@@ -434,11 +434,12 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
-// Scores of keys key0 .. key0 + 31 outside the row's range become -inf.
-__device__ __forceinline__ void mask_keys(uint32_t (&v)[32], int key0, const Row& row) {
+// Scores of keys key0 .. key0 + N - 1 outside the row's range become -inf.
+template <int N>
+__device__ __forceinline__ void mask_keys(uint32_t (&v)[N], int key0, const Row& row) {
   const int lo = row.lo - key0, hi = row.hi - key0;
 #pragma unroll
-  for (int i = 0; i < 32; ++i)
+  for (int i = 0; i < N; ++i)
     if (i < lo || i >= hi) v[i] = 0xff800000u;
 }
 
@@ -458,7 +459,7 @@ __device__ __forceinline__ float max_of(const uint32_t (&v)[N], float m) {
 // over.
 __device__ __forceinline__ void follow_max(float mc, const Row& row, bool first, uint32_t tO, int hd, float& R, float& l) {
   const bool grow = mc > R + kGrow;  // R = -inf before the row's first key
-  if (!first && __any_sync(0xffffffffu, grow && row.ok)) {
+  if (__builtin_expect(!first && __any_sync(0xffffffffu, grow && row.ok), 0)) {
     const float f = grow ? ex2(R - mc) : 1.f;
     l *= f;
 #pragma unroll 1
@@ -499,21 +500,10 @@ __device__ __forceinline__ void weights32(const uint32_t (&v)[N], int at, f2_t c
 template <typename T>
 __device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, int key0, const Row& row, float c, bool first, int hd, float& R,
                                              float& l, uint32_t p_half, int lane) {
-  if (__any_sync(0xffffffffu, row.ok && (key0 < row.lo || key0 + BK > row.hi))) {
-    // the masked columns are written back first, 32 at a time: tiles like this
-    // come once a piece or so, and 128 comparisons in line cost their fetches
-#pragma unroll 1
-    for (int d = 0; d < BK; d += 32) {
-      if (!__any_sync(0xffffffffu, row.ok && (key0 + d < row.lo || key0 + d + 32 > row.hi))) continue;
-      uint32_t w[32];
-      tmem_read(tS + d, w);
-      mask_keys(w, key0 + d, row);
-      tmem_write(tS + d, w);
-    }
-    tmem_wait_st();
-  }
+  const bool ragged = __any_sync(0xffffffffu, row.ok && (key0 < row.lo || key0 + BK > row.hi));
   uint32_t v[128];
   tmem_read(tS, v);
+  if (__builtin_expect(ragged, 0)) mask_keys(v, key0, row);
   follow_max(max_of(v, -INFINITY) * c, row, first, tO, hd, R, l);
   const float nr = kShift - (R == -INFINITY ? 0.f : R);
   const f2_t c2 = pk2(c, c), r2 = pk2(nr, nr);
@@ -1035,7 +1025,7 @@ __global__ void __launch_bounds__(CTHREADS, 1) chunk_kernel(const __grid_constan
         ok = __all_sync(0xffffffffu, ok && cwait(smem_u32(&sh.s_full[slot]), ns & 1, ab));
         ++ns;
         tc_fence_after();
-        if ((j + 1) * BK > p.kl || j * BK < p.lo) {
+        if (__builtin_expect((j + 1) * BK > p.kl || j * BK < p.lo, 0)) {
           // rows of V that no query may see can hold anything: 0 * NaN would
           // reach every row through the product.  (This wait comes after
           // s_full: the MMA warp has then consumed the stage's previous
