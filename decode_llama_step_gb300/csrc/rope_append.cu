@@ -16,8 +16,16 @@
 // pairing one holds the partners of the other, in the adjacent pairing each
 // holds its own), so nothing is exchanged but the sum of squares, loads and
 // stores are contiguous over a head's lanes, and in-place calls are safe.  A
-// warp stays on one token and walks its heads, so the eight sincospi of a
-// lane serve every head of the walk.
+// warp stays on one token and walks its heads, one pass fetched ahead, so a
+// token's cos and sin serve every head of the walk; the lanes that hold the
+// same pairs of different heads share the work of them.
+// Measured: 8192 bf16 tokens of 72 heads of 128, normed and turned, 57.7 us
+// (5.2 TB/s; 44.5 at the copy rate); an append of 7600 tokens with q, k and v
+// in bf16 50.9 us (4.7 TB/s).  Without any arithmetic the same walk takes as
+// long: what is left is the walk's thousands of streams, one a warp.  A CTA
+// that walks four tokens together reaches 49 us as a bare copy, but 67 with
+// the norm, whose exchanges then stand in the way; two passes fetched ahead
+// cost the warps that they gain.
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -49,7 +57,7 @@ struct RopeArgs {
   int page_shift, n_pages, max_pages, n_kv;
   int lanes_log2;        // lanes of a head (power of two >= head_dim / 16)
   int heads_total, passes, per_warp, chunks;  // head passes of a token, passes of a warp, warps of a token
-  float eps;
+  float eps, inv_hd;
   unsigned long long turn[kMaxPairs];
 };
 
@@ -144,8 +152,8 @@ __device__ __noinline__ void check_lengths(const RopeArgs& a, int lane) {
   if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(a.status, kBadPos);
 }
 
-template <typename IN, typename OUT>
-__global__ void __launch_bounds__(RTHREADS) rope_kernel(const __grid_constant__ RopeArgs a) {
+template <typename IN, typename OUT, bool HALVES>
+__global__ void __launch_bounds__(RTHREADS, sizeof(IN) == 4 ? 5 : 6) rope_kernel(const __grid_constant__ RopeArgs a) {
   const int lane = threadIdx.x & 31;
   const unsigned w = blockIdx.x * (RTHREADS / 32) + (threadIdx.x >> 5);
   const int t = (int)(w / (unsigned)a.chunks), part = (int)(w - (unsigned)t * a.chunks);
@@ -207,18 +215,29 @@ __global__ void __launch_bounds__(RTHREADS) rope_kernel(const __grid_constant__ 
   // cos and sin of the lane's eight pairs (elements e, e of the two vectors
   // in the halves pairing; 2e, 2e + 1 of each vector in the adjacent one)
   float cs[8], sn[8];
-  if (rot) {
+  auto turned = [&](int e, float* sine, float* cosine) {
+    const int pair = HALVES ? 8 * c + e : (e < 4 ? 4 * c + e : (a.rot_dim >> 2) + 4 * c + e - 4);
+    const unsigned long long f = (unsigned long long)(long long)pos * a.turn[pair & (kMaxPairs - 1)];
+    sincospif((float)(int)(f >> 32) * 4.656612873077393e-10f, sine, cosine);  // 2^-31: half turns
+  };
+  if (a.lanes_log2 <= 3) {
+    // four lanes at least hold the same pairs of different heads: each works out two of the eight
+    float s0, s1, c0, c1;
+    turned(sub & 3, &s0, &c0);
+    turned((sub & 3) + 4, &s1, &c1);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int pair = a.pairing == DLS_ROPE_HALVES ? 8 * c + e : (e < 4 ? 4 * c + e : (a.rot_dim >> 2) + 4 * c + e - 4);
-      const unsigned long long f = (unsigned long long)(long long)pos * a.turn[pair];
-      const float half_turns = (float)(int)(f >> 32) * 4.656612873077393e-10f;  // 2^-31
-      sincospif(half_turns, &sn[e], &cs[e]);
+    for (int e = 0; e < 4; ++e) {
+      const int src = (e << a.lanes_log2) + c;
+      sn[e] = __shfl_sync(0xffffffffu, s0, src);
+      cs[e] = __shfl_sync(0xffffffffu, c0, src);
+      sn[e + 4] = __shfl_sync(0xffffffffu, s1, src);
+      cs[e + 4] = __shfl_sync(0xffffffffu, c1, src);
     }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) turned(e, &sn[e], &cs[e]);
   }
 
-  int kind = -2;
-  float wa[8], wb[8];
   for (int pass = pass0; pass < pass1; ++pass) {
     const Item next = item(pass + 1);
     Vec8<IN> na, nb;
@@ -235,17 +254,19 @@ __global__ void __launch_bounds__(RTHREADS) rope_kernel(const __grid_constant__ 
     if (it.kind >= 0) {
       const RopeSrc& s = a.src[it.kind];
       if (s.norm) {
-        if (kind != it.kind) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) wa[e] = s.norm[ea + e], wb[e] = s.norm[eb + e];
-          kind = it.kind;
-        }
-        const float r = rsqrtf(ss / (float)a.head_dim + a.eps);
+        // the weights come from L1 each time: kept, they cost a fifth of the warps
+        Vec8<float> na8, nb8;
+        na8.load(s.norm + ea);
+        nb8.load(s.norm + eb);
+        float wa[8], wb[8];
+        na8.get(wa);
+        nb8.get(wb);
+        const float r = rsqrtf(ss * a.inv_hd + a.eps);
 #pragma unroll
         for (int e = 0; e < 8; ++e) xa[e] *= r * wa[e], xb[e] *= r * wb[e];
       }
       if (rot && s.rotate) {
-        if (a.pairing == DLS_ROPE_HALVES) {
+        if (HALVES) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const float x = xa[e], y = xb[e];
@@ -283,12 +304,18 @@ __global__ void __launch_bounds__(RTHREADS) rope_kernel(const __grid_constant__ 
   }
 }
 
+template <typename IN, typename OUT>
+void launch_rope_out(const RopeArgs& a, unsigned grid, cudaStream_t s) {
+  if (a.pairing == DLS_ROPE_HALVES) rope_kernel<IN, OUT, true><<<grid, RTHREADS, 0, s>>>(a);
+  else rope_kernel<IN, OUT, false><<<grid, RTHREADS, 0, s>>>(a);
+}
+
 template <typename IN>
 cudaError_t launch_rope_in(const RopeArgs& a, int out_type, unsigned grid, cudaStream_t s) {
   switch (out_type) {
-    case DLS_F32: rope_kernel<IN, float><<<grid, RTHREADS, 0, s>>>(a); break;
-    case DLS_F16: rope_kernel<IN, __half><<<grid, RTHREADS, 0, s>>>(a); break;
-    default: rope_kernel<IN, __nv_bfloat16><<<grid, RTHREADS, 0, s>>>(a); break;
+    case DLS_F32: launch_rope_out<IN, float>(a, grid, s); break;
+    case DLS_F16: launch_rope_out<IN, __half>(a, grid, s); break;
+    default: launch_rope_out<IN, __nv_bfloat16>(a, grid, s); break;
   }
   return cudaGetLastError();
 }
@@ -314,14 +341,19 @@ bool set_turns(RopeArgs* a, const double* inv_freq) {
 int launch_rope(RopeArgs& a, int in_type, int out_type, const char* what, cudaStream_t s) {
   a.lanes_log2 = 0;
   while ((16 << a.lanes_log2) < a.head_dim) ++a.lanes_log2;
+  a.inv_hd = 1.0f / (float)a.head_dim;
   a.heads_total = a.src[0].heads + a.src[1].heads + a.src[2].heads;
   const int hpw = 32 >> a.lanes_log2;
   a.passes = (a.heads_total + hpw - 1) / hpw;
-  // passes of a warp: as many as keep 32 warps on each of the SMs in flight, at most all of a token's
-  const long long total = (long long)a.n_tokens * a.passes;
-  const long long want = total / (152 * 32);
+  // Passes of a warp: few enough for three rounds of the 24 warps an SM holds.
+  // 8192 bf16 tokens of 72 heads of 128: 57.7 us with 2 warps a token (9
+  // passes each), 59.9 with one (18; the last round a quarter full), 59.5 and
+  // 66.5 with 3 and 4 (each repeats the token's start); 46.6 for a plain copy
+  // of the bytes.
+  const long long want = (long long)a.n_tokens * a.passes / (152 * 24 * 3);
   a.per_warp = (int)(want < 1 ? 1 : want > a.passes ? a.passes : want);
   a.chunks = (a.passes + a.per_warp - 1) / a.per_warp;
+  a.per_warp = (a.passes + a.chunks - 1) / a.chunks;
   const long long warps = (long long)a.n_tokens * a.chunks;
   const long long grid = (warps + RTHREADS / 32 - 1) / (RTHREADS / 32);
   if (warps > 0x7fffffff - RTHREADS) return report_error(DLS_ERR_ARG, "%s: n_tokens=%d heads=%d are too many", what, a.n_tokens, a.heads_total);
