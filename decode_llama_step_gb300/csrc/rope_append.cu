@@ -333,7 +333,7 @@ bool set_turns(RopeArgs* a, const double* inv_freq) {
     if (!isfinite(inv_freq[i])) return false;
     double turns = inv_freq[i] / 6.283185307179586476925286766559;
     turns -= floor(turns);
-    a->turn[i] = turns >= 1.0 ? 0ull : (unsigned long long)ldexp(turns, 64);
+    a->turn[i] = turns >= 1.0 ? 0ull : (unsigned long long)(turns * 18446744073709551616.0);  // 2^64
   }
   return true;
 }

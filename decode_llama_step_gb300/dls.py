@@ -213,81 +213,98 @@ ROPE_PAIRINGS = {"adjacent": 0, "halves": 1}
 _QK_NORM_ROPE = struct.Struct("@4P4q4P8if")
 _KV_APPEND = struct.Struct("@6P4q2P5P12if")
 _ATTENTION_CHUNK = struct.Struct("@8PPQP2q11if")
+_torch = None
 _dtypes = {}
 
 
+def _types():
+    """torch's types by the header's numbers; torch is imported with the first call."""
+    global _torch
+    import torch
+
+    _torch = torch
+    _dtypes.update({torch.float32: DLS_F32, torch.float16: DLS_F16, torch.bfloat16: DLS_BF16})
+    return _dtypes
+
+
 def _dtype(t, name):
-    if not _dtypes:
-        import torch
-
-        _dtypes.update({torch.float32: DLS_F32, torch.float16: DLS_F16, torch.bfloat16: DLS_BF16})
-    try:
-        return _dtypes[t.dtype]
-    except KeyError:
-        raise ValueError(f"{name}: type {t.dtype} (float32, float16 or bfloat16)") from None
+    typ = (_dtypes or _types()).get(t.dtype)
+    if typ is None:
+        raise ValueError(f"{name}: type {t.dtype} (float32, float16 or bfloat16)")
+    return typ
 
 
-def _rows(t, name, n=None, heads=None, hd=None, typ=None):
-    """(pointer, elements between tokens) of a [tokens, heads, head_dim] tensor whose rows are contiguous."""
-    if t.dim() != 3:
-        raise ValueError(f"{name}: shape {tuple(t.shape)} ([tokens, heads, head_dim])")
+def _rows(t, name, n, heads, hd, dtype, device):
+    """(pointer, elements between tokens) of a [n, heads, hd] tensor whose rows are contiguous.  These checks run
+    before every launch, which itself takes a few microseconds: few calls into torch, and no strings before an error."""
     shape, stride = t.shape, t.stride()
-    if (n is not None and shape[0] != n) or (heads is not None and shape[1] != heads) or (hd is not None and shape[2] != hd):
-        raise ValueError(f"{name}: shape {tuple(shape)}, wanted {(n, heads, hd)}")
-    if typ is not None and _dtype(t, name) != typ:
-        raise ValueError(f"{name}: type {t.dtype}")
-    row = shape[1] * shape[2]
-    if (stride[2] != 1 and shape[2] > 1) or (stride[1] != shape[2] and shape[1] > 1):
+    if shape != (n, heads, hd):
+        raise ValueError(f"{name}: shape {tuple(shape)}, wanted {(n, heads, hd)} ([tokens, heads, head_dim])")
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: type {t.dtype}, wanted {dtype}")
+    if (stride[2] != 1 and hd > 1) or (stride[1] != hd and heads > 1):
         raise ValueError(f"{name}: a token's heads must be contiguous (strides {stride})")
-    return t.data_ptr(), (stride[0] if shape[0] > 1 else row)
+    if t.get_device() != device:
+        raise ValueError(f"{name}: on {t.device}: all tensors must be on one CUDA device")
+    return t.data_ptr(), (stride[0] if n > 1 else heads * hd)
 
 
-def _array(t, name, typ, shape):
-    """Pointer of a contiguous tensor of the given type (its name) and shape; None -> 0."""
+def _array(t, name, dtype, shape, device):
+    """Pointer of a contiguous tensor of the given type and shape; None -> 0."""
     if t is None:
         return 0
-    if str(t.dtype) != typ or tuple(t.shape) != shape or not t.is_contiguous():
-        raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)}, wanted contiguous {typ} {shape}")
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)}, wanted contiguous {dtype} {shape}")
+    if t.get_device() != device:
+        raise ValueError(f"{name}: on {t.device}: all tensors must be on one CUDA device")
     return t.data_ptr()
 
 
-def _call(fn, desc, stream, *tensors):
-    """One library call on the tensors' own device (all on one)."""
-    import torch
+def _dims(t, name):
+    shape = t.shape
+    if len(shape) != 3:
+        raise ValueError(f"{name}: shape {tuple(shape)} ([tokens, heads, head_dim])")
+    return shape
 
-    device = tensors[0].get_device()
-    for t in tensors:
-        if t is not None and (t.get_device() != device or not t.is_cuda):
-            raise ValueError("all tensors must be on one CUDA device")
-    if torch.cuda.current_device() == device:
+
+def _call(fn, desc, stream, device):
+    """One library call on the tensors' own device."""
+    if device < 0:
+        raise ValueError("all tensors must be on one CUDA device")
+    if _torch.cuda.current_device() == device:
         _check(fn(desc, _stream_handle(stream)))
     else:
-        with torch.cuda.device(device):
+        with _torch.cuda.device(device):
             _check(fn(desc, _stream_handle(stream)))
 
 
 def _inv_freq(inv_freq):
+    """(array to keep, pointer, rot_dim) of host frequencies."""
     if inv_freq is None:
         return None, 0, 0
     a = np.ascontiguousarray(inv_freq, dtype=np.float64)
     if a.ndim != 1:
         raise ValueError(f"inv_freq: shape {a.shape} ([rot_dim / 2])")
-    return a, a.ctypes.data, 2 * a.size
+    return a, a.__array_interface__["data"][0], 2 * a.size
 
 
-def _pools(k_pages, v_pages, page_table, cu_q, kv_len):
-    """Shapes of the cache and the batch: (pages, KV heads, page tokens, head_dim, table pointer, entries of a
-    sequence, cu_q and kv_len pointers, sequences)."""
-    if k_pages.dim() != 4 or k_pages.shape != v_pages.shape or k_pages.dtype != v_pages.dtype:
+def _pools(k_pages, v_pages, page_table, cu_q, kv_len, device):
+    """Shapes and pointers of the cache and the batch: (pages, KV heads, page tokens, head_dim, k and v pointers, table
+    pointer, entries of a sequence, cu_q and kv_len pointers, sequences)."""
+    shape = k_pages.shape
+    if len(shape) != 4 or v_pages.shape != shape or k_pages.dtype != v_pages.dtype:
         raise ValueError(f"k_pages {tuple(k_pages.shape)} {k_pages.dtype}, v_pages {tuple(v_pages.shape)} {v_pages.dtype}: "
                          "one [pages, kv_heads, page_tokens, head_dim] and type wanted")
     if not k_pages.is_contiguous() or not v_pages.is_contiguous():
         raise ValueError("k_pages and v_pages must be contiguous")
+    if k_pages.get_device() != device or v_pages.get_device() != device:
+        raise ValueError(f"k_pages on {k_pages.device}, v_pages on {v_pages.device}: all tensors must be on one CUDA device")
     if page_table.dim() != 2:
         raise ValueError(f"page_table: shape {tuple(page_table.shape)} ([sequences, pages])")
     n, most = page_table.shape
-    return (*k_pages.shape, _array(page_table, "page_table", "torch.int32", (n, most)), most,
-            _array(cu_q, "cu_q", "torch.int32", (n + 1,)), _array(kv_len, "kv_len", "torch.int32", (n,)), n)
+    i32_ = _torch.int32
+    return (*shape, k_pages.data_ptr(), v_pages.data_ptr(), _array(page_table, "page_table", i32_, (n, most), device), most,
+            _array(cu_q, "cu_q", i32_, (n + 1,), device), _array(kv_len, "kv_len", i32_, (n,), device), n)
 
 
 def rope_inv_freq(rot_dim: int, theta: float) -> np.ndarray:
@@ -300,27 +317,27 @@ def qk_norm_rope(q, k, positions, inv_freq, q_out, k_out, *, q_norm=None, k_norm
     """Per-head RMSNorm (where a norm is given) and rotation of q and k [tokens, heads, head_dim] into q_out and
     k_out, which may be q and k themselves.  Either pair may be None.  positions: device int32 [tokens]; inv_freq:
     host float64 [rot_dim / 2], or None for no rotation."""
-    one = q if q is not None else k
+    one, one_out = (q, q_out) if q is not None else (k, k_out)
     if one is None or (q is None) != (q_out is None) or (k is None) != (k_out is None):
         raise ValueError("q with q_out, k with k_out, or both")
-    n, _, hd = one.shape if one.dim() == 3 else (0, 0, 0)
-    typ = _dtype(one, "q")
-    out = _dtype(q_out if q is not None else k_out, "q_out")
+    n, _, hd = _dims(one, "q" if q is not None else "k")
+    typ, out, device = _dtype(one, "q"), _dtype(one_out, "q_out"), one.get_device()
+    tin, tout, f32 = one.dtype, one_out.dtype, _torch.float32
     qp = qs = qop = qos = qh = kp = ks = kop = kos = kh = 0
     if q is not None:
-        qh = q.shape[1] if q.dim() == 3 else 0
-        qp, qs = _rows(q, "q")
-        qop, qos = _rows(q_out, "q_out", n, qh, hd, out)
+        qh = q.shape[1]
+        qp, qs = _rows(q, "q", n, qh, hd, tin, device)
+        qop, qos = _rows(q_out, "q_out", n, qh, hd, tout, device)
     if k is not None:
-        kh = k.shape[1] if k.dim() == 3 else 0
-        kp, ks = _rows(k, "k", n, None, hd, typ)
-        kop, kos = _rows(k_out, "k_out", n, kh, hd, out)
+        kh = _dims(k, "k")[1]
+        kp, ks = _rows(k, "k", n, kh, hd, tin, device)
+        kop, kos = _rows(k_out, "k_out", n, kh, hd, tout, device)
     keep, fp, rot = _inv_freq(inv_freq)
-    desc = _QK_NORM_ROPE.pack(qp, kp, qop, kop, qs, ks, qos, kos, _array(q_norm, "q_norm", "torch.float32", (hd,)),
-                              _array(k_norm, "k_norm", "torch.float32", (hd,)),
-                              _array(positions, "positions", "torch.int32", (n,)), fp, n, qh, kh, hd, rot,
+    desc = _QK_NORM_ROPE.pack(qp, kp, qop, kop, qs, ks, qos, kos, _array(q_norm, "q_norm", f32, (hd,), device),
+                              _array(k_norm, "k_norm", f32, (hd,), device),
+                              _array(positions, "positions", _torch.int32, (n,), device), fp, n, qh, kh, hd, rot,
                               ROPE_PAIRINGS[pairing], typ, out, eps)
-    _call(load().dls_qk_norm_rope, desc, stream, one, q_out, k, k_out, q_norm, k_norm, positions)
+    _call((_lib or load()).dls_qk_norm_rope, desc, stream, device)
 
 
 def kv_append(k, v, k_pages, v_pages, page_table, cu_q, kv_len, inv_freq, *, q=None, q_out=None, q_norm=None, k_norm=None,
@@ -328,26 +345,24 @@ def kv_append(k, v, k_pages, v_pages, page_table, cu_q, kv_len, inv_freq, *, q=N
     """Append a ragged chunk's keys (normed where k_norm is given, rotated by their cache position) and values
     [tokens, kv_heads, head_dim] to the pages; with q, q_out = q normed and rotated in the same pass, in the
     cache's type.  cu_q: device int32 [sequences + 1], kv_len: device int32 [sequences], the new tokens counted."""
-    pages, kvh, pt, hd, table, most, cu, kl, seqs = _pools(k_pages, v_pages, page_table, cu_q, kv_len)
     if (q is None) != (q_out is None):
         raise ValueError("q with q_out, or neither")
-    typ, kv_type = _dtype(k, "k"), _dtype(k_pages, "k_pages")
-    kp, ks = _rows(k, "k", None, kvh, hd)
-    n = k.shape[0]
-    vptr, vs = _rows(v, "v", n, kvh, hd, typ)
+    typ, kv_type, device = _dtype(k, "k"), _dtype(k_pages, "k_pages"), k.get_device()
+    pages, kvh, pt, hd, kpp, vpp, table, most, cu, kl, seqs = _pools(k_pages, v_pages, page_table, cu_q, kv_len, device)
+    n, tin, f32 = _dims(k, "k")[0], k.dtype, _torch.float32
+    kp, ks = _rows(k, "k", n, kvh, hd, tin, device)
+    vptr, vs = _rows(v, "v", n, kvh, hd, tin, device)
     qp = qs = qop = qos = qh = 0
     if q is not None:
-        qp, qs = _rows(q, "q", n, None, hd, typ)
-        qh = q.shape[1]
-        qop, qos = _rows(q_out, "q_out", n, qh, hd, kv_type)
+        qh = _dims(q, "q")[1]
+        qp, qs = _rows(q, "q", n, qh, hd, tin, device)
+        qop, qos = _rows(q_out, "q_out", n, qh, hd, k_pages.dtype, device)
     keep, fp, rot = _inv_freq(inv_freq)
-    desc = _KV_APPEND.pack(kp, vptr, qp, k_pages.data_ptr(), v_pages.data_ptr(), qop, ks, vs, qs, qos,
-                           _array(k_norm, "k_norm", "torch.float32", (hd,)),
-                           _array(q_norm, "q_norm", "torch.float32", (hd,)), table, cu, kl, fp,
-                           _array(status, "status", "torch.int32", (1,)), n, seqs, qh, kvh, hd, rot,
+    desc = _KV_APPEND.pack(kp, vptr, qp, kpp, vpp, qop, ks, vs, qs, qos, _array(k_norm, "k_norm", f32, (hd,), device),
+                           _array(q_norm, "q_norm", f32, (hd,), device), table, cu, kl, fp,
+                           _array(status, "status", _torch.int32, (1,), device), n, seqs, qh, kvh, hd, rot,
                            ROPE_PAIRINGS[pairing], typ, kv_type, pt, pages, most, eps)
-    _call(load().dls_kv_append, desc, stream, k, v, k_pages, v_pages, page_table, cu_q, kv_len, q, q_out, q_norm, k_norm,
-          status)
+    _call((_lib or load()).dls_kv_append, desc, stream, device)
 
 
 def attention_chunk_workspace_bytes(head_dim: int) -> int:
@@ -359,19 +374,18 @@ def attention_chunk(q, k_pages, v_pages, page_table, cu_q, kv_len, o, workspace,
     """Attention of ragged chunks of new tokens (q, o [tokens, heads, head_dim] in the cache's type) over the paged
     cache.  workspace: a uint8 tensor of attention_chunk_workspace_bytes(head_dim) zeros, kept from call to call.
     lse: fp32 [tokens, heads] or None.  scale 0: 1 / sqrt(head_dim)."""
-    pages, kvh, pt, hd, table, most, cu, kl, seqs = _pools(k_pages, v_pages, page_table, cu_q, kv_len)
-    kv_type = _dtype(k_pages, "k_pages")
-    qp, qs = _rows(q, "q", None, None, hd, kv_type)
-    n, heads, _ = q.shape
-    op, os_ = _rows(o, "o", n, heads, hd, kv_type)
-    if not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
-    desc = _ATTENTION_CHUNK.pack(qp, k_pages.data_ptr(), v_pages.data_ptr(), table, cu, kl, op,
-                                 _array(lse, "lse", "torch.float32", (n, heads)), workspace.data_ptr(),
-                                 workspace.numel() * workspace.element_size(),
-                                 _array(status, "status", "torch.int32", (1,)), qs, os_, n, seqs, heads, kvh, hd, pt, pages,
-                                 most, kv_type, int(bool(causal)), window, scale)
-    _call(load().dls_attention_chunk, desc, stream, q, k_pages, v_pages, page_table, cu_q, kv_len, o, workspace, lse, status)
+    kv_type, device = _dtype(k_pages, "k_pages"), q.get_device()
+    pages, kvh, pt, hd, kpp, vpp, table, most, cu, kl, seqs = _pools(k_pages, v_pages, page_table, cu_q, kv_len, device)
+    n, heads, _ = _dims(q, "q")
+    qp, qs = _rows(q, "q", n, heads, hd, k_pages.dtype, device)
+    op, os_ = _rows(o, "o", n, heads, hd, k_pages.dtype, device)
+    if not workspace.is_contiguous() or workspace.get_device() != device:
+        raise ValueError(f"workspace: on {workspace.device}: contiguous, and all tensors on one CUDA device")
+    desc = _ATTENTION_CHUNK.pack(qp, kpp, vpp, table, cu, kl, op, _array(lse, "lse", _torch.float32, (n, heads), device),
+                                 workspace.data_ptr(), workspace.nbytes,
+                                 _array(status, "status", _torch.int32, (1,), device), qs, os_, n, seqs, heads, kvh, hd, pt,
+                                 pages, most, kv_type, 1 if causal else 0, window, scale)
+    _call((_lib or load()).dls_attention_chunk, desc, stream, device)
 
 
 DLS_Q4_K = 12
