@@ -23,8 +23,8 @@
 // single token's softmax is spread over all eight warps.
 //
 // Work is divided by key tiles, not by sequences: the key tiles of all
-// (KV head, sequence, token tile) in a row are cut into one equal range per
-// CTA, whatever the mix of prompts and single tokens; a tile cut by a range
+// (KV head, sequence, token tile) in a row, each tile of work led by what it
+// costs besides (kTileCost), are cut into one equal range per CTA, whatever the mix of prompts and single tokens; a tile cut by a range
 // border leaves partial (R, l, O) in the workspace and the last CTA to arrive
 // joins them in range order.  Each CTA finds its range itself from the
 // device-side lengths, so a call is one launch and a captured graph follows
@@ -50,7 +50,8 @@ constexpr int MAXC = 152;        // CTAs at most (one per SM)
 constexpr int CTHREADS = 384;
 constexpr int CWARPS = CTHREADS / 32;
 constexpr int QDEPTH = 4;        // pieces the list runs ahead
-constexpr int kMinSteps = 2;     // key tiles of a range at least (one per slot of a split tile)
+constexpr int kMinSteps = 2;     // units of a range at least (a key tile per slot of a split tile)
+constexpr int kTileCost = 3;     // what a tile of work costs beyond its key tiles, in key tiles
 constexpr float kGrow = 8.f;     // log2 the maximum may exceed the reference by
 constexpr float kShift = 7.f;    // weights are kept as 2^(c s - R + 7): at most 2^15 in fp16, with 7 more binades below
 constexpr uint64_t kWaitNsC = 2000000000ull;
@@ -206,7 +207,7 @@ __device__ __forceinline__ Seq seq_get(const ChunkArgs& a, int b) {
 }
 
 struct Tile {
-  int mode, n, pos0, lo, j0, keys, steps;  // keys: key tiles to do; steps: its weight in the division (at least 1)
+  int mode, n, pos0, lo, j0, keys, units;  // keys: key tiles to do; units: kTileCost and the key tiles (one at least)
 };
 
 __device__ __forceinline__ Tile tile_of(const ChunkArgs& a, int ql, int kl, int t) {
@@ -219,7 +220,7 @@ __device__ __forceinline__ Tile tile_of(const ChunkArgs& a, int ql, int kl, int 
   x.lo = a.window && x.pos0 >= a.window ? min(x.pos0 - a.window + 1, hi) : 0;
   x.j0 = x.lo / BK;
   x.keys = hi > x.lo ? (hi + BK - 1) / BK - x.j0 : 0;
-  x.steps = max(x.keys, 1);
+  x.units = kTileCost + max(x.keys, 1);
   return x;
 }
 
@@ -292,7 +293,7 @@ __device__ __noinline__ void plan(const ChunkArgs& a, int4* info, CMisc& sh) {
 #pragma unroll 1
       while (b + 1 < a.n_seqs && info[b + 1].x <= t) ++b;
       const int4 f = info[b];
-      const int st = tile_of(a, f.y, f.z, t - f.x).steps;
+      const int st = tile_of(a, f.y, f.z, t - f.x).units;
       if (stop >= 0 && sum + st > stop) {
         sh.off0 = (int)(stop - sum);
         sh.b0 = b;
@@ -346,7 +347,7 @@ __device__ __forceinline__ void plan_warp(const ChunkArgs& a, int lane, long lon
       bad |= s.bad;
 #pragma unroll 1
       for (int t = 0; t * tp < s.ql; ++t) {
-        const unsigned st = tile_of(a, s.ql, s.kl, t).steps;
+        const unsigned st = tile_of(a, s.ql, s.kl, t).units;
         if (seek && sum + st > stop) {
           b0 = b, t0 = t, off0 = (int)(stop - sum), seq0 = s;
           found = true;
@@ -944,30 +945,32 @@ __global__ void __launch_bounds__(CTHREADS, 1) chunk_kernel(const __grid_constan
       }
       bool ok = true;
       int k = 0;
-      for (;; ++k) {
-        if (k >= QDEPTH && !(ok = __all_sync(0xffffffffu, cwait(smem_u32(&sh.pq_empty[k % QDEPTH]), ((k / QDEPTH) - 1) & 1, ab)))) break;
+      for (;;) {
         Piece p;
-        if (pos >= end) {
-          p.mode = END;
-        } else {
+        p.mode = END;
+        while (pos < end) {
           const Tile x = tile_of(a, s.ql, s.kl, t);
-          const int take = (int)min((long long)(x.steps - off), end - pos);
-          const long long p0 = pos - off;
-          p.mode = x.mode;
-          p.b = b;
-          p.kvh = kvh;
-          p.row0 = s.start + t * 2 * a.tpq;
-          p.n = x.n;
-          p.pos0 = x.pos0;
-          p.kl = s.kl;
-          p.lo = x.lo;
-          p.ja = x.j0 + off;
-          p.jb = x.keys ? p.ja + take : p.ja;
-          p.c0 = (int)quotient(p0, per);
-          p.np = (int)quotient(p0 + x.steps - 1, per) - p.c0 + 1;
-          p.idx = (int)blockIdx.x - p.c0;
+          const int take = (int)min((long long)(x.units - off), end - pos);
+          const int u0 = max(off - kTileCost, 0), u1 = off + take - kTileCost;  // key tiles of it here
+          const long long first = pos - off + kTileCost;                       // position of the tile's first key tile
+          if (u1 > u0) {
+            p.mode = x.mode;
+            p.b = b;
+            p.kvh = kvh;
+            p.row0 = s.start + t * 2 * a.tpq;
+            p.n = x.n;
+            p.pos0 = x.pos0;
+            p.kl = s.kl;
+            p.lo = x.lo;
+            p.ja = x.j0 + u0;
+            p.jb = x.keys ? x.j0 + u1 : p.ja;
+            p.c0 = (int)quotient(first, per);
+            p.np = (int)quotient(first + (x.units - kTileCost) - 1, per) - p.c0 + 1;
+            p.idx = (int)blockIdx.x - p.c0;
+          }
           pos += take;
-          if (off + take == x.steps) {
+          off += take;
+          if (off == x.units) {
             off = 0;
             if (++t * 2 * a.tpq >= s.ql && pos < end) {
               t = 0;
@@ -978,12 +981,15 @@ __global__ void __launch_bounds__(CTHREADS, 1) chunk_kernel(const __grid_constan
               } while (s.ql == 0);
             }
           }
+          if (u1 > u0) break;
         }
+        if (k >= QDEPTH && !(ok = __all_sync(0xffffffffu, cwait(smem_u32(&sh.pq_empty[k % QDEPTH]), ((k / QDEPTH) - 1) & 1, ab)))) break;
         if (lane == 0) {
           sh.pq[k % QDEPTH] = p;
           mbar_arrive(smem_u32(&sh.pq_full[k % QDEPTH]));
         }
         __syncwarp();
+        ++k;
         if (p.mode == END) break;
       }
     }
