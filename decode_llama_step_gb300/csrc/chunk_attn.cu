@@ -1103,8 +1103,44 @@ __global__ void __launch_bounds__(CTHREADS, 1) chunk_kernel(const __grid_constan
         // covers 8 rows x 64 bytes (a lane storing its own row: 32 rows x 16,
         // 32 cycles a store); partials lie column by column and need none
         const uint32_t stage = qbase + (slot ? C::kJOff : C::kXOff) + quarter * 2048;
+        // the four rows that this lane stores a 16-byte chunk of, and where
+        T* to[4];
+        bool mine[4];
+        const int ch = lane & 3;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int rr = quarter * 32 + 8 * i + (lane >> 2), tk = token_of(a, rr);
+          mine[i] = tk < ntok;
+          to[i] = static_cast<T*>(a.o) + ((size_t)p.row0 + tok0 + tk) * a.o_stride + (size_t)(p.kvh * G + rr - tk * G) * hd + 8 * ch;
+        }
+        const uint32_t put = stage + lane * 64, get = stage + (lane >> 2) * 64;
+        const int swz = lane >> 1 & 3;                 // of the row lane and, for every i, of row 8 i + lane / 4: (lane >> 3 & 3)
+        const uint32_t got = get + ((ch ^ (lane >> 3 & 3)) << 4);
 #pragma unroll 1
         for (int d = 0; d < hd; d += 32) {
+          if (use0 && !use1 && !part) {  // the common case: one slot's whole tile
+            uint32_t v[32];
+            tmem_read(tO + d, v);
+            const f2_t w2 = pk2(w0, w0), none = pk2(-0.f, -0.f);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t y[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float2 g = upk2(ffma2(pk2(__uint_as_float(v[8 * i + 2 * e]), __uint_as_float(v[8 * i + 2 * e + 1])), w2, none));
+                y[e] = Kind<T>::pack(g.x, g.y);
+              }
+              sts128(put + ((i ^ swz) << 4), make_uint4(y[0], y[1], y[2], y[3]));
+            }
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint4 y = lds128(got + i * 512);
+              if (mine[i] && d + 8 * ch < hd) *reinterpret_cast<uint4*>(to[i] + d) = y;
+            }
+            __syncwarp();
+            continue;
+          }
           float f[32];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
@@ -1127,18 +1163,14 @@ __global__ void __launch_bounds__(CTHREADS, 1) chunk_kernel(const __grid_constan
           } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              sts128(stage + lane * 64 + ((i ^ (lane >> 1 & 3)) << 4),
+              sts128(put + ((i ^ swz) << 4),
                      make_uint4(Kind<T>::pack(f[8 * i], f[8 * i + 1]), Kind<T>::pack(f[8 * i + 2], f[8 * i + 3]),
                                 Kind<T>::pack(f[8 * i + 4], f[8 * i + 5]), Kind<T>::pack(f[8 * i + 6], f[8 * i + 7])));
             __syncwarp();
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const int x = 8 * i + (lane >> 2), ch = lane & 3, rr = quarter * 32 + x;  // row of the warp, 16-byte chunk
-              const uint4 y = lds128(stage + x * 64 + ((ch ^ (x >> 1 & 3)) << 4));
-              const int tk = token_of(a, rr);
-              if (tk < ntok && d + 8 * ch < hd)
-                *reinterpret_cast<uint4*>(static_cast<T*>(a.o) + ((size_t)p.row0 + tok0 + tk) * a.o_stride +
-                                          (size_t)(p.kvh * G + rr - tk * G) * hd + d + 8 * ch) = y;
+              const uint4 y = lds128(got + i * 512);
+              if (mine[i] && d + 8 * ch < hd) *reinterpret_cast<uint4*>(to[i] + d) = y;
             }
             __syncwarp();
           }
