@@ -840,10 +840,17 @@ __global__ void __launch_bounds__(CTHREADS, 1) chunk_kernel(const __grid_constan
         umma_commit_warp(smem_u32(&sh.s_full[slot]));
       };
       // the weights arrive in two halves (64 keys each); the first product of
-      // a piece waits until the piece before has read the slot's O
-      auto pv = [&](int slot, int phase, int u, bool first, int k) {
+      // a piece waits until the slot's last O has been read (of: a bit per
+      // slot whether there is one, and the parity of their number four bits
+      // up.  Only pieces with products of the slot have a phase of o_free: a
+      // slot without keys waits for nothing, and its warps may be pieces ahead)
+      uint32_t of = 0;
+      auto pv = [&](int slot, int phase, int u, bool first) {
         if (!wait(sh.p_full[slot][0], phase)) return false;
-        if (first && k > 0 && !wait(sh.o_free[slot], k - 1)) return false;
+        if (first) {
+          if ((of >> slot & 1) && !wait(sh.o_free[slot], 1 ^ (of >> (4 + slot) & 1))) return false;
+          of = (of | 1u << slot) ^ 16u << slot;
+        }
         tc_fence_after();
         const uint32_t vt = kvbase + (u % NST) * C::kKV, tp = tmem + slot * 128 + kPCol, to = tmem + 256 + slot * HDP;
         const uint64_t vd = umma_desc_mn128(vt, BK * 128, 1024);
@@ -882,7 +889,7 @@ __global__ void __launch_bounds__(CTHREADS, 1) chunk_kernel(const __grid_constan
               const bool more = i + 1 < n;
               if (!(ok = wait_full(uv))) break;
               if (i >= f0 && i < e0) {
-                if (!(ok = pv(0, np0++, uv, i == f0, k))) break;
+                if (!(ok = pv(0, np0++, uv, i == f0))) break;
                 if (i + 1 == e0) umma_commit_warp(smem_u32(&sh.o_full[0]));
               }
               if (more) {
@@ -890,7 +897,7 @@ __global__ void __launch_bounds__(CTHREADS, 1) chunk_kernel(const __grid_constan
                 if (i + 1 >= f0 && i + 1 < e0) qk(0, qbase, uk);
               }
               if (i >= f1 && i < e1) {
-                if (!(ok = pv(1, np1++, uv, i == f1, k))) break;
+                if (!(ok = pv(1, np1++, uv, i == f1))) break;
                 if (i + 1 == e1) umma_commit_warp(smem_u32(&sh.o_full[1]));
               }
               release(uv);
@@ -913,7 +920,7 @@ __global__ void __launch_bounds__(CTHREADS, 1) chunk_kernel(const __grid_constan
             for (int i = 0; ok && i < n; ++i) {
               const int slot = i & 1, uv = u + ring_v(mode, i, n);
               if (!(ok = wait_full(uv))) break;
-              if (!(ok = pv(slot, slot ? np1++ : np0++, uv, i < 2, k))) break;
+              if (!(ok = pv(slot, slot ? np1++ : np0++, uv, i < 2))) break;
               release(uv);
               if (i + 2 >= n) umma_commit_warp(smem_u32(&sh.o_full[slot]));
               if (i + 2 < n) {
@@ -926,9 +933,6 @@ __global__ void __launch_bounds__(CTHREADS, 1) chunk_kernel(const __grid_constan
             }
           }
         }
-        // every phase of o_free is passed, in order
-        if (ok && k > 0 && c0 == 0) ok = wait(sh.o_free[0], k - 1);
-        if (ok && k > 0 && c1 == 0) ok = wait(sh.o_free[1], k - 1);
       }
       __syncwarp();
     } else if (warp == 2) {
@@ -1242,8 +1246,8 @@ __global__ void __launch_bounds__(CTHREADS, 1) chunk_kernel(const __grid_constan
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(smem_u32(&sh.o_free[slot]));
-        if (p.mode != PAIR) mbar_arrive(smem_u32(&sh.o_free[1]));
+        if (use0) mbar_arrive(smem_u32(&sh.o_free[slot]));
+        if (use1) mbar_arrive(smem_u32(&sh.o_free[1]));
       }
       if (row.ok && (p.mode != QUAD || quarter == 0)) {
         if (part) {

@@ -378,6 +378,14 @@ def test_attention_chunk_rows_without_keys(gpu_lib):
     check_attend([(5, 3), (4, 0), (1, 1)], 4, 2, 128, 32, "f16", causal=False)
 
 
+@pytest.mark.parametrize("hd,window", [(64, 0), (128, 2)])
+def test_attention_chunk_runs_of_rows_without_keys(gpu_lib, hd, window):
+    """Many tiles in a row without any key, or with keys for one half of their rows only, between ordinary ones: the
+    warps that have nothing to wait for must not get ahead of those that have."""
+    lengths = ([(2, 0)] * 5 + [(5, 40), (1, 1), (0, 7), (3, 0)] * 2 + [(140, 60), (7, 0), (200, 30)]) * 16
+    check_attend(lengths, 2, 2, hd, 16, "f16", window=window)
+
+
 def test_attention_chunk_every_key(gpu_lib):
     check_attend([(5, 700), (130, 257), (300, 40), (1, 1)], 8, 4, 128, 64, "bf16", causal=False)
     check_attend([(64, 64)] * 3, 3, 3, 64, 16, "f16", causal=False)
