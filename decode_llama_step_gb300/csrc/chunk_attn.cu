@@ -96,15 +96,21 @@ struct CCfg {
   static constexpr int KA = HDP / 64;        // 64-wide swizzle atoms along the head dimension
   static constexpr int kQ = 128 * HDP * 2;   // one slot's Q
   static constexpr int kKV = BK * HDP * 2;   // one K or V tile
-  static constexpr int NST = HDP == 128 ? 4 : 8;
+  // Stages of 32 KB: a K or a V tile, or both of a narrow head's key tile.
+  // There one barrier serves both: the MMA warp's waits (about 100 cycles
+  // each) are then as long as its products.
+  static constexpr bool kTogether = HDP == 64;
+  static constexpr int kUses = kTogether ? 1 : 2;  // ring uses of a key tile
+  static constexpr int kStage = kTogether ? 2 * kKV : kKV;
+  static constexpr int NST = 4;
   static constexpr int kKVOff = 2 * kQ;
-  static constexpr int kXOff = kKVOff + NST * kKV;  // float [4][32][32]: joins the quarters of a quad tile
+  static constexpr int kXOff = kKVOff + NST * kStage;  // float [4][32][32]: joins the quarters of a quad tile
   static constexpr int kJOff = kXOff + 4 * 32 * 32 * 4;  // statistics being joined: slot 0's in X, slot 1's here
   static constexpr int kMiscOff = kJOff + 2 * kJoinCap * 4;
 };
 
 struct CMisc {
-  uint64_t full[8], empty[8], s_full[2], p_full[2][2], o_full[2], o_free[2], q_full, q_empty, x_full, pq_full[QDEPTH], pq_empty[QDEPTH];
+  uint64_t full[4], empty[4], s_full[2], p_full[2][2], o_full[2], o_free[2], q_full, q_empty, x_full, pq_full[QDEPTH], pq_empty[QDEPTH];
   Piece pq[QDEPTH];
   float xm[128], xl[128];        // slot 1's statistics for slot 0 (split)
   float qm[4][32], ql[4][32];    // per quarter (quad)
@@ -782,14 +788,18 @@ __global__ void __launch_bounds__(CTHREADS, 1) chunk_kernel(const __grid_constan
         ++nq;
         q_out = true;
         const int32_t* table = a.page_table + (size_t)p.b * a.max_pages;
+        // ring use: key tile j's K, its V, or both
         auto tile = [&](int j, bool is_v) {
           const int s = u % NST;
           if (u >= NST && !(ok = __all_sync(0xffffffffu, cwait(smem_u32(&sh.empty[s]), ((u / NST) - 1) & 1, ab)))) return;
-          const uint32_t bar = smem_u32(&sh.full[s]), dst = kvbase + s * C::kKV;
-          if (lane == 0) mbar_expect_tx(bar, C::kKV);
+          const uint32_t bar = smem_u32(&sh.full[s]);
+          uint32_t dst = kvbase + s * C::kStage;
+          if (lane == 0) mbar_expect_tx(bar, C::kStage);
           __syncwarp();
-          if (lane < npc * C::KA) {
-            const int x = lane / C::KA, at = lane % C::KA;
+          constexpr int kPer = C::kTogether ? 2 : C::KA;  // copies of a page's piece: K and V, or the halves of a row
+          if (lane < npc * kPer) {
+            const int x = lane / kPer, which = lane % kPer, at = C::kTogether ? 0 : which;
+            if (C::kTogether) is_v = which, dst += which * C::kKV;
             const int key = j * BK + x * pr;
             int y = a.pool_rows;  // past the end of the pool: the copy fills zeros
             if (key < p.kl && key + pr > p.lo) {
@@ -804,8 +814,8 @@ __global__ void __launch_bounds__(CTHREADS, 1) chunk_kernel(const __grid_constan
           ++u;
         };
 #pragma unroll 1
-        for (int x = 0; ok && x < 2 * n; ++x) {
-          const RingUse r = ring_use(p.mode, x, n);
+        for (int x = 0; ok && x < C::kUses * n; ++x) {
+          const RingUse r = C::kTogether ? RingUse{x, false} : ring_use(p.mode, x, n);
           tile(p.ja + r.tile, r.is_v);
         }
       }
@@ -819,6 +829,7 @@ __global__ void __launch_bounds__(CTHREADS, 1) chunk_kernel(const __grid_constan
       const uint32_t id_s = umma_idesc_f16(128, BK) | Kind<T>::kIdesc;
       const uint32_t id_o = umma_idesc_f16_bmn(128, a.head_dim) | Kind<T>::kIdesc;
       const int ksteps = a.head_dim / 16;
+      constexpr bool T2 = C::kTogether;
       int u0 = 0, nq = 0;        // ring position of the piece, Q tiles seen
       int np0 = 0, np1 = 0;      // weights consumed, per slot
       bool ok = true;
@@ -826,7 +837,7 @@ __global__ void __launch_bounds__(CTHREADS, 1) chunk_kernel(const __grid_constan
       auto wait_full = [&](int u) { return wait(sh.full[u % NST], u / NST); };
       auto release = [&](int u) { umma_commit_warp(smem_u32(&sh.empty[u % NST])); };
       auto qk = [&](int slot, uint32_t q, int u) {
-        const uint32_t kt = kvbase + (u % NST) * C::kKV;
+        const uint32_t kt = kvbase + (u % NST) * C::kStage;
         tc_fence_after();
         const uint64_t qd = umma_desc_k128(q), kd = umma_desc_k128(kt);
         int ks = 0;
@@ -852,7 +863,7 @@ __global__ void __launch_bounds__(CTHREADS, 1) chunk_kernel(const __grid_constan
           of = (of | 1u << slot) ^ 16u << slot;
         }
         tc_fence_after();
-        const uint32_t vt = kvbase + (u % NST) * C::kKV, tp = tmem + slot * 128 + kPCol, to = tmem + 256 + slot * HDP;
+        const uint32_t vt = kvbase + (u % NST) * C::kStage + (T2 ? C::kKV : 0), tp = tmem + slot * 128 + kPCol, to = tmem + 256 + slot * HDP;
         const uint64_t vd = umma_desc_mn128(vt, BK * 128, 1024);
         umma_f16_ta_warp4(to, tp, vd, id_o, !first);
         if (!wait(sh.p_full[slot][1], phase)) return false;
@@ -875,19 +886,19 @@ __global__ void __launch_bounds__(CTHREADS, 1) chunk_kernel(const __grid_constan
           if (!(ok = wait(sh.q_full, nq))) break;
           ++nq;
           const int u = u0;
-          u0 += 2 * n;
+          u0 += C::kUses * n;
           if (mode == PAIR) {
             const int e0 = f0 + c0, e1 = f1 + c1;  // slot s works on key tiles f .. e - 1
             if (!(ok = wait_full(u))) break;
             if (f0 == 0 && c0) qk(0, qbase, u);
             if (f1 == 0 && c1) qk(1, qbase + C::kQ, u);
-            release(u);
+            if (!T2) release(u);
             if (n == 1) umma_commit_warp(smem_u32(&sh.q_empty));
 #pragma unroll 1
             for (int i = 0; i < n; ++i) {
-              const int uv = u + 2 * i + 1, uk = uv + 1;
+              const int uv = u + (T2 ? i : 2 * i + 1), uk = uv + 1;
               const bool more = i + 1 < n;
-              if (!(ok = wait_full(uv))) break;
+              if (!T2 && !(ok = wait_full(uv))) break;
               if (i >= f0 && i < e0) {
                 if (!(ok = pv(0, np0++, uv, i == f0))) break;
                 if (i + 1 == e0) umma_commit_warp(smem_u32(&sh.o_full[0]));
@@ -903,7 +914,7 @@ __global__ void __launch_bounds__(CTHREADS, 1) chunk_kernel(const __grid_constan
               release(uv);
               if (more) {
                 if (i + 1 >= f1 && i + 1 < e1) qk(1, qbase + C::kQ, uk);
-                release(uk);
+                if (!T2) release(uk);
                 if (i + 2 == n) umma_commit_warp(smem_u32(&sh.q_empty));
               }
             }
@@ -913,21 +924,21 @@ __global__ void __launch_bounds__(CTHREADS, 1) chunk_kernel(const __grid_constan
             for (int i = 0; i < 2 && i < n; ++i) {
               if (!(ok = wait_full(u + i))) break;
               qk(i, qbase, u + i);
-              release(u + i);
+              if (!T2) release(u + i);
               if (i == n - 1) umma_commit_warp(smem_u32(&sh.q_empty));
             }
 #pragma unroll 1
             for (int i = 0; ok && i < n; ++i) {
-              const int slot = i & 1, uv = u + ring_v(mode, i, n);
-              if (!(ok = wait_full(uv))) break;
+              const int slot = i & 1, uv = u + (T2 ? i : ring_v(mode, i, n));
+              if (!T2 && !(ok = wait_full(uv))) break;
               if (!(ok = pv(slot, slot ? np1++ : np0++, uv, i < 2))) break;
               release(uv);
               if (i + 2 >= n) umma_commit_warp(smem_u32(&sh.o_full[slot]));
               if (i + 2 < n) {
-                const int uk = u + ring_k(mode, i + 2);
+                const int uk = u + (T2 ? i + 2 : ring_k(mode, i + 2));
                 if (!(ok = wait_full(uk))) break;
                 qk(slot, qbase, uk);
-                release(uk);
+                if (!T2) release(uk);
                 if (i + 2 == n - 1) umma_commit_warp(smem_u32(&sh.q_empty));
               }
             }
@@ -1014,7 +1025,7 @@ __global__ void __launch_bounds__(CTHREADS, 1) chunk_kernel(const __grid_constan
       const Piece& p = sh.pq[k % QDEPTH];
       if (p.mode == END) break;
       const int n = p.jb - p.ja, u = u0;
-      u0 += 2 * n;
+      u0 += C::kUses * n;
       const Steps st = slot_steps(a, p, slot);
       const int r = p.mode == QUAD ? lane : tw;
       const int tok0 = p.mode == PAIR ? slot * a.tpq : 0;
@@ -1040,11 +1051,11 @@ __global__ void __launch_bounds__(CTHREADS, 1) chunk_kernel(const __grid_constan
           // reach every row through the product.  (This wait comes after
           // s_full: the MMA warp has then consumed the stage's previous
           // tile, so the barrier is at most one phase behind.)
-          const int uv = u + ring_v(p.mode, j - p.ja, n);
+          const int uv = u + (C::kTogether ? j - p.ja : ring_v(p.mode, j - p.ja, n));
           ok = __all_sync(0xffffffffu, ok && cwait(smem_u32(&sh.full[uv % NST]), (uv / NST) & 1, ab));
           const int key = j * BK + tw;
           if (key >= p.kl || key < p.lo) {
-            const uint32_t v = kvbase + (uv % NST) * C::kKV + tw * 128;
+            const uint32_t v = kvbase + (uv % NST) * C::kStage + (C::kTogether ? C::kKV : 0) + tw * 128;
             for (int at = 0; at < C::KA; ++at)
               for (int x = 0; x < 8; ++x) sts128(v + at * (BK * 128) + x * 16, make_uint4(0, 0, 0, 0));
           }
