@@ -504,7 +504,7 @@ __device__ __forceinline__ void weights32(const uint32_t (&v)[N], int at, f2_t c
 // One key tile's softmax for the thread's row: 128 score columns at tS, the
 // weights to the packed operand at tS + kPCol, over scores that are in
 // registers by then.
-template <typename T>
+template <typename T, bool HALVES>
 __device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, int key0, const Row& row, float c, bool first, int hd, float& R,
                                              float& l, uint32_t p_half, int lane) {
   const bool ragged = __any_sync(0xffffffffu, row.ok && (key0 < row.lo || key0 + BK > row.hi));
@@ -520,7 +520,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, int key0,
     uint32_t w[16];
     weights32<T>(v, 32 * k, c2, r2, w, sum);
     tmem_st16(tS + kPCol + 16 * k, w);
-    if (k == 1) hand_over(p_half, lane);
+    if (HALVES && k == 1) hand_over(p_half, lane);
   }
   const float2 s2 = upk2(fadd2(sum[0], sum[1]));
   l += s2.x + s2.y;
@@ -857,7 +857,8 @@ __global__ void __launch_bounds__(CTHREADS, 1) chunk_kernel(const __grid_constan
       // slot without keys waits for nothing, and its warps may be pieces ahead)
       uint32_t of = 0;
       auto pv = [&](int slot, int phase, int u, bool first) {
-        if (!wait(sh.p_full[slot][0], phase)) return false;
+        if (!T2 && !wait(sh.p_full[slot][0], phase)) return false;
+        if (T2 && !wait(sh.p_full[slot][1], phase)) return false;
         if (first) {
           if ((of >> slot & 1) && !wait(sh.o_free[slot], 1 ^ (of >> (4 + slot) & 1))) return false;
           of = (of | 1u << slot) ^ 16u << slot;
@@ -866,7 +867,7 @@ __global__ void __launch_bounds__(CTHREADS, 1) chunk_kernel(const __grid_constan
         const uint32_t vt = kvbase + (u % NST) * C::kStage + (T2 ? C::kKV : 0), tp = tmem + slot * 128 + kPCol, to = tmem + 256 + slot * HDP;
         const uint64_t vd = umma_desc_mn128(vt, BK * 128, 1024);
         umma_f16_ta_warp4(to, tp, vd, id_o, !first);
-        if (!wait(sh.p_full[slot][1], phase)) return false;
+        if (!T2 && !wait(sh.p_full[slot][1], phase)) return false;
         tc_fence_after();
         umma_f16_ta_warp4(to, tp + 32, vd + 512, id_o, true);
         return true;
@@ -1064,10 +1065,10 @@ __global__ void __launch_bounds__(CTHREADS, 1) chunk_kernel(const __grid_constan
         const uint32_t h0 = smem_u32(&sh.p_full[slot][0]), h1 = smem_u32(&sh.p_full[slot][1]);
         if (p.mode == QUAD) {
           softmax_quad<T>(tS, tO, quarter, j * BK + quarter * 32, row, a.c, i == 0, hd, R, l);
-          hand_over(h0, lane);
-          if (lane == 0) mbar_arrive(h1);
+          hand_over(h1, lane);
+          if (!C::kTogether && lane == 0) mbar_arrive(h0);
         } else {
-          softmax_tile<T>(tS, tO, j * BK, row, a.c, i == 0, hd, R, l, h0, lane);
+          softmax_tile<T, !C::kTogether>(tS, tO, j * BK, row, a.c, i == 0, hd, R, l, h0, lane);
           hand_over(h1, lane);
         }
       }
