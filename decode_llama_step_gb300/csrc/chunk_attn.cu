@@ -16,19 +16,34 @@
 //   P = 2^(...) softmax warps, thread = row, written over S as 16-bit TMEM operand
 //   O += P V    M = 128, N = head_dim, K = 128 keys (A from TMEM, V MN-major)
 // While one slot's softmax runs, the tensor core works for the other.  Tiles
-// with rows for one slot only (few new tokens) give both slots the same Q
-// and every second key tile ("split"), joined in the epilogue; with at most
-// 32 rows ("quad") Q is replicated into the four lane quarters of the
-// operand and each softmax warp takes a quarter of the key columns, so a
-// single token's softmax is spread over all eight warps.
+// with rows for one slot only (few new tokens: single tokens, verify passes,
+// the ends of chunks) give both slots the same Q and every second key tile
+// ("split"), joined in the epilogue.
 //
 // Work is divided by key tiles, not by sequences: the key tiles of all
 // (KV head, sequence, token tile) in a row, each tile of work led by what it
-// costs besides (kTileCost), are cut into one equal range per CTA, whatever the mix of prompts and single tokens; a tile cut by a range
-// border leaves partial (R, l, O) in the workspace and the last CTA to arrive
-// joins them in range order.  Each CTA finds its range itself from the
-// device-side lengths, so a call is one launch and a captured graph follows
-// the lengths.
+// costs besides (kTileCost), are cut into one equal range per CTA, whatever
+// the mix of prompts and single tokens; a tile cut by a range border leaves
+// partial (R, l, O) in the workspace and the last CTA to arrive joins them in
+// range order.  Each CTA finds its range itself from the device-side lengths,
+// so a call is one launch and a captured graph follows the lengths.
+//
+// What bounds it, measured on one GB300 (8B and 70B head counts, head_dim
+// 128, bf16, GPU time):
+//  - prompts: 8192 tokens of 32 heads 400 us (1372 TFLOP/s), 2048 tokens of
+//    64 heads over 32768 1470 us (1445 TFLOP/s; cuBLAS reaches 1919 in a burst,
+//    1698 under the power cap).  The MMA warp: the tensor pipe takes about two
+//    products ahead, and its barrier waits (about 100 cycles each) show
+//    between them; QK^T also reads 128 bytes a cycle of shared memory, all
+//    there is.  Slower in this place: a warp per slot (the slots fall into
+//    step and their softmaxes collide: 1540 us on the second case), asking
+//    barriers between the halves of a product (1530), a third score buffer
+//    for narrow heads, softmax in rolled chunks (1573).  Moving R at every new
+//    maximum (kGrow = 0): 475 and 1600 us.
+//  - single tokens: 64 of 64 heads over 4096 cached on average 220 us, 6.3 TB/s
+//    (a plain copy moves 6.8): the cache is read once.
+//  - small calls: latencies in a row (lengths, page table, first tiles,
+//    epilogue, arrival, join): one token over 2048 cached 15.9 us.
 //
 // Warps: 0 copies (TMA), 1 MMA, 2 the CTA's piece list, 4-7 / 8-11 softmax of
 // slot 0 / 1.  Every wait is bounded (2 s) and sets an abort flag.
@@ -59,7 +74,7 @@ constexpr int kPCol = 64;         // the weights' columns in a slot's S (packed:
 constexpr int kJoinCap = 1024;     // (piece, row) statistics of a slot that a join keeps in shared memory
 constexpr int kCounterBytes = 4096;  // int [MAXC][2], at the start of the workspace
 
-enum Mode { PAIR = 0, SPLIT = 1, QUAD = 2, END = 3 };
+enum Mode { PAIR = 0, SPLIT = 1, END = 2 };
 
 struct ChunkArgs {
   void* o;
@@ -73,7 +88,6 @@ struct ChunkArgs {
   int page_shift, n_pages, max_pages, pool_rows;
   int causal, window;
   int tpq;      // tokens of a slot: 128 / group
-  int tpq_quad; // tokens of a quad tile: 32 / group (0: none)
   unsigned inv_group;  // ceil(2^16 / group): r / group = r * inv_group >> 16 for r < 128
   float c;      // scale * log2(e)
   int small_plan;  // few sequences and tiles: one warp plans
@@ -104,16 +118,14 @@ struct CCfg {
   static constexpr int kStage = kTogether ? 2 * kKV : kKV;
   static constexpr int NST = 4;
   static constexpr int kKVOff = 2 * kQ;
-  static constexpr int kXOff = kKVOff + NST * kStage;  // float [4][32][32]: joins the quarters of a quad tile
-  static constexpr int kJOff = kXOff + 4 * 32 * 32 * 4;  // statistics being joined: slot 0's in X, slot 1's here
-  static constexpr int kMiscOff = kJOff + 2 * kJoinCap * 4;
+  static constexpr int kXOff = kKVOff + NST * kStage;  // 8 KB a slot: its output rows on their way out, or statistics being joined
+  static constexpr int kMiscOff = kXOff + 2 * 8192;
 };
 
 struct CMisc {
   uint64_t full[4], empty[4], s_full[2], p_full[2][2], o_full[2], o_free[2], q_full, q_empty, x_full, pq_full[QDEPTH], pq_empty[QDEPTH];
   Piece pq[QDEPTH];
   float xm[128], xl[128];        // slot 1's statistics for slot 0 (split)
-  float qm[4][32], ql[4][32];    // per quarter (quad)
   long long scan[CWARPS];
   long long range0, range1, per;
   int b0, t0, off0, kvh0;
@@ -126,7 +138,7 @@ template <int HDP>
 constexpr int chunk_smem() {
   return CCfg<HDP>::kMiscOff + (int)sizeof(CMisc) + 1024;
 }
-static_assert(2 * kJoinCap * 4 <= 4 * 32 * 32 * 4, "join area");
+static_assert(2 * kJoinCap * 4 <= 8192, "join area");
 static_assert(chunk_smem<128>() <= 227 * 1024 && chunk_smem<64>() <= 227 * 1024, "shared memory");
 // a CTA allocates all of tensor memory: a second one must not fit on the SM
 static_assert(2 * chunk_smem<64>() > 227 * 1024, "one CTA per SM");
@@ -220,7 +232,7 @@ __device__ __forceinline__ Tile tile_of(const ChunkArgs& a, int ql, int kl, int 
   Tile x;
   const int i0 = t * 2 * a.tpq;
   x.n = min(2 * a.tpq, ql - i0);
-  x.mode = x.n > a.tpq ? PAIR : x.n > a.tpq_quad ? SPLIT : QUAD;
+  x.mode = x.n > a.tpq ? PAIR : SPLIT;
   x.pos0 = kl - ql + i0;
   const int hi = a.causal ? min(max(x.pos0 + x.n, 0), kl) : kl;
   x.lo = a.window && x.pos0 >= a.window ? min(x.pos0 - a.window + 1, hi) : 0;
@@ -526,30 +538,6 @@ __device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, int key0,
   l += s2.x + s2.y;
 }
 
-// The same for a quad tile: the warp's quarter of the columns, zero weights in
-// the others of its rows.
-template <typename T>
-__device__ __forceinline__ void softmax_quad(uint32_t tS, uint32_t tO, int quarter, int key0, const Row& row, float c, bool first, int hd,
-                                             float& R, float& l) {
-  uint32_t v[32], w[16];
-  tmem_read(tS + 32 * quarter, v);
-  if (__any_sync(0xffffffffu, row.ok && (key0 < row.lo || key0 + 32 > row.hi))) mask_keys(v, key0, row);
-  follow_max(max_of(v, -INFINITY) * c, row, first, tO, hd, R, l);
-  const float nr = kShift - (R == -INFINITY ? 0.f : R);
-  f2_t sum[2] = {pk2(0.f, 0.f), pk2(0.f, 0.f)};
-  weights32<T>(v, 0, pk2(c, c), pk2(nr, nr), w, sum);
-  const float2 s2 = upk2(fadd2(sum[0], sum[1]));
-  l += s2.x + s2.y;
-  uint32_t z[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) z[i] = 0;
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    if (q == quarter) tmem_st16(tS + kPCol + 16 * q, w);
-    else tmem_st16(tS + kPCol + 16 * q, z);
-  }
-}
-
 __device__ __forceinline__ float weight(float R, float M) { return R == -INFINITY ? 0.f : ex2(R - M); }
 
 template <int HDP>
@@ -696,7 +684,6 @@ __device__ __noinline__ void join(const ChunkArgs& a, int c0, int np, int kvh, i
 
 template <typename T, int HDP>
 __global__ void __launch_bounds__(CTHREADS, 1) chunk_kernel(const __grid_constant__ CUtensorMap tm_q,
-                                                            const __grid_constant__ CUtensorMap tm_q4,
                                                             const __grid_constant__ CUtensorMap tm_k,
                                                             const __grid_constant__ CUtensorMap tm_v,
                                                             const __grid_constant__ ChunkArgs a) {
@@ -734,7 +721,6 @@ __global__ void __launch_bounds__(CTHREADS, 1) chunk_kernel(const __grid_constan
   }
   if (tid == 96) {
     prefetch_tmap(&tm_q);
-    prefetch_tmap(&tm_q4);
     prefetch_tmap(&tm_k);
     prefetch_tmap(&tm_v);
   }
@@ -759,7 +745,7 @@ __global__ void __launch_bounds__(CTHREADS, 1) chunk_kernel(const __grid_constan
       // ---------------- copies: Q tiles, and K/V tiles piece by piece of a page
       const int pr = min(1 << a.page_shift, BK);  // keys of a copy
       const int npc = BK / pr;
-      const uint32_t qbytes = 128u * a.group * a.tpq * C::KA, q4bytes = 4u * 128u * a.group * a.tpq_quad * C::KA;
+      const uint32_t qbytes = 128u * a.group * a.tpq * C::KA;
       int u = 0, nq = 0;
       bool ok = true, q_out = false;
       for (int k = 0; ok; ++k) {
@@ -773,16 +759,12 @@ __global__ void __launch_bounds__(CTHREADS, 1) chunk_kernel(const __grid_constan
         if (nq > 0 && !(ok = __all_sync(0xffffffffu, cwait(smem_u32(&sh.q_empty), (nq - 1) & 1, ab)))) break;
         if (lane == 0) {
           const uint32_t bar = smem_u32(&sh.q_full);
-          mbar_expect_tx(bar, p.mode == PAIR ? 2 * qbytes : p.mode == SPLIT ? qbytes : q4bytes);
+          mbar_expect_tx(bar, p.mode == PAIR ? 2 * qbytes : qbytes);
           const int h0 = p.kvh * a.group;
           for (int at = 0; at < C::KA; ++at) {
             const uint32_t d = qbase + at * (128 * 128);
-            if (p.mode == QUAD) {
-              for (int w = 0; w < 4; ++w) tma_load_3d(d + w * (32 * 128), &tm_q4, at * 64, h0, p.row0, bar);
-            } else {
-              tma_load_3d(d, &tm_q, at * 64, h0, p.row0, bar);
-              if (p.mode == PAIR) tma_load_3d(d + C::kQ, &tm_q, at * 64, h0, p.row0 + a.tpq, bar);
-            }
+            tma_load_3d(d, &tm_q, at * 64, h0, p.row0, bar);
+            if (p.mode == PAIR) tma_load_3d(d + C::kQ, &tm_q, at * 64, h0, p.row0 + a.tpq, bar);
           }
         }
         ++nq;
@@ -1028,10 +1010,10 @@ __global__ void __launch_bounds__(CTHREADS, 1) chunk_kernel(const __grid_constan
       const int n = p.jb - p.ja, u = u0;
       u0 += C::kUses * n;
       const Steps st = slot_steps(a, p, slot);
-      const int r = p.mode == QUAD ? lane : tw;
       const int tok0 = p.mode == PAIR ? slot * a.tpq : 0;
       const int ntok = p.mode == PAIR ? min(p.n - tok0, a.tpq) : p.n;
-      const int tok = token_of(a, r), hg = r - tok * G;
+      const int tok = token_of(a, tw), hg = tw - tok * G;
+      const bool busy = quarter * 32 < ntok * G;  // the warp has rows of the batch
       Row row;
       row.ok = tok < ntok;
       row.lo = 0;
@@ -1063,13 +1045,15 @@ __global__ void __launch_bounds__(CTHREADS, 1) chunk_kernel(const __grid_constan
           fence_async_smem();
         }
         const uint32_t h0 = smem_u32(&sh.p_full[slot][0]), h1 = smem_u32(&sh.p_full[slot][1]);
-        if (p.mode == QUAD) {
-          softmax_quad<T>(tS, tO, quarter, j * BK + quarter * 32, row, a.c, i == 0, hd, R, l);
-          hand_over(h1, lane);
-          if (!C::kTogether && lane == 0) mbar_arrive(h0);
-        } else {
+        if (busy) {
           softmax_tile<T, !C::kTogether>(tS, tO, j * BK, row, a.c, i == 0, hd, R, l, h0, lane);
           hand_over(h1, lane);
+        } else {
+          // (after s_full, so that no warp arrives for two tiles in one phase)
+          tc_fence_before();
+          __syncwarp();
+          if (!C::kTogether && lane == 0) mbar_arrive(h0);
+          if (lane == 0) mbar_arrive(h1);
         }
       }
       if (st.count) {
@@ -1110,148 +1094,84 @@ __global__ void __launch_bounds__(CTHREADS, 1) chunk_kernel(const __grid_constan
       if (count1) ++no[1];
       tc_fence_after();
       const uint32_t tO1 = tO + HDP;  // slot 1's O
-      if (p.mode != QUAD) {
-        float inv = 1.f;
-        if (!part) inv = l > 0.f ? 1.f / l : 0.f;
-        w0 *= inv;
-        w1 *= inv;
-        // 64 bytes of each row at a time through shared memory, so that a store
-        // covers 8 rows x 64 bytes (a lane storing its own row: 32 rows x 16,
-        // 32 cycles a store); partials lie column by column and need none
-        const uint32_t stage = qbase + (slot ? C::kJOff : C::kXOff) + quarter * 2048;
-        // the four rows that this lane stores a 16-byte chunk of, and where
-        T* to[4];
-        bool mine[4];
-        const int ch = lane & 3;
+      float inv = 1.f;
+      if (!part) inv = l > 0.f ? 1.f / l : 0.f;
+      w0 *= inv;
+      w1 *= inv;
+      // 64 bytes of each row at a time through shared memory, so that a store
+      // covers 8 rows x 64 bytes (a lane storing its own row: 32 rows x 16,
+      // 32 cycles a store); partials lie column by column and need none
+      const uint32_t stage = qbase + C::kXOff + slot * 8192 + quarter * 2048;
+      // the four rows that this lane stores a 16-byte chunk of, and where
+      T* to[4];
+      bool mine[4];
+      const int ch = lane & 3;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int rr = quarter * 32 + 8 * i + (lane >> 2), tk = token_of(a, rr);
-          mine[i] = tk < ntok;
-          to[i] = static_cast<T*>(a.o) + ((size_t)p.row0 + tok0 + tk) * a.o_stride + (size_t)(p.kvh * G + rr - tk * G) * hd + 8 * ch;
-        }
-        const uint32_t put = stage + lane * 64, get = stage + (lane >> 2) * 64;
-        const int swz = lane >> 1 & 3;                 // of the row lane and, for every i, of row 8 i + lane / 4: (lane >> 3 & 3)
-        const uint32_t got = get + ((ch ^ (lane >> 3 & 3)) << 4);
+      for (int i = 0; i < 4; ++i) {
+        const int rr = quarter * 32 + 8 * i + (lane >> 2), tk = token_of(a, rr);
+        mine[i] = tk < ntok;
+        to[i] = static_cast<T*>(a.o) + ((size_t)p.row0 + tok0 + tk) * a.o_stride + (size_t)(p.kvh * G + rr - tk * G) * hd + 8 * ch;
+      }
+      const uint32_t put = stage + lane * 64, get = stage + (lane >> 2) * 64;
+      const int swz = lane >> 1 & 3;                 // of the row lane and, for every i, of row 8 i + lane / 4: (lane >> 3 & 3)
+      const uint32_t got = get + ((ch ^ (lane >> 3 & 3)) << 4);
 #pragma unroll 1
-        for (int d = 0; d < hd; d += 32) {
-          if (use0 && !use1 && !part) {  // the common case: one slot's whole tile
-            uint32_t v[32];
-            tmem_read(tO + d, v);
-            const f2_t w2 = pk2(w0, w0), none = pk2(-0.f, -0.f);
+      for (int d = 0; busy && d < hd; d += 32) {
+        if (use0 && !use1 && !part) {  // the common case: one slot's whole tile
+          uint32_t v[32];
+          tmem_read(tO + d, v);
+          const f2_t w2 = pk2(w0, w0), none = pk2(-0.f, -0.f);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint32_t y[4];
+          for (int i = 0; i < 4; ++i) {
+            uint32_t y[4];
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float2 g = upk2(ffma2(pk2(__uint_as_float(v[8 * i + 2 * e]), __uint_as_float(v[8 * i + 2 * e + 1])), w2, none));
-                y[e] = Kind<T>::pack(g.x, g.y);
-              }
-              sts128(put + ((i ^ swz) << 4), make_uint4(y[0], y[1], y[2], y[3]));
+            for (int e = 0; e < 4; ++e) {
+              const float2 g = upk2(ffma2(pk2(__uint_as_float(v[8 * i + 2 * e]), __uint_as_float(v[8 * i + 2 * e + 1])), w2, none));
+              y[e] = Kind<T>::pack(g.x, g.y);
             }
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint4 y = lds128(got + i * 512);
-              if (mine[i] && d + 8 * ch < hd) *reinterpret_cast<uint4*>(to[i] + d) = y;
-            }
-            __syncwarp();
-            continue;
+            sts128(put + ((i ^ swz) << 4), make_uint4(y[0], y[1], y[2], y[3]));
           }
-          float f[32];
+          __syncwarp();
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t v[16] = {}, w[16] = {};
-            if (use0) tmem_read(tO + d + 16 * h, v);  // (a column past head_dim is allocated, and not stored)
-            if (use1) tmem_read(tO1 + d + 16 * h, w);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              f[16 * h + i] = use0 ? __uint_as_float(v[i]) * w0 : 0.f;
-              if (use1) f[16 * h + i] = fmaf(__uint_as_float(w[i]), w1, f[16 * h + i]);
-            }
+          for (int i = 0; i < 4; ++i) {
+            const uint4 y = lds128(got + i * 512);
+            if (mine[i] && d + 8 * ch < hd) *reinterpret_cast<uint4*>(to[i] + d) = y;
           }
-          if (part) {
-            if (row.ok)
+          __syncwarp();
+          continue;
+        }
+        float f[32];
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
-                if (d + 4 * i < hd)
-                  __stcg(reinterpret_cast<float4*>(part + 256) + (d / 4 + i) * 128 + tw,
-                         make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]));
-          } else {
+        for (int h = 0; h < 2; ++h) {
+          uint32_t v[16] = {}, w[16] = {};
+          if (use0) tmem_read(tO + d + 16 * h, v);  // (a column past head_dim is allocated, and not stored)
+          if (use1) tmem_read(tO1 + d + 16 * h, w);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              sts128(put + ((i ^ swz) << 4),
-                     make_uint4(Kind<T>::pack(f[8 * i], f[8 * i + 1]), Kind<T>::pack(f[8 * i + 2], f[8 * i + 3]),
-                                Kind<T>::pack(f[8 * i + 4], f[8 * i + 5]), Kind<T>::pack(f[8 * i + 6], f[8 * i + 7])));
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint4 y = lds128(got + i * 512);
-              if (mine[i] && d + 8 * ch < hd) *reinterpret_cast<uint4*>(to[i] + d) = y;
-            }
-            __syncwarp();
+          for (int i = 0; i < 16; ++i) {
+            f[16 * h + i] = use0 ? __uint_as_float(v[i]) * w0 : 0.f;
+            if (use1) f[16 * h + i] = fmaf(__uint_as_float(w[i]), w1, f[16 * h + i]);
           }
         }
-      } else {
-        // join the quarters, 32 output columns at a time
-        sh.qm[quarter][lane] = R;
-        sh.ql[quarter][lane] = l;
-        wg_sync(slot);
-        float M = -INFINITY, L = 0.f;
+        if (part) {
+          if (row.ok)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) M = fmaxf(M, sh.qm[q][lane]);
+            for (int i = 0; i < 8; ++i)
+              if (d + 4 * i < hd)
+                __stcg(reinterpret_cast<float4*>(part + 256) + (d / 4 + i) * 128 + tw,
+                       make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]));
+        } else {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) L = fmaf(weight(sh.qm[q][lane], M), sh.ql[q][lane], L);
-        float f = weight(R, M);
-        if (!part) f *= L > 0.f ? 1.f / L : 0.f;
-        w0 *= f;
-        w1 *= f;
-        R = M;
-        l = L;
-        // [quarter][row][chunk of 4 columns], chunk ^ (row & 7); as many columns a turn as the rows leave room for
-        float4* const X = reinterpret_cast<float4*>(csm + pad + C::kXOff);
-        const int rs = nrows <= 8 ? 3 : nrows <= 16 ? 4 : 5, cs = 8 - rs;  // log2 of rows and chunks a quarter holds
-#pragma unroll 1
-        for (int d = 0; d < hd; d += 4 << cs) {
-          const int cols = min(4 << cs, hd - d);
-#pragma unroll 1
-          for (int h = 0; h < cols; h += 16) {
-            uint32_t v[16] = {}, w[16] = {};
-            if (use0) tmem_read(tO + d + h, v);
-            if (use1) tmem_read(tO1 + d + h, w);
-            if (row.ok) {
+          for (int i = 0; i < 4; ++i)
+            sts128(put + ((i ^ swz) << 4),
+                   make_uint4(Kind<T>::pack(f[8 * i], f[8 * i + 1]), Kind<T>::pack(f[8 * i + 2], f[8 * i + 3]),
+                              Kind<T>::pack(f[8 * i + 4], f[8 * i + 5]), Kind<T>::pack(f[8 * i + 6], f[8 * i + 7])));
+          __syncwarp();
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                float g[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  g[e] = use0 ? __uint_as_float(v[4 * i + e]) * w0 : 0.f;
-                  if (use1) g[e] = fmaf(__uint_as_float(w[4 * i + e]), w1, g[e]);
-                }
-                X[(((quarter << rs) + lane) << cs) + ((h / 4 + i) ^ (lane & 7))] = make_float4(g[0], g[1], g[2], g[3]);
-              }
-            }
+          for (int i = 0; i < 4; ++i) {
+            const uint4 y = lds128(got + i * 512);
+            if (mine[i] && d + 8 * ch < hd) *reinterpret_cast<uint4*>(to[i] + d) = y;
           }
-          wg_sync(slot);
-          for (int x = tw; x < nrows << cs; x += 128) {
-            const int rr = x >> cs, ch = x & ((1 << cs) - 1), dd = d + 4 * ch;
-            if (dd < hd) {
-              float4 s = X[(rr << cs) + (ch ^ (rr & 7))];
-#pragma unroll
-              for (int q = 1; q < 4; ++q) {
-                const float4 y = X[(((q << rs) + rr) << cs) + (ch ^ (rr & 7))];
-                s.x += y.x, s.y += y.y, s.z += y.z, s.w += y.w;
-              }
-              if (part) {
-                __stcg(reinterpret_cast<float4*>(part + 256) + dd / 4 * 128 + rr, s);
-              } else {
-                const int tk = token_of(a, rr);
-                *reinterpret_cast<uint2*>(static_cast<T*>(a.o) + ((size_t)p.row0 + tk) * a.o_stride +
-                                          (size_t)(p.kvh * G + rr - tk * G) * hd + dd) =
-                    make_uint2(Kind<T>::pack(s.x, s.y), Kind<T>::pack(s.z, s.w));
-              }
-            }
-          }
-          wg_sync(slot);
+          __syncwarp();
         }
       }
       // O is read: the next piece may overwrite it
@@ -1261,10 +1181,10 @@ __global__ void __launch_bounds__(CTHREADS, 1) chunk_kernel(const __grid_constan
         if (use0) mbar_arrive(smem_u32(&sh.o_free[slot]));
         if (use1) mbar_arrive(smem_u32(&sh.o_free[1]));
       }
-      if (row.ok && (p.mode != QUAD || quarter == 0)) {
+      if (row.ok) {
         if (part) {
-          __stcg(part + r, R);
-          __stcg(part + 128 + r, l);
+          __stcg(part + tw, R);
+          __stcg(part + 128 + tw, l);
         } else if (a.lse) {
           a.lse[t * (a.n_kv * G) + head] = lse_of(R, l);
         }
@@ -1283,7 +1203,7 @@ __global__ void __launch_bounds__(CTHREADS, 1) chunk_kernel(const __grid_constan
         }
         wg_sync(slot);
         if (sh.last[slot]) {
-          float* area = reinterpret_cast<float*>(csm + pad + (slot ? C::kJOff : C::kXOff));
+          float* area = reinterpret_cast<float*>(csm + pad + C::kXOff + slot * 8192);
           join<T, HDP>(a, p.c0, p.np, p.kvh, p.row0 + tok0, slot, nrows, tw, area);
         }
       }
@@ -1300,7 +1220,7 @@ __global__ void __launch_bounds__(CTHREADS, 1) chunk_kernel(const __grid_constan
   }
 }
 
-using ChunkFn = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const CUtensorMap, const ChunkArgs);
+using ChunkFn = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const ChunkArgs);
 
 // SMs of the current device, with the kernels' attributes set on it; 0 on an error.
 int device_ready(cudaError_t* err) {
@@ -1385,18 +1305,17 @@ extern "C" int dls_attention_chunk(const dls_attention_chunk_desc* d, void* cuda
   a.page_shift = pt == 16 ? 4 : pt == 32 ? 5 : pt == 64 ? 6 : pt == 128 ? 7 : 8;
   a.n_pages = d->n_pages, a.max_pages = d->max_pages, a.pool_rows = d->n_pages * d->n_kv_heads * pt;
   a.causal = d->causal, a.window = d->window;
-  a.tpq = 128 / a.group, a.tpq_quad = 32 / a.group, a.inv_group = (65536 + a.group - 1) / a.group;
+  a.tpq = 128 / a.group, a.inv_group = (65536 + a.group - 1) / a.group;
   a.c = (d->scale > 0.f ? d->scale : 1.0f / sqrtf((float)hd)) * 1.4426950408889634f;
   // a lane of the planning warp walks at most 4 sequences and 8 more tiles; its sums fit 32 bits
   a.small_plan = d->n_seqs <= 128 && d->n_tokens <= 8 * 2 * a.tpq && (long long)d->max_pages * pt <= 1 << 24;
   const CUtensorMapDataType dt = d->kv_type == DLS_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const uint32_t pr = pt < BK ? pt : BK;
-  CUtensorMap tq, tq4, tk, tv;
+  CUtensorMap tq, tk, tv;
   const uint64_t dims[3] = {(uint64_t)hd, (uint64_t)d->n_heads, (uint64_t)d->n_tokens};
   const uint64_t strides[2] = {(uint64_t)hd * 2, (uint64_t)d->q_stride * 2};
-  const uint32_t box[3] = {64, (uint32_t)a.group, (uint32_t)a.tpq}, box4[3] = {64, (uint32_t)a.group, (uint32_t)(a.tpq_quad ? a.tpq_quad : 1)};
+  const uint32_t box[3] = {64, (uint32_t)a.group, (uint32_t)a.tpq};
   if (!make_tmap_3d(&tq, dt, d->q, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !make_tmap_3d(&tq4, dt, d->q, dims, strides, box4, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !make_tmap_2d(&tk, dt, d->k_pages, hd, a.pool_rows, hd * 2, 64, pr, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !make_tmap_2d(&tv, dt, d->v_pages, hd, a.pool_rows, hd * 2, 64, pr, CU_TENSOR_MAP_SWIZZLE_128B))
     return report_error(DLS_ERR_CUDA, "attention_chunk: tensor map (head_dim=%d n_heads=%d n_tokens=%d)", hd, d->n_heads, d->n_tokens);
@@ -1405,7 +1324,7 @@ extern "C" int dls_attention_chunk(const dls_attention_chunk_desc* d, void* cuda
     const bool half = d->kv_type == DLS_F16;
     const ChunkFn f = hd <= 64 ? (half ? chunk_kernel<__half, 64> : chunk_kernel<__nv_bfloat16, 64>)
                                : (half ? chunk_kernel<__half, 128> : chunk_kernel<__nv_bfloat16, 128>);
-    f<<<sms < MAXC ? sms : MAXC, CTHREADS, hd <= 64 ? chunk_smem<64>() : chunk_smem<128>(), s>>>(tq, tq4, tk, tv, a);
+    f<<<sms < MAXC ? sms : MAXC, CTHREADS, hd <= 64 ? chunk_smem<64>() : chunk_smem<128>(), s>>>(tq, tk, tv, a);
     e = cudaGetLastError();
   }
   if (e != cudaSuccess) return report_error(DLS_ERR_CUDA, "attention_chunk: cuda=%s", cudaGetErrorString(e));
