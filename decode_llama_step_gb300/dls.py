@@ -372,8 +372,8 @@ def attention_chunk_workspace_bytes(head_dim: int) -> int:
 def attention_chunk(q, k_pages, v_pages, page_table, cu_q, kv_len, o, workspace, *, lse=None, scale=0.0, causal=True,
                     window=0, status=None, stream=None):
     """Attention of ragged chunks of new tokens (q, o [tokens, heads, head_dim] in the cache's type) over the paged
-    cache.  workspace: a uint8 tensor of attention_chunk_workspace_bytes(head_dim) zeros, kept from call to call.
-    lse: fp32 [tokens, heads] or None.  scale 0: 1 / sqrt(head_dim)."""
+    cache; o may be q.  workspace: a uint8 tensor of attention_chunk_workspace_bytes(head_dim) zeros, kept from call to
+    call, one for each of the calls that may overlap.  lse: fp32 [tokens, heads] or None.  scale 0: 1 / sqrt(head_dim)."""
     kv_type, device = _dtype(k_pages, "k_pages"), q.get_device()
     pages, kvh, pt, hd, kpp, vpp, table, most, cu, kl, seqs = _pools(k_pages, v_pages, page_table, cu_q, kv_len, device)
     n, heads, _ = _dims(q, "q")

@@ -530,9 +530,13 @@ int dls_kv_append(const dls_kv_append_desc* d, void* cuda_stream);
  * with no key (kv_len below the chunk's length) gives o = 0 and lse = -inf.
  * Scores, softmax statistics and sums are fp32; the weights are rounded to
  * kv_type for the product with V.  Keys at or past kv_len, and before every
- * window, are never used, whatever their pages hold, and their page-table
- * entries are not read.  Results do not depend on timing: partial sums are
- * joined in a fixed order.
+ * window of the chunk's rows, are never used, whatever their pages hold, and
+ * page-table entries of pages with none but such keys are not read.  The other
+ * keys and values of a sequence should be finite: a NaN or an infinity in one
+ * token's V may reach every row of its sequence (zero times infinity), never
+ * another sequence's.  A page flagged in status counts as zeros.  Results do
+ * not depend on timing: partial sums are joined in a fixed order.  o may be q
+ * itself (the same stride); it must not overlap an input otherwise.
  * workspace: dls_attention_chunk_workspace_bytes(head_dim) bytes, 256-byte
  * aligned, zeroed before its first call (a call leaves it ready for the
  * next, of any shape with that head_dim or a smaller one; zero it again after a call that

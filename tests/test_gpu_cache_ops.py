@@ -480,6 +480,65 @@ def test_attention_chunk_on_a_stream_of_its_own(gpu_lib):
     check_attend([(1, 900), (150, 300)], 8, 2, 128, 64, "bf16", stream=s)
 
 
+def test_attention_chunk_in_place(gpu_lib):
+    """o = q: tiles cut among CTAs, tiles of neighbours in one load, single tokens."""
+    B = Batch([(1, 3000), (300, 900), (2, 700), (77, 77)], 2, 128, 64, torch.bfloat16, 6)
+    B.fill()
+    q = torch.randn(B.rows, 8, 128, generator=B.g, device="cuda").to(B.typ)
+    o, ws = torch.empty_like(q), workspace(128)
+    dls.attention_chunk(q, B.k, B.v, B.table, B.cu_q, B.kv_len, o, ws)
+    for _ in range(5):
+        x = q.clone()
+        dls.attention_chunk(x, B.k, B.v, B.table, B.cu_q, B.kv_len, x, ws)
+        assert torch.equal(x, o)
+
+
+def test_attention_chunk_two_calls_at_once(gpu_lib):
+    """Calls on two streams, a workspace each, give what each gives alone."""
+    made = []
+    for lengths, hd in (([(1, 2000)] * 5 + [(70, 200)], 128), ([(400, 1000), (1, 3000)], 64)):
+        B = Batch(lengths, 2, hd, 32, torch.float16, 13)
+        B.fill()
+        q = torch.randn(B.rows, 8, hd, generator=B.g, device="cuda").half()
+        made.append((B, q, torch.empty_like(q), torch.empty_like(q), workspace(hd), torch.cuda.Stream()))
+    for B, q, alone, _, ws, _ in made:
+        dls.attention_chunk(q, B.k, B.v, B.table, B.cu_q, B.kv_len, alone, ws)
+        torch.cuda.synchronize()
+    for _ in range(30):
+        for B, q, _, o, ws, stream in made:
+            dls.attention_chunk(q, B.k, B.v, B.table, B.cu_q, B.kv_len, o, ws, stream=stream)
+    torch.cuda.synchronize()
+    for _, _, alone, o, _, _ in made:
+        assert torch.equal(o, alone)
+
+
+def test_a_pool_of_more_than_two_to_the_31_elements(gpu_lib):
+    """Append and attention over the last pages of pools whose element offsets pass 32 bits."""
+    kvh, page, hd, heads, n_pages = 2, 128, 128, 8, 70000  # 2.3e9 elements, 4.6 GB each
+    pools = [torch.empty(n_pages, kvh, page, hd, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    B = Batch([(150, 150), (1, 300)], kvh, hd, page, torch.bfloat16, 31, extra=0)
+    B.fill()
+    own = (B.table >= 0) & (B.table < B.n_pages)
+    used = B.table[own].long()
+    moved = n_pages - 1 - 3 * used                       # far pages, in another order
+    for pool, src in zip(pools, (B.k, B.v)):
+        pool[moved] = src[used]
+    table = torch.where(own, n_pages - 1 - 3 * B.table, B.table)
+    x = torch.randn(B.rows, heads + 2 * kvh, hd, generator=B.g, device="cuda").to(B.typ)
+    q = torch.empty(B.rows, heads, hd, dtype=B.typ, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    freq, ws, o = dls.rope_inv_freq(hd, 500000.0), workspace(hd), torch.empty_like(q)
+    dls.kv_append(x[:, heads:heads + kvh], x[:, heads + kvh:], *pools, table, B.cu_q, B.kv_len, freq, q=x[:, :heads], q_out=q,
+                  status=status)
+    dls.attention_status(status)
+    dls.attention_chunk(q, *pools, table, B.cu_q, B.kv_len, o, ws, status=status)
+    dls.attention_status(status)
+    dls.kv_append(x[:, heads:heads + kvh], x[:, heads + kvh:], B.k, B.v, B.table, B.cu_q, B.kv_len, freq)  # the small pool
+    for pool, small in zip(pools, (B.k, B.v)):
+        assert torch.equal(pool[moved].view(torch.int16), small[used].view(torch.int16))
+    close_attend(B, o, None, attend64(B, q, heads, hd ** -0.5, True, 0), heads)
+
+
 def test_attention_chunk_matches_single_token_attention(gpu_lib):
     """The same rows as dls_attention_decode (fp32 q and o) on the same pages."""
     B = Batch([(1, 513), (1, 64), (1, 1300)], 8, 128, 64, torch.float16, 8, extra=0)
