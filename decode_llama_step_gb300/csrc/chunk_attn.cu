@@ -30,8 +30,8 @@
 //
 // What bounds it, measured on one GB300 (8B and 70B head counts, head_dim
 // 128, bf16, GPU time):
-//  - prompts: 8192 tokens of 32 heads 400 us (1372 TFLOP/s), 2048 tokens of
-//    64 heads over 32768 1470 us (1445 TFLOP/s; cuBLAS reaches 1919 in a burst,
+//  - prompts: 8192 tokens of 32 heads 397 us (1386 TFLOP/s), 2048 tokens of
+//    64 heads over 32768 1490 us (1430 TFLOP/s; cuBLAS reaches 1919 in a burst,
 //    1698 under the power cap).  The MMA warp: the tensor pipe takes about two
 //    products ahead, and its barrier waits (about 100 cycles each) show
 //    between them; QK^T also reads 128 bytes a cycle of shared memory, all
@@ -40,10 +40,10 @@
 //    barriers between the halves of a product (1530), a third score buffer
 //    for narrow heads, softmax in rolled chunks (1573).  Moving R at every new
 //    maximum (kGrow = 0): 475 and 1600 us.
-//  - single tokens: 64 of 64 heads over 4096 cached on average 220 us, 6.3 TB/s
+//  - single tokens: 64 of 64 heads over 4096 cached on average 222 us, 6.3 TB/s
 //    (a plain copy moves 6.8): the cache is read once.
 //  - small calls: latencies in a row (lengths, page table, first tiles,
-//    epilogue, arrival, join): one token over 2048 cached 15.9 us.
+//    epilogue, arrival, join): one token over 2048 cached 15.7 us.
 //
 // Warps: 0 copies (TMA), 1 MMA, 2 the CTA's piece list, 4-7 / 8-11 softmax of
 // slot 0 / 1.  Every wait is bounded (2 s) and sets an abort flag.
