@@ -1279,13 +1279,20 @@ extern "C" int dls_attention_chunk(const dls_attention_chunk_desc* d, void* cuda
   if ((d->causal != 0 && d->causal != 1) || d->window < 0 || (d->window && !d->causal))
     return report_error(DLS_ERR_ARG, "attention_chunk: causal=%d window=%d (a window needs causal = 1)", d->causal, d->window);
   if (!(d->scale >= 0.f) || !isfinite(d->scale)) return report_error(DLS_ERR_ARG, "attention_chunk: scale=%g", d->scale);
-  if (d->n_tokens == 0 || d->n_seqs == 0) return DLS_OK;
+  const int tpq = 128 / (d->n_heads / d->n_kv_heads);
+  // decreasing cu_q can give every sequence all the rows: their tiles still have to fit an int
+  if (((long long)d->n_tokens / (2 * tpq) + 1) * d->n_seqs > 0x7fffffff)
+    return report_error(DLS_ERR_ARG, "attention_chunk: n_tokens=%d n_seqs=%d are too many", d->n_tokens, d->n_seqs);
+  if (!aligned_to(d->status, 4) || !aligned_to(d->lse, 4))
+    return report_error(DLS_ERR_ARG, "attention_chunk: lse=%p status=%p", (void*)d->lse, (void*)d->status);
+  if (d->n_tokens == 0 || d->n_seqs == 0) return empty_call(d->status, cuda_stream, "attention_chunk");
   if (!rows_ok(d->q, d->q_stride, (long long)d->n_heads * hd) || !rows_ok(d->o, d->o_stride, (long long)d->n_heads * hd))
     return report_error(DLS_ERR_ARG, "attention_chunk: q and o need 16-byte aligned rows of n_heads * head_dim elements (strides %lld, %lld)",
                         (long long)d->q_stride, (long long)d->o_stride);
+  if (d->q == d->o && d->q_stride != d->o_stride) return report_error(DLS_ERR_ARG, "attention_chunk: in place needs the same stride");
   if (!d->k_pages || !d->v_pages || ((reinterpret_cast<uintptr_t>(d->k_pages) | reinterpret_cast<uintptr_t>(d->v_pages)) & 15))
     return report_error(DLS_ERR_ARG, "attention_chunk: k_pages=%p v_pages=%p (16-byte aligned)", d->k_pages, d->v_pages);
-  if (!d->page_table || !d->cu_q || !d->kv_len)
+  if (!d->page_table || !d->cu_q || !d->kv_len || !aligned_to(d->page_table, 4) || !aligned_to(d->cu_q, 4) || !aligned_to(d->kv_len, 4))
     return report_error(DLS_ERR_ARG, "attention_chunk: page_table=%p cu_q=%p kv_len=%p", (const void*)d->page_table, (const void*)d->cu_q,
                         (const void*)d->kv_len);
   if (!d->workspace || (reinterpret_cast<uintptr_t>(d->workspace) & 255) || d->workspace_bytes < dls_attention_chunk_workspace_bytes(hd))
@@ -1305,7 +1312,7 @@ extern "C" int dls_attention_chunk(const dls_attention_chunk_desc* d, void* cuda
   a.page_shift = pt == 16 ? 4 : pt == 32 ? 5 : pt == 64 ? 6 : pt == 128 ? 7 : 8;
   a.n_pages = d->n_pages, a.max_pages = d->max_pages, a.pool_rows = d->n_pages * d->n_kv_heads * pt;
   a.causal = d->causal, a.window = d->window;
-  a.tpq = 128 / a.group, a.inv_group = (65536 + a.group - 1) / a.group;
+  a.tpq = tpq, a.inv_group = (65536 + a.group - 1) / a.group;
   a.c = (d->scale > 0.f ? d->scale : 1.0f / sqrtf((float)hd)) * 1.4426950408889634f;
   // a lane of the planning warp walks at most 4 sequences and 8 more tiles; its sums fit 32 bits
   a.small_plan = d->n_seqs <= 128 && d->n_tokens <= 8 * 2 * a.tpq && (long long)d->max_pages * pt <= 1 << 24;

@@ -6,6 +6,7 @@
 
 #include <algorithm>
 
+#include "../../include/dls.h"
 #include "common.cuh"
 
 namespace dls {
@@ -347,5 +348,14 @@ cudaError_t launch_fattn(const FattnArgs& a, const __half* k_pool, const __half*
 // Record a failure for dls_last_error(NULL) (calls without a model) and
 // return `code`.
 int report_error(int code, const char* fmt, ...);
+
+// Whether p (or NULL) stands at a multiple of `bytes`.
+inline bool aligned_to(const void* p, unsigned bytes) { return !(reinterpret_cast<uintptr_t>(p) & (bytes - 1)); }
+
+// A call without rows: its status word (or NULL) says so all the same.
+inline int empty_call(int32_t* status, void* stream, const char* what) {
+  const cudaError_t e = status ? cudaMemsetAsync(status, 0, sizeof(int32_t), static_cast<cudaStream_t>(stream)) : cudaSuccess;
+  return e == cudaSuccess ? DLS_OK : report_error(DLS_ERR_CUDA, "%s: cuda=%s", what, cudaGetErrorString(e));
+}
 
 }  // namespace dls

@@ -391,7 +391,9 @@ extern "C" int dls_qk_norm_rope(const dls_qk_norm_rope_desc* d, void* cuda_strea
   if (d->n_tokens < 0 || d->n_heads < 0 || d->n_kv_heads < 0 || d->n_heads > 4096 || d->n_kv_heads > 4096)
     return report_error(DLS_ERR_ARG, "qk_norm_rope: n_tokens=%d n_heads=%d n_kv_heads=%d", d->n_tokens, d->n_heads, d->n_kv_heads);
   if (d->n_tokens == 0 || d->n_heads + d->n_kv_heads == 0) return DLS_OK;
-  if (!d->positions) return report_error(DLS_ERR_ARG, "qk_norm_rope: positions=NULL");
+  if (!d->positions || !aligned_to(d->positions, 4) || !aligned_to(d->q_norm, 16) || !aligned_to(d->k_norm, 16))
+    return report_error(DLS_ERR_ARG, "qk_norm_rope: positions=%p q_norm=%p k_norm=%p (16-byte aligned norms)", (const void*)d->positions,
+                        (const void*)d->q_norm, (const void*)d->k_norm);
   if ((d->n_heads && (!rows_ok(d->q, d->q_stride, d->n_heads, d->head_dim, d->in_type) ||
                       !rows_ok(d->q_out, d->q_out_stride, d->n_heads, d->head_dim, d->out_type))) ||
       (d->n_kv_heads && (!rows_ok(d->k, d->k_stride, d->n_kv_heads, d->head_dim, d->in_type) ||
@@ -428,10 +430,13 @@ extern "C" int dls_kv_append(const dls_kv_append_desc* d, void* cuda_stream) {
       (long long)d->max_pages * pt > 0x7fffffff || (d->q && (d->n_heads < 1 || d->n_heads > 4096)))
     return report_error(DLS_ERR_ARG, "kv_append: n_tokens=%d n_seqs=%d n_heads=%d n_kv_heads=%d n_pages=%d max_pages=%d", d->n_tokens,
                         d->n_seqs, d->n_heads, d->n_kv_heads, d->n_pages, d->max_pages);
-  if (d->n_tokens == 0 || d->n_seqs == 0) return DLS_OK;
-  if (!d->page_table || !d->cu_q || !d->kv_len)
+  if (!aligned_to(d->status, 4)) return report_error(DLS_ERR_ARG, "kv_append: status=%p", (void*)d->status);
+  if (d->n_tokens == 0 || d->n_seqs == 0) return empty_call(d->status, cuda_stream, "kv_append");
+  if (!d->page_table || !d->cu_q || !d->kv_len || !aligned_to(d->page_table, 4) || !aligned_to(d->cu_q, 4) || !aligned_to(d->kv_len, 4))
     return report_error(DLS_ERR_ARG, "kv_append: page_table=%p cu_q=%p kv_len=%p", (const void*)d->page_table, (const void*)d->cu_q,
                         (const void*)d->kv_len);
+  if (!aligned_to(d->q_norm, 16) || !aligned_to(d->k_norm, 16))
+    return report_error(DLS_ERR_ARG, "kv_append: q_norm=%p k_norm=%p (16-byte aligned)", (const void*)d->q_norm, (const void*)d->k_norm);
   if (!rows_ok(d->k, d->k_stride, d->n_kv_heads, d->head_dim, d->in_type) ||
       !rows_ok(d->v, d->v_stride, d->n_kv_heads, d->head_dim, d->in_type) ||
       (d->q && (!rows_ok(d->q, d->q_stride, d->n_heads, d->head_dim, d->in_type) ||

@@ -206,6 +206,7 @@ def attention_decode_noalloc(q, k_pages, v_pages, page_table, lengths, o, n_batc
 
 
 # --- the paged cache: filling it and attending over it
+# (stream None is the default stream, as everywhere here: under torch.cuda.stream(s) or a capture pass that stream)
 
 DLS_F32, DLS_F16, DLS_BF16 = 1, 2, 3
 ROPE_PAIRINGS = {"adjacent": 0, "halves": 1}
@@ -278,6 +279,13 @@ def _call(fn, desc, stream, device):
             _check(fn(desc, _stream_handle(stream)))
 
 
+def _pairing(name):
+    number = ROPE_PAIRINGS.get(name)
+    if number is None:
+        raise ValueError(f"pairing: {name!r} ({' or '.join(ROPE_PAIRINGS)})")
+    return number
+
+
 def _inv_freq(inv_freq):
     """(array to keep, pointer, rot_dim) of host frequencies."""
     if inv_freq is None:
@@ -336,7 +344,7 @@ def qk_norm_rope(q, k, positions, inv_freq, q_out, k_out, *, q_norm=None, k_norm
     desc = _QK_NORM_ROPE.pack(qp, kp, qop, kop, qs, ks, qos, kos, _array(q_norm, "q_norm", f32, (hd,), device),
                               _array(k_norm, "k_norm", f32, (hd,), device),
                               _array(positions, "positions", _torch.int32, (n,), device), fp, n, qh, kh, hd, rot,
-                              ROPE_PAIRINGS[pairing], typ, out, eps)
+                              _pairing(pairing), typ, out, eps)
     _call((_lib or load()).dls_qk_norm_rope, desc, stream, device)
 
 
@@ -361,7 +369,7 @@ def kv_append(k, v, k_pages, v_pages, page_table, cu_q, kv_len, inv_freq, *, q=N
     desc = _KV_APPEND.pack(kp, vptr, qp, kpp, vpp, qop, ks, vs, qs, qos, _array(k_norm, "k_norm", f32, (hd,), device),
                            _array(q_norm, "q_norm", f32, (hd,), device), table, cu, kl, fp,
                            _array(status, "status", _torch.int32, (1,), device), n, seqs, qh, kvh, hd, rot,
-                           ROPE_PAIRINGS[pairing], typ, kv_type, pt, pages, most, eps)
+                           _pairing(pairing), typ, kv_type, pt, pages, most, eps)
     _call((_lib or load()).dls_kv_append, desc, stream, device)
 
 

@@ -438,8 +438,9 @@ int dls_kquant_gemv(int32_t type, const void* packed, int32_t rows, int32_t cols
  * Common to the three calls:
  *  - Tensors are device memory of the current device, rows (one token's
  *    heads, contiguous) `*_stride` elements apart, so slices of a fused
- *    projection's output can be passed as they are.  Pointers are 16-byte
- *    aligned and strides a multiple of 16 bytes (else DLS_ERR_ARG).
+ *    projection's output can be passed as they are.  Tensors, pools and
+ *    norms are 16-byte aligned, strides a multiple of 16 bytes and the other
+ *    arrays aligned to their elements (else DLS_ERR_ARG).
  *  - A batch is ragged: sequence b's new tokens are rows cu_q[b] ..
  *    cu_q[b + 1] - 1 (device int32 [n_seqs + 1], not decreasing, cu_q[0] >= 0)
  *    and kv_len[b] (device int32 [n_seqs]) counts the sequence's cached

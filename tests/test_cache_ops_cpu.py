@@ -102,6 +102,31 @@ def test_null_descriptors_and_empty_batches(lib):
     assert lib.dls_attention_chunk(dls._ATTENTION_CHUNK.pack(*{**CHUNK, "n_seqs": 0}.values()), None) == 0
 
 
+@pytest.mark.parametrize("name,over,word", [
+    # rows and weights are read 16 bytes at a time: a view that begins inside such a piece is refused
+    ("dls_qk_norm_rope", dict(q_norm=P + 4), "q_norm"), ("dls_qk_norm_rope", dict(k_norm=P + 8), "k_norm"),
+    ("dls_qk_norm_rope", dict(positions=P + 2), "positions"), ("dls_kv_append", dict(q_norm=P + 8), "q_norm"),
+    ("dls_kv_append", dict(k_norm=P + 4), "k_norm"), ("dls_kv_append", dict(cu_q=P + 1), "cu_q"),
+    ("dls_kv_append", dict(status=P + 2), "status"), ("dls_kv_append", dict(status=P + 2, n_tokens=0), "status"),
+    ("dls_attention_chunk", dict(kv_len=P + 2), "kv_len"), ("dls_attention_chunk", dict(page_table=P + 2), "page_table"),
+    ("dls_attention_chunk", dict(lse=P + 2), "lse"), ("dls_attention_chunk", dict(status=P + 1), "status"),
+    # in place, other strides; more tiles than an int counts should cu_q decrease all the time
+    ("dls_attention_chunk", dict(o_stride=8192), "in place"),
+    ("dls_attention_chunk", dict(n_tokens=1 << 30, n_seqs=4096), "too many"),
+    ("dls_attention_chunk", dict(n_tokens=(1 << 30) + 1), "n_tokens"),
+])
+def test_alignment_and_limits(lib, name, over, word):
+    fmt, base = {"dls_qk_norm_rope": (dls._QK_NORM_ROPE, ROPE), "dls_kv_append": (dls._KV_APPEND, APPEND),
+                 "dls_attention_chunk": (dls._ATTENTION_CHUNK, CHUNK)}[name]
+    refused(lib, name, fmt, base, over, word)
+
+
+def test_binding_refuses_an_unknown_pairing():
+    k = torch.zeros(3, 2, 64)
+    with pytest.raises(ValueError, match="pairing"):
+        dls.qk_norm_rope(k, None, torch.zeros(3, dtype=torch.int32), np.ones(32), k, None, pairing="split")
+
+
 def test_workspace_bytes(lib):
     for bad in (0, 8, 24, 136, 256, -16):
         assert dls.attention_chunk_workspace_bytes(bad) == 0

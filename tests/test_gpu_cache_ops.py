@@ -493,6 +493,17 @@ def test_attention_chunk_in_place(gpu_lib):
         assert torch.equal(x, o)
 
 
+def test_empty_calls_clear_the_status(gpu_lib):
+    B = Batch([(1, 20)], 2, 64, 16, torch.float16, 3)
+    x = torch.zeros(0, 2, 64, dtype=torch.float16, device="cuda")
+    status = torch.full((1,), 5, dtype=torch.int32, device="cuda")
+    dls.kv_append(x, x, B.k, B.v, B.table, B.cu_q, B.kv_len, None, status=status)
+    assert status.item() == 0
+    status.fill_(5)
+    dls.attention_chunk(x, B.k, B.v, B.table, B.cu_q, B.kv_len, x, workspace(64), status=status)
+    assert status.item() == 0
+
+
 def test_attention_chunk_two_calls_at_once(gpu_lib):
     """Calls on two streams, a workspace each, give what each gives alone."""
     made = []
