@@ -293,7 +293,11 @@ def _inv_freq(inv_freq):
     a = np.ascontiguousarray(inv_freq, dtype=np.float64)
     if a.ndim != 1:
         raise ValueError(f"inv_freq: shape {a.shape} ([rot_dim / 2])")
-    return a, a.__array_interface__["data"][0], 2 * a.size
+    try:
+        at = ctypes.addressof(ctypes.c_char.from_buffer(a))  # a third of what __array_interface__ takes
+    except (TypeError, ValueError):                          # read-only, or empty
+        at = a.__array_interface__["data"][0]
+    return a, at, 2 * a.size
 
 
 def _pools(k_pages, v_pages, page_table, cu_q, kv_len, device):

@@ -127,6 +127,16 @@ def test_binding_refuses_an_unknown_pairing():
         dls.qk_norm_rope(k, None, torch.zeros(3, dtype=torch.int32), np.ones(32), k, None, pairing="split")
 
 
+def test_frequencies_of_any_kind_of_array():
+    f = dls.rope_inv_freq(64, 10000.0)
+    fixed = f.copy()
+    fixed.flags.writeable = False
+    for given in (f, fixed, f.astype(np.float32), list(f), np.repeat(f, 2)[::2]):
+        a, at, rot = dls._inv_freq(given)
+        assert rot == 64 and at == a.ctypes.data and np.allclose(a, f, rtol=1e-7, atol=0)
+    assert dls._inv_freq(np.zeros(0))[2] == 0 and dls._inv_freq(None) == (None, 0, 0)
+
+
 def test_workspace_bytes(lib):
     for bad in (0, 8, 24, 136, 256, -16):
         assert dls.attention_chunk_workspace_bytes(bad) == 0
