@@ -30,8 +30,8 @@
 //
 // What bounds it, measured on one GB300 (8B and 70B head counts, head_dim
 // 128, bf16, GPU time):
-//  - prompts: 8192 tokens of 32 heads 397 us (1386 TFLOP/s), 2048 tokens of
-//    64 heads over 32768 1490 us (1430 TFLOP/s; cuBLAS reaches 1919 in a burst,
+//  - prompts: 8192 tokens of 32 heads 395 us (1394 TFLOP/s), 2048 tokens of
+//    64 heads over 32768 1480 us (1440 TFLOP/s; cuBLAS reaches 1919 in a burst,
 //    1698 under the power cap).  The MMA warp: the tensor pipe takes about two
 //    products ahead, and its barrier waits (about 100 cycles each) show
 //    between them; QK^T also reads 128 bytes a cycle of shared memory, all
