@@ -111,8 +111,9 @@ struct CCfg {
   static constexpr int kQ = 128 * HDP * 2;   // one slot's Q
   static constexpr int kKV = BK * HDP * 2;   // one K or V tile
   // Stages of 32 KB: a K or a V tile, or both of a narrow head's key tile.
-  // There one barrier serves both: the MMA warp's waits (about 100 cycles
-  // each) are then as long as its products.
+  // There one barrier serves both: apart, the MMA warp's waits (about 100
+  // cycles each) took as long as its products.  13 ragged chunks of 32 heads of
+  // 64: 98 us, 100 with K and V in stages of their own.
   static constexpr bool kTogether = HDP == 64;
   static constexpr int kUses = kTogether ? 1 : 2;  // ring uses of a key tile
   static constexpr int kStage = kTogether ? 2 * kKV : kKV;
@@ -501,7 +502,10 @@ __device__ __forceinline__ void hand_over(uint32_t bar, int lane) {
   if (lane == 0) mbar_arrive(bar);
 }
 
-// Weights of scores v[at .. at + 31], rounded to the operand's type, and their sum.
+// Weights of scores v[at .. at + 31] and their sum.  The weights are rounded to
+// 16 bits because a product with 16-bit V takes nothing wider (a second one
+// for the remainders would add half to the tensor work); their sum takes them
+// unrounded, so the roundings stay independent errors of half a step.
 template <typename T, int N>
 __device__ __forceinline__ void weights32(const uint32_t (&v)[N], int at, f2_t c2, f2_t r2, uint32_t (&w)[16], f2_t (&sum)[2]) {
 #pragma unroll
@@ -1314,7 +1318,8 @@ extern "C" int dls_attention_chunk(const dls_attention_chunk_desc* d, void* cuda
   a.causal = d->causal, a.window = d->window;
   a.tpq = tpq, a.inv_group = (65536 + a.group - 1) / a.group;
   a.c = (d->scale > 0.f ? d->scale : 1.0f / sqrtf((float)hd)) * 1.4426950408889634f;
-  // a lane of the planning warp walks at most 4 sequences and 8 more tiles; its sums fit 32 bits
+  // a lane of the planning warp walks at most 4 sequences and 8 more tiles; its sums fit 32 bits.
+  // One token over 2048: 15.5 us with the warp's plan, 16.2 with the block's; 64 tokens over 4096 each 218 and 220 us.
   a.small_plan = d->n_seqs <= 128 && d->n_tokens <= 8 * 2 * a.tpq && (long long)d->max_pages * pt <= 1 << 24;
   const CUtensorMapDataType dt = d->kv_type == DLS_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const uint32_t pr = pt < BK ? pt : BK;
