@@ -240,6 +240,44 @@ def test_kv_append_flags_what_does_not_fit(gpu_lib):
         dls.attention_status(torch.full((1,), 4, dtype=torch.int32, device="cuda"))
 
 
+def append_where(cu, kl, n_tokens, n_seqs, room):
+    """{(sequence, position): row} of the rows that an append with these lengths may write: rows of sequences that fit."""
+    return {(b, kl[b] - cu[b + 1] + t): t for b in range(n_seqs)
+            if 0 <= cu[b] <= cu[b + 1] <= n_tokens and cu[b + 1] - cu[b] <= kl[b] <= room for t in range(cu[b], cu[b + 1])}
+
+
+@pytest.mark.parametrize("cu,kl", [
+    ([0, 8, 0, 1], [8, 0, 32]), ([0, 6, 2, 3], [6, 4, 32]), ([0, 8, 0, 1, 0], [8, 0, 32, 5]), ([8, 0, 8, 0], [8, 8, 8]),
+    ([3, 1, 2, 0, 8], [32, 32, 32, 32]), ([0, 4, 4, 2, 8, 1, 5], [4, 0, 9, 17, 1, 32]), ([0, 8] * 40, [31, 32] * 39 + [32]),
+])
+def test_kv_append_where_cu_q_decreases(gpu_lib, cu, kl):
+    """No row goes to a slot that is not its own, and none looks past its sequence's row of the page table: the rows of the
+    table around the batch name pages of the pool too, which stay as they are."""
+    n, page, rows, most = len(kl), 16, 8, 2
+    pages = 2 * n + 8
+    table = torch.arange(pages, dtype=torch.int32, device="cuda").flip(0).reshape(-1, most).contiguous()  # 2 spare rows at each end
+    k = torch.arange(1.0, rows + 1, device="cuda")[:, None, None].expand(rows, 2, 32).contiguous()
+    pools = [torch.zeros(pages, 2, page, 32, dtype=torch.float16, device="cuda") for _ in range(2)]
+    qo = torch.zeros(rows, 2, 32, dtype=torch.float16, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    dls.kv_append(k, -k, *pools, table[2:2 + n], torch.tensor(cu, dtype=torch.int32, device="cuda"),
+                  torch.tensor(kl, dtype=torch.int32, device="cuda"), None, q=2 * k, q_out=qo, status=status)
+    torch.cuda.synchronize()
+    assert int(status) == 4
+    own = append_where(cu, kl, rows, n, most * page)
+    for pool, sign in zip(pools, (1.0, -1.0)):
+        allowed = torch.zeros(pages, page)
+        for (b, pos), t in own.items():
+            allowed[int(table[2 + b, pos // page]), pos % page] = sign * (t + 1)
+        got = pool.float().cpu()
+        assert torch.equal(got, got[:, :1, :, :1].expand_as(got))  # whole rows, every head
+        got = got[:, 0, :, 0]
+        assert bool(((got == 0) | (got == allowed)).all()), (got != 0).nonzero().tolist()
+    for t in range(rows):
+        x = qo[t].float().unique().tolist()
+        assert x == [0.0] or (x == [2.0 * (t + 1)] and t in own.values())
+
+
 # ---- attention -----------------------------------------------------------------------------------
 
 def attend64(B, q, heads, scale, causal, window):
