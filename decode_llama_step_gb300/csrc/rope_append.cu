@@ -201,13 +201,14 @@ __global__ void __launch_bounds__(RTHREADS, sizeof(IN) == 4 ? 5 : 6) rope_kernel
     const int b = seq_of(a.cu_q, a.n_seqs, t, lane);
     if (b >= a.n_seqs) return;  // behind the last sequence
     const int start = a.cu_q[b], end = a.cu_q[b + 1], kl = a.kv_len[b];
-    const long long p = (long long)kl - end + t, room = (long long)a.max_pages << a.page_shift;
+    const long long room = (long long)a.max_pages << a.page_shift;
     // before the first sequence, or lengths that do not fit (check_lengths
     // flags them).  Where cu_q decreases, seq_of's count can name a sequence
-    // that ends before t: only start <= t < end puts p below kl, and so inside
-    // the sequence's row of the page table.
-    if (t < start || t >= end || start < 0 || end > a.n_tokens || kl < 0 || kl > room || p < 0) return;
-    pos = (int)p;
+    // that ends before t: only start <= t < end and end - start <= kl <= room
+    // put the position into [0, kl), inside the sequence's row of the page
+    // table.  A sequence whose kl does not hold its chunk is left out whole.
+    if (t < start || t >= end || start < 0 || end > a.n_tokens || kl < end - start || kl > room) return;
+    pos = kl - (end - t);
     const int page = a.page_table[(size_t)b * a.max_pages + (pos >> a.page_shift)];
     if (page >= 0 && page < a.n_pages)
       slot = (((long long)page * a.n_kv) << a.page_shift) + (pos & ((1 << a.page_shift) - 1));

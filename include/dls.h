@@ -495,7 +495,9 @@ int dls_qk_norm_rope(const dls_qk_norm_rope_desc* d, void* cuda_stream);
  * rounded once to kv_type, V rounded to kv_type.  With q given, q_out =
  * the normed and rotated q in kv_type, as dls_attention_chunk reads it, in
  * the same pass.  A token whose page is missing keeps its q_out; its K and
- * V are dropped and flagged.  Two rows that name the same slot (pages shared
+ * V are dropped and flagged.  A sequence whose lengths do not fit is left
+ * out whole, its rows of q_out too; where cu_q decreases, rows of other
+ * sequences may be left out with it.  Two rows that name the same slot (pages shared
  * by two sequences that both append) leave one of the two in it. */
 typedef struct dls_kv_append_desc {
   const void* k;            /* in_type [n_tokens][n_kv_heads][head_dim] */

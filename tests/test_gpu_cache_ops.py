@@ -278,6 +278,28 @@ def test_kv_append_where_cu_q_decreases(gpu_lib, cu, kl):
         assert x == [0.0] or (x == [2.0 * (t + 1)] and t in own.values())
 
 
+@pytest.mark.parametrize("short", [0, 1, 4, 7])
+def test_kv_append_skips_a_sequence_shorter_than_its_chunk(gpu_lib, short):
+    """kv_len below the chunk's length is flagged, and no row of that sequence reaches a page or q_out; its neighbours do."""
+    cu, kl, rows, pages = [0, 3, 11, 13], [20, short, 2], 13, 6
+    table = torch.arange(pages, dtype=torch.int32, device="cuda").reshape(3, 2)
+    k = torch.arange(1.0, rows + 1, device="cuda")[:, None, None].expand(rows, 2, 32).contiguous()
+    pools = [torch.zeros(pages, 2, 16, 32, dtype=torch.float16, device="cuda") for _ in range(2)]
+    qo = torch.zeros(rows, 2, 32, dtype=torch.float16, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    dls.kv_append(k, -k, *pools, table, torch.tensor(cu, dtype=torch.int32, device="cuda"),
+                  torch.tensor(kl, dtype=torch.int32, device="cuda"), None, q=2 * k, q_out=qo, status=status)
+    torch.cuda.synchronize()
+    assert int(status) == 4
+    want = torch.zeros(pages, 16)
+    for (b, pos), t in append_where(cu, kl, rows, 3, 32).items():
+        want[2 * b + pos // 16, pos % 16] = t + 1
+    assert int((want != 0).sum()) == 5
+    for pool, sign in zip(pools, (1.0, -1.0)):
+        assert torch.equal(pool.float().cpu(), (sign * want)[:, None, :, None].expand(pages, 2, 16, 32))
+    assert qo[:, 0, 0].tolist() == [2.0, 4.0, 6.0] + [0.0] * 8 + [24.0, 26.0]
+
+
 # ---- attention -----------------------------------------------------------------------------------
 
 def attend64(B, q, heads, scale, causal, window):
