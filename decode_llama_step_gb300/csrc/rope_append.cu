@@ -7,8 +7,10 @@
 // Angles: the host turns inv_freq[i] into F[i] = round(inv_freq[i] / 2 pi *
 // 2^64), a turn being 2^64.  p * F[i] in 64-bit integers wraps modulo one
 // turn exactly, so the fraction of a turn has no cancellation however far
-// p is; its upper 32 bits go to sincospi.  F's own rounding (2^-53 of
-// inv_freq, a double) is all that grows with p.
+// p is; its upper 32 bits, rounded to the 24 of a float, go to sincospi.  All
+// that grows with p is F's own error: the roundings of 2 pi and of the
+// quotient, each 2^-53 of inv_freq at most, and 2^-65 of a turn (at position
+// 2^31 less than 2^-34 of one).
 //
 // What bounds it: bytes (each element is read once and written once).  A
 // lane owns sixteen elements of a head as two 8-element vectors whose
@@ -335,9 +337,12 @@ bool rows_ok(const void* p, long long stride, int heads, int hd, int type) {
 bool set_turns(RopeArgs* a, const double* inv_freq) {
   for (int i = 0; i < a->rot_dim / 2; ++i) {
     if (!isfinite(inv_freq[i])) return false;
-    double turns = inv_freq[i] / 6.283185307179586476925286766559;
+    // the fraction of |inv_freq|, which a double holds exactly; one of a small
+    // negative frequency would lie next to 1, on steps of 2^-53 whatever it is
+    double turns = fabs(inv_freq[i]) / 6.283185307179586476925286766559;
     turns -= floor(turns);
-    a->turn[i] = turns >= 1.0 ? 0ull : (unsigned long long)(turns * 18446744073709551616.0);  // 2^64
+    const unsigned long long f = (unsigned long long)rint(turns * 18446744073709551616.0);  // 2^64; turns <= 1 - 2^-53
+    a->turn[i] = inv_freq[i] < 0.0 ? 0ull - f : f;
   }
   return true;
 }

@@ -125,6 +125,19 @@ def test_qk_norm_rope_rows_of_zeros_and_infinities_stay_apart(gpu_lib):
     assert bool(((out.double() - want).abs()[ok] <= (33 * F32 * size)[ok] + 1e-38).all())
 
 
+@pytest.mark.parametrize("pairing", ["adjacent", "halves"])
+def test_negative_frequencies_are_the_turn_of_negative_positions(gpu_lib, pairing):
+    """f p is the same angle as (-f)(-p), bit by bit, for the slowest frequency at the farthest positions too."""
+    g = torch.Generator(device="cuda").manual_seed(17)
+    q = torch.randn(2000, 2, 128, generator=g, device="cuda")
+    pos = torch.randint(-(1 << 31) + 1, (1 << 31) - 1, (2000,), generator=g, device="cuda").to(torch.int32)
+    freq = dls.rope_inv_freq(128, 500000.0)
+    a, b = torch.empty_like(q), torch.empty_like(q)
+    dls.qk_norm_rope(q, None, pos, freq, a, None, pairing=pairing)
+    dls.qk_norm_rope(q, None, -pos, -freq, b, None, pairing=pairing)
+    assert torch.equal(a, b)
+
+
 # ---- a paged batch ----------------------------------------------------------------------------
 
 class Batch:
