@@ -435,8 +435,8 @@ extern "C" int dls_kv_append(const dls_kv_append_desc* d, void* cuda_stream) {
   const int pt = d->page_tokens;
   if (pt != 16 && pt != 32 && pt != 64 && pt != 128 && pt != 256)
     return report_error(DLS_ERR_ARG, "kv_append: page_tokens=%d (16, 32, 64, 128 or 256)", pt);
-  if (d->n_tokens < 0 || d->n_seqs < 0 || d->n_kv_heads < 1 || d->n_kv_heads > 4096 || d->n_pages < 1 || d->max_pages < 1 ||
-      (long long)d->max_pages * pt > 0x7fffffff || (d->q && (d->n_heads < 1 || d->n_heads > 4096)))
+  if (d->n_tokens < 0 || d->n_seqs < 0 || d->n_seqs > 1 << 30 || d->n_kv_heads < 1 || d->n_kv_heads > 4096 || d->n_pages < 1 ||
+      d->max_pages < 1 || (long long)d->max_pages * pt > 0x7fffffff || (d->q && (d->n_heads < 1 || d->n_heads > 4096)))
     return report_error(DLS_ERR_ARG, "kv_append: n_tokens=%d n_seqs=%d n_heads=%d n_kv_heads=%d n_pages=%d max_pages=%d", d->n_tokens,
                         d->n_seqs, d->n_heads, d->n_kv_heads, d->n_pages, d->max_pages);
   if (!aligned_to(d->status, 4)) return report_error(DLS_ERR_ARG, "kv_append: status=%p", (void*)d->status);

@@ -514,7 +514,8 @@ typedef struct dls_kv_append_desc {
   const int32_t* kv_len;
   const double* inv_freq;   /* HOST [rot_dim / 2] */
   int32_t* status;
-  int32_t n_tokens, n_seqs, n_heads, n_kv_heads;
+  int32_t n_tokens, n_seqs; /* n_seqs: 0..2^30 */
+  int32_t n_heads, n_kv_heads;
   int32_t head_dim, rot_dim, pairing; /* as above */
   int32_t in_type;          /* dls_dtype */
   int32_t kv_type;          /* DLS_F16 or DLS_BF16 */

@@ -121,6 +121,12 @@ def test_alignment_and_limits(lib, name, over, word):
     refused(lib, name, fmt, base, over, word)
 
 
+@pytest.mark.parametrize("n_seqs", [(1 << 30) + 1, 0x7fffffff - 30, 0x7fffffff])
+def test_kv_append_refuses_more_sequences_than_its_lookup_counts(lib, n_seqs):
+    """The search over cu_q probes up to 31 entries past the end before it looks at them: those numbers have to fit an int."""
+    refused(lib, "dls_kv_append", dls._KV_APPEND, APPEND, dict(n_seqs=n_seqs), f"n_seqs={n_seqs}")
+
+
 def test_binding_refuses_an_unknown_pairing():
     k = torch.zeros(3, 2, 64)
     with pytest.raises(ValueError, match="pairing"):
