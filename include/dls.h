@@ -454,7 +454,9 @@ int dls_kquant_gemv(int32_t type, const void* packed, int32_t rows, int32_t cols
  *    kv_len negative or above page_tokens * max_pages, an append with
  *    kv_len below the chunk's length) and bit 8 when a bounded wait ran out.  Read it with
  *    dls_attention_status.  What a flagged entry would have addressed is
- *    skipped, never accessed.
+ *    skipped, never accessed.  (Where cu_q decreases, other sequences may hold
+ *    the same row: an append leaves such rows out or takes them for one of
+ *    the sequences, attention leaves results of any of them there.)
  *  - Work is enqueued on cuda_stream (NULL: the default stream); nothing is
  *    allocated or synchronised.  Errors are in dls_last_error(NULL). */
 
@@ -494,11 +496,13 @@ int dls_qk_norm_rope(const dls_qk_norm_rope_desc* d, void* cuda_stream);
  * K normed (where k_norm is given), rotated by its cache position and
  * rounded once to kv_type, V rounded to kv_type.  With q given, q_out =
  * the normed and rotated q in kv_type, as dls_attention_chunk reads it, in
- * the same pass.  A token whose page is missing keeps its q_out; its K and
- * V are dropped and flagged.  A sequence whose lengths do not fit is left
- * out whole, its rows of q_out too; where cu_q decreases, rows of other
- * sequences may be left out with it.  Two rows that name the same slot (pages shared
- * by two sequences that both append) leave one of the two in it. */
+ * the same pass; q_out may be q itself (in_type = kv_type, the same stride)
+ * and must not overlap an input otherwise.  A token whose page is missing
+ * keeps its q_out; its K and V are dropped and flagged.  A sequence whose
+ * lengths do not fit is left out whole, its rows of q_out too; where cu_q
+ * decreases, rows of other sequences may be left out with it.  Two rows that
+ * name the same slot (pages shared by two sequences that both append) leave
+ * one of the two in it. */
 typedef struct dls_kv_append_desc {
   const void* k;            /* in_type [n_tokens][n_kv_heads][head_dim] */
   const void* v;

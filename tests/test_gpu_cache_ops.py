@@ -313,6 +313,25 @@ def test_kv_append_skips_a_sequence_shorter_than_its_chunk(gpu_lib, short):
     assert qo[:, 0, 0].tolist() == [2.0, 4.0, 6.0] + [0.0] * 8 + [24.0, 26.0]
 
 
+@pytest.mark.parametrize("pairing,rot", [("adjacent", 128), ("halves", 96)])
+def test_kv_append_turns_q_in_place(gpu_lib, pairing, rot):
+    """q_out = q: the bits of a call with an output of its own, rows outside the sequences untouched."""
+    B = Batch([(1, 40), (300, 300), (33, 65)], 2, 128, 32, torch.bfloat16, 12, first=2, pad=3)
+    x = (torch.randn(B.rows, 8 + 4, 128, generator=B.g, device="cuda") * 1.5).to(B.typ)
+    w = [1 + 0.1 * torch.randn(128, generator=B.g, device="cuda") for _ in range(2)]
+    freq, away = dls.rope_inv_freq(rot, 500000.0), torch.full((B.rows, 8, 128), 7.0, dtype=B.typ, device="cuda")
+    args = B.k, B.v, B.table, B.cu_q, B.kv_len, freq
+    dls.kv_append(x[:, 8:10], x[:, 10:], *args, q=x[:, :8], q_out=away, q_norm=w[0], k_norm=w[1], pairing=pairing)
+    k, v, y = B.k.clone(), B.v.clone(), x.clone()
+    dls.kv_append(y[:, 8:10], y[:, 10:], *args, q=y[:, :8], q_out=y[:, :8], q_norm=w[0], k_norm=w[1], pairing=pairing)
+    inside = slice(B.starts[0], B.starts[-1])
+    assert torch.equal(y[inside, :8], away[inside])
+    y[inside, :8] = x[inside, :8]
+    assert torch.equal(y, x)  # padding rows, k and v
+    for now, was in ((B.k, k), (B.v, v)):
+        assert torch.equal(now.view(torch.int16), was.view(torch.int16))
+
+
 # ---- attention -----------------------------------------------------------------------------------
 
 def attend64(B, q, heads, scale, causal, window):
@@ -638,6 +657,77 @@ def test_attention_chunk_matches_single_token_attention(gpu_lib):
     dls.attention_decode(q.float(), B.k, B.v, B.table, B.kv_len, o32, ws, n, 3, 32, 8, 128, 64, B.max_pages, 4)
     close_attend(B, o32.half(), None, attend64(B, q, 32, 128 ** -0.5, True, 0), 32)
     close_attend(B, o, None, attend64(B, q, 32, 128 ** -0.5, True, 0), 32)
+
+
+@pytest.mark.parametrize("cu,kl", [
+    ([0, 8, 0, 1], [8, 0, 32]), ([0, 6, 2, 3], [20, 4, 32]), ([0, 300, 290, 300], [320, 7, 40]), ([8, 0, 8, 0], [8, 9, 8]),
+    ([3, 1, 2, 0, 8], [32, 32, 32, 32]), ([0, 400, 8, 300, 0, 50], [400, 3, 310, 5, 200]),
+])
+def test_attention_chunk_where_cu_q_decreases(gpu_lib, cu, kl):
+    """Flagged; rows of no sequence stay as they are, and a row that one sequence alone holds has that sequence's result."""
+    rows, heads, hd = max(cu) + 2, 4, 64
+    # every sequence has keys for its length; those whose rows do not fit get none of the batch
+    B = Batch([(0, n) for n in kl], 2, hd, 16, torch.float16, 40)
+    B.fill()
+    B.cu_q = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    q = torch.randn(rows, heads, hd, generator=B.g, device="cuda").half()
+    o, status = torch.full_like(q, 7.0), torch.zeros(1, dtype=torch.int32, device="cuda")
+    dls.attention_chunk(q, B.k, B.v, B.table, B.cu_q, B.kv_len, o, workspace(hd), status=status)
+    torch.cuda.synchronize()
+    assert int(status) == 4
+    held = [sum(a <= t < b for a, b in zip(cu, cu[1:])) for t in range(rows)]
+    assert bool((o[torch.tensor(held) == 0] == 7).all())
+    for b, (first, end) in enumerate(zip(cu, cu[1:])):
+        if first >= end:
+            continue
+        B.lengths, B.starts, B.rows = [(0, 0)] * b + [(end - first, kl[b])], [first] * (b + 1) + [end], rows
+        want = attend64(B, q, heads, hd ** -0.5, True, 0)
+        alone = torch.tensor([t for t in range(first, end) if held[t] == 1], device="cuda", dtype=torch.long)
+        got = want[0].to(B.typ)
+        got[alone] = o[alone]
+        close_attend(B, got, None, want, heads)
+
+
+def border_keys(B, b, window):
+    """Keys of sequence b at the borders of key tiles, their halves and pages, of the cache and of its rows' windows."""
+    ql, kl = B.lengths[b]
+    keys = {0, kl - 1} | {j + x for j in range(0, kl, 128) for x in (0, 15, 16, 63, 64, 127)}
+    for pos in (kl - ql, kl - ql // 2 - 1, kl - 1):
+        keys |= {pos - 1, pos, pos + 1} | ({pos - window, pos - window + 1, pos - window + 2} if window else set())
+    return sorted(k for k in keys if 0 <= k < kl)
+
+
+@pytest.mark.parametrize("lengths,heads,kvh,hd,page,typ,window", [
+    ([(1, 20011)], 8, 2, 128, 64, "bf16", 0),
+    ([(1, 9000), (1, 33), (5, 8200)], 16, 2, 64, 128, "f16", 0),
+    ([(5, 4101), (1, 3661), (4, 1803), (60, 3001)], 16, 8, 128, 32, "f16", 0),
+    ([(700, 1300)], 4, 2, 128, 64, "bf16", 0),
+    ([(300, 1500), (1, 1200), (130, 900)], 8, 2, 64, 16, "f16", 333),
+    ([(1, 2000), (200, 1000)], 4, 4, 80, 256, "bf16", 129),
+])
+def test_attention_chunk_each_value_row_counts_once(gpu_lib, lengths, heads, kvh, hd, page, typ, window):
+    """V with one key for each column and zeros elsewhere: an output element is one key's weight times its value, held to a
+    relative bound, so that a row of V that is lost, taken twice, zeroed or taken from another place shows whatever the
+    length.  Flat scores keep every weight well above the roundings."""
+    B = Batch(lengths, kvh, hd, page, TYPES[typ], 33)
+    B.fill()
+    q = (0.3 * torch.randn(B.rows, heads, hd, generator=B.g, device="cuda")).to(B.typ)
+    o, lse, ws = torch.empty_like(q), torch.empty(B.rows, heads, device="cuda"), workspace(hd)
+    keys = []
+    for b in range(len(lengths)):
+        border = torch.tensor(border_keys(B, b, window))
+        keys.append(border[torch.randperm(len(border), generator=torch.Generator().manual_seed(b))])
+    value = (32.0 + torch.arange(hd, device="cuda")).to(B.typ)  # (whole numbers up to 159: exact)
+    for part in range(-(-max(len(k) for k in keys) // hd)):
+        for b, (_, kl) in enumerate(lengths):
+            p, s = B.slots(b, 0, kl)
+            B.v[p, :, s] = 0.0
+            some = keys[b][torch.arange(part * hd, part * hd + hd) % len(keys[b])].cuda()
+            B.v[p[some], :, s[some], torch.arange(hd, device="cuda")] = value[:, None]
+        dls.attention_chunk(q, B.k, B.v, B.table, B.cu_q, B.kv_len, o, ws, lse=lse, window=window)
+        want = attend64(B, q, heads, hd ** -0.5, True, window)
+        close_attend(B, o, lse, want, heads)
+        assert torch.equal(o == 0, want[0] == 0)  # every key that a row sees, and no other
 
 
 # ---- together -------------------------------------------------------------------------------------
