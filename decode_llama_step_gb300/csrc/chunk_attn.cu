@@ -40,10 +40,12 @@
 //    barriers between the halves of a product (1530), a third score buffer
 //    for narrow heads, softmax in rolled chunks (1573).  Moving R at every new
 //    maximum (kGrow = 0): 475 and 1600 us.
-//  - single tokens: 64 of 64 heads over 4096 cached on average 222 us, 6.3 TB/s
-//    (a plain copy moves 6.8): the cache is read once.
+//  - single tokens: 64 of 64 heads over up to 8192 cached (5301 on average,
+//    1.39 GB) 222 us, 6.3 TB/s (a plain copy moves 6.8): the cache is read once.
 //  - small calls: latencies in a row (lengths, page table, first tiles,
-//    epilogue, arrival, join): one token over 2048 cached 15.7 us.
+//    epilogue, arrival, join): one token over 2048 cached 15.7 us (16.9 with
+//    the cache in HBM).  The split-K kernel of dls_attention_decode, which
+//    takes one fp32 row a sequence, has a shorter chain: 10.6 (11.8) there.
 //
 // Warps: 0 copies (TMA), 1 MMA, 2 the CTA's piece list, 4-7 / 8-11 softmax of
 // slot 0 / 1.  Every wait is bounded (2 s) and sets an abort flag.
@@ -1319,7 +1321,7 @@ extern "C" int dls_attention_chunk(const dls_attention_chunk_desc* d, void* cuda
   a.tpq = tpq, a.inv_group = (65536 + a.group - 1) / a.group;
   a.c = (d->scale > 0.f ? d->scale : 1.0f / sqrtf((float)hd)) * 1.4426950408889634f;
   // a lane of the planning warp walks at most 4 sequences and 8 more tiles; its sums fit 32 bits.
-  // One token over 2048: 15.5 us with the warp's plan, 16.2 with the block's; 64 tokens over 4096 each 218 and 220 us.
+  // One token over 2048: 15.5 us with the warp's plan, 16.2 with the block's; 64 over up to 8192 (5301 on average) 218 and 220 us.
   a.small_plan = d->n_seqs <= 128 && d->n_tokens <= 8 * 2 * a.tpq && (long long)d->max_pages * pt <= 1 << 24;
   const CUtensorMapDataType dt = d->kv_type == DLS_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const uint32_t pr = pt < BK ? pt : BK;

@@ -22,9 +22,10 @@
 // token's cos and sin serve every head of the walk; the lanes that hold the
 // same pairs of different heads share the work of them.
 // Measured: 8192 bf16 tokens of 72 heads of 128, normed and turned, 57.7 us
-// (5.2 TB/s; 44.5 at the copy rate); an append of 7600 tokens with q, k and v
-// in bf16 50.9 us (4.7 TB/s).  Without any arithmetic the same walk takes as
-// long: what is left is the walk's thousands of streams, one a warp.  A CTA
+// (5.2 TB/s; 44.5 at the copy rate); an append of 9762 tokens with q, k and v
+// in bf16 (32 + 2 x 8 heads of 128) 50.5 us (4.8 TB/s).  Without any arithmetic
+// the same walk takes as long: what is left is the walk's thousands of
+// streams, one a warp, a limit of this walk and not of the operator.  A CTA
 // that walks four tokens together reaches 49 us as a bare copy, but 67 with
 // the norm, whose exchanges then stand in the way; two passes fetched ahead
 // cost the warps that they gain.
@@ -354,8 +355,10 @@ int launch_rope(RopeArgs& a, int in_type, int out_type, const char* what, cudaSt
   a.heads_total = a.src[0].heads + a.src[1].heads + a.src[2].heads;
   const int hpw = 32 >> a.lanes_log2;
   a.passes = (a.heads_total + hpw - 1) / hpw;
-  // Passes of a warp: few enough for three rounds of the 24 warps an SM holds.
-  // 8192 bf16 tokens of 72 heads of 128: 57.7 us with 2 warps a token (9
+  // Passes of a warp: few enough for three rounds of the 24 warps that an SM
+  // holds with 16-bit inputs (with fp32 ones it holds 20, so the rounds are a
+  // little more: 1021 tokens of 40 fp32 heads of 64 run 5105 warps of one pass
+  // in 1.7 rounds, 7.7 us over a floor of 3.1).  8192 bf16 tokens of 72 heads of 128: 57.7 us with 2 warps a token (9
   // passes each), 59.9 with one (18; the last round a quarter full), 59.5 and
   // 66.5 with 3 and 4 (each repeats the token's start); 46.6 for a plain copy
   // of the bytes.

@@ -328,7 +328,8 @@ def qk_norm_rope(q, k, positions, inv_freq, q_out, k_out, *, q_norm=None, k_norm
                  stream=None):
     """Per-head RMSNorm (where a norm is given) and rotation of q and k [tokens, heads, head_dim] into q_out and
     k_out, which may be q and k themselves.  Either pair may be None.  positions: device int32 [tokens]; inv_freq:
-    host float64 [rot_dim / 2], or None for no rotation."""
+    host float64 [rot_dim / 2], or None for no rotation.  stream None is the default stream, whatever torch's current
+    one is: under torch.cuda.stream(s) or a capture pass that stream."""
     one, one_out = (q, q_out) if q is not None else (k, k_out)
     if one is None or (q is None) != (q_out is None) or (k is None) != (k_out is None):
         raise ValueError("q with q_out, k with k_out, or both")
@@ -356,7 +357,8 @@ def kv_append(k, v, k_pages, v_pages, page_table, cu_q, kv_len, inv_freq, *, q=N
               eps=1e-5, pairing="adjacent", status=None, stream=None):
     """Append a ragged chunk's keys (normed where k_norm is given, rotated by their cache position) and values
     [tokens, kv_heads, head_dim] to the pages; with q, q_out = q normed and rotated in the same pass, in the
-    cache's type.  cu_q: device int32 [sequences + 1], kv_len: device int32 [sequences], the new tokens counted."""
+    cache's type; q_out may be q where it has that type.  cu_q: device int32 [sequences + 1], kv_len: device int32
+    [sequences], the new tokens counted.  stream None is the default stream, as in qk_norm_rope."""
     if (q is None) != (q_out is None):
         raise ValueError("q with q_out, or neither")
     typ, kv_type, device = _dtype(k, "k"), _dtype(k_pages, "k_pages"), k.get_device()
@@ -385,7 +387,8 @@ def attention_chunk(q, k_pages, v_pages, page_table, cu_q, kv_len, o, workspace,
                     window=0, status=None, stream=None):
     """Attention of ragged chunks of new tokens (q, o [tokens, heads, head_dim] in the cache's type) over the paged
     cache; o may be q.  workspace: a uint8 tensor of attention_chunk_workspace_bytes(head_dim) zeros, kept from call to
-    call, one for each of the calls that may overlap.  lse: fp32 [tokens, heads] or None.  scale 0: 1 / sqrt(head_dim)."""
+    call, one for each of the calls that may overlap.  lse: fp32 [tokens, heads] or None.  scale 0: 1 / sqrt(head_dim).
+    stream None is the default stream, as in qk_norm_rope."""
     kv_type, device = _dtype(k_pages, "k_pages"), q.get_device()
     pages, kvh, pt, hd, kpp, vpp, table, most, cu, kl, seqs = _pools(k_pages, v_pages, page_table, cu_q, kv_len, device)
     n, heads, _ = _dims(q, "q")
