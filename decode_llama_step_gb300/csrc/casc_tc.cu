@@ -281,15 +281,10 @@ __global__ void __launch_bounds__(CTHR, 1) casc_tc_kernel(const __grid_constant_
       if (ok && !twait(smem_u32(&sh.o_full[b]), (jj >> 1) & 1, &sh.abort)) ok = false;
       if (ok) {
         tc_fence_after();
+        uint32_t v[OH];  // this part's columns in one load
+        tmem_read(trow + CBK + b * HD + hf * OH, v);
 #pragma unroll
-        uint32_t v[OH / 16][16];  // every load of this part's columns in flight per wait
-#pragma unroll
-        for (int c = 0; c < OH / 16; ++c) tmem_ld16(trow + CBK + b * HD + hf * OH + c * 16, v[c]);
-        tmem_wait_ld();
-#pragma unroll
-        for (int c = 0; c < OH / 16; ++c)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) o[c * 16 + i] = fmaf(o[c * 16 + i], alpha, __uint_as_float(v[c][i]));
+        for (int i = 0; i < OH; ++i) o[i] = fmaf(o[i], alpha, __uint_as_float(v[i]));
         tc_fence_before();
       }
       __syncwarp();
@@ -304,18 +299,14 @@ __global__ void __launch_bounds__(CTHR, 1) casc_tc_kernel(const __grid_constant_
       // P buffer j & 1: its previous tile's P V (j - 2) has completed, as
       // has every MMA issued before this tile's S = Q K^T
       const uint32_t pbuf = pbase + 2 * (j & 1) * C::kP;
-      uint32_t sv[KH / 16][16];
-      if (ok) {
-#pragma unroll
-        for (int c = 0; c < KH / 16; ++c) tmem_ld16(trow + hf * KH + c * 16, sv[c]);
-        tmem_wait_ld();
-      }
+      uint32_t sv[KH];
+      if (ok) tmem_read(trow + hf * KH, sv);
       float mx = -INFINITY;
 #pragma unroll
       for (int hh = 0; hh < KH / 16; ++hh)
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-          if (ok && kbase + hh * 16 + i < n) mx = fmaxf(mx, __uint_as_float(sv[hh][i]) * scale);
+          if (ok && kbase + hh * 16 + i < n) mx = fmaxf(mx, __uint_as_float(sv[hh * 16 + i]) * scale);
       // the row's max over all its parts
       float* xm = xch + (j & 1) * HPR * CROWS;
       xm[hf * CROWS + r] = mx;
@@ -331,7 +322,7 @@ __global__ void __launch_bounds__(CTHR, 1) casc_tc_kernel(const __grid_constant_
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const bool in = ok && live && kbase + c1 * 16 + i < n && m_new != -INFINITY;
-          p[i] = in ? expf(__uint_as_float(sv[c1][i]) * scale - m_new) : 0.f;
+          p[i] = in ? expf(__uint_as_float(sv[c1 * 16 + i]) * scale - m_new) : 0.f;
           sum += p[i];
         }
         // keys 16 (hf KH / 16 + c1) .. +15 = 16-byte chunks 2 (hf KH / 16 + c1) and +1 of the row

@@ -227,8 +227,7 @@ __global__ void __launch_bounds__(FTHREADS, 1) fattn_kernel(const __grid_constan
 #pragma unroll 1
       for (int c = 0; c < FBK / 16; ++c) {
         uint32_t v[16];
-        tmem_ld16(trow + c * 16, v);
-        tmem_wait_ld();
+        tmem_read(trow + c * 16, v);
 #pragma unroll
         for (int i = 0; i < 16; ++i)
           if (kbase + c * 16 + i <= qpos) mx = fmaxf(mx, __uint_as_float(v[i]));
@@ -239,8 +238,7 @@ __global__ void __launch_bounds__(FTHREADS, 1) fattn_kernel(const __grid_constan
 #pragma unroll 1
       for (int c = 0; c < FBK / 16; ++c) {
         uint32_t v[16];
-        tmem_ld16(trow + c * 16, v);
-        tmem_wait_ld();
+        tmem_read(trow + c * 16, v);
         float p[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
@@ -279,8 +277,7 @@ __global__ void __launch_bounds__(FTHREADS, 1) fattn_kernel(const __grid_constan
 #pragma unroll
       for (int c = 0; c < HD / 16; ++c) {
         uint32_t v[16];
-        tmem_ld16(trow + 128 + c * 16, v);
-        tmem_wait_ld();
+        tmem_read(trow + 128 + c * 16, v);
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[c * 16 + i] = fmaf(o[c * 16 + i], alpha, __uint_as_float(v[i]));
       }

@@ -305,8 +305,7 @@ __global__ void __launch_bounds__(GTHREADS) tgemm_kernel(const __grid_constant__
 #pragma unroll 1
       for (int c0 = 0; c0 < CW; c0 += 8) {
         uint32_t v[8];
-        tmem_ld8(taddr + c0, v);
-        tmem_wait_ld();
+        tmem_read(taddr + c0, v);
         if (!ok || n0 + cb + c0 >= a.T) continue;
 #pragma unroll
         for (int j = 0; j < 8; ++j) epi_store<EPI>(a, n0 + cb + c0 + j, m, w.rows, __uint_as_float(v[j]));
@@ -316,8 +315,7 @@ __global__ void __launch_bounds__(GTHREADS) tgemm_kernel(const __grid_constant__
 #pragma unroll 1
       for (int c0 = 0; c0 < CW; c0 += 8) {
         uint32_t v[8];
-        tmem_ld8(taddr + c0, v);
-        tmem_wait_ld();
+        tmem_read(taddr + c0, v);
         if (!ok) continue;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {

@@ -286,9 +286,7 @@ __global__ void __launch_bounds__(CTHREADS, 1) cgemm_kernel(const __grid_constan
       const float2 dd = sc[rg * CBM + row];
       const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16) + 256 * rg + 32 * grp;
       uint32_t v[32], u[32];
-      tmem_ld32(tbase, v);        // block 0 of the step
-      tmem_ld32(tbase + 128, u);  // block 1
-      tmem_wait_ld();
+      tmem_read2(tbase, v, tbase + 128, u);  // blocks 0 and 1 of the step
 #pragma unroll
       for (int j = 0; j < 32; ++j)
         y[j] = fmaf(dd.y, __uint_as_float(u[j]), fmaf(dd.x, __uint_as_float(v[j]), y[j]));

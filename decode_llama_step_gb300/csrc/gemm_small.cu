@@ -318,16 +318,13 @@ __global__ void __launch_bounds__(STHREADS) sgemm_kernel(const __grid_constant__
            swait(smem_u32(&sh.tfull[rg]), (i / kSR) & 1, &sh.abort);
       if (!ok) break;
       tc_fence_after();
-      uint32_t v[16], u[16];
-      const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + 32 * rg;
-      tmem_ld16(taddr, v);
-      tmem_ld16(taddr + 16, u);
-      tmem_wait_ld();
+      uint32_t v[32];
+      tmem_read(tmem + ((uint32_t)(q * 32) << 16) + 32 * rg, v);
       const float2 dd = sc[rg * SBM + row];
 #pragma unroll
       for (int t = 0; t < 8; ++t) {
         y[t] = fmaf(dd.x, __uint_as_float(v[t]) + __uint_as_float(v[t + 8]), y[t]);
-        y[t] = fmaf(dd.y, __uint_as_float(u[t]) + __uint_as_float(u[t + 8]), y[t]);
+        y[t] = fmaf(dd.y, __uint_as_float(v[t + 16]) + __uint_as_float(v[t + 24]), y[t]);
       }
       tc_fence_before();
       __syncwarp();
