@@ -67,8 +67,15 @@ constexpr int MAXC = 152;        // CTAs at most (one per SM)
 constexpr int CTHREADS = 384;
 constexpr int CWARPS = CTHREADS / 32;
 constexpr int QDEPTH = 4;        // pieces the list runs ahead
-constexpr int kMinSteps = 2;     // units of a range at least (a key tile per slot of a split tile)
-constexpr int kTileCost = 3;     // what a tile of work costs beyond its key tiles, in key tiles
+// Units of a range at least: a key tile per slot of a split tile.  One token
+// over 2048: 15.3 us with two, 15.7 with one (on twice the SMs, but twice the
+// partials to join), 16.3 with four; the larger calls do not notice.
+constexpr int kMinSteps = 2;
+// What a tile of work costs beyond its key tiles (Q, first product, epilogue,
+// join), in key tiles: one value for both head widths.  0, 2, 3 and 5 of them:
+// prompt of 8192 458, 399, 398, 406 us; of 2048 80, 61, 62, 64; eight verify
+// passes 37.8, 34.3, 33.3, 35.3; mixed batch of narrow heads 96, 96, 96, 97.
+constexpr int kTileCost = 3;
 constexpr float kGrow = 8.f;     // log2 the maximum may exceed the reference by
 constexpr float kShift = 7.f;    // weights are kept as 2^(c s - R + 7): at most 2^15 in fp16, with 7 more binades below
 constexpr uint64_t kWaitNsC = 2000000000ull;
