@@ -307,14 +307,14 @@ def _plain_reserve(s):
     fits = (new > 0) & (kv + new <= most * page)
     need = torch.where(fits, ((kv + new + page - 1) // page - held).clamp(min=0), 0)
     fits &= (need == 0) | (need.cumsum(0) <= avail)
-    need = torch.where(fits, need, 0)
-    i = j - held[:, None]
-    fresh = (i >= 0) & (i < need[:, None])
-    table[fresh] = stack[(avail - 1 - (need.cumsum(0) - need)[:, None] - i)[fresh]]
-    # rows
+    # rows, while they last; who gets none takes no pages
     rows = s["positions"].shape[0]
     q = torch.where(fits, new, 0)
     q = torch.where(q.cumsum(0) <= rows, q, 0)
+    need = torch.where(q > 0, need, 0)
+    i = j - held[:, None]
+    fresh = (i >= 0) & (i < need[:, None])
+    table[fresh] = stack[(avail - 1 - (need.cumsum(0) - need)[:, None] - i)[fresh]]
     s["cu_q"][1:] = q.cumsum(0)
     s["kv_len_out"].copy_(torch.where(new < 0, 0, kv + q))
     s["held_out"].copy_(torch.where(new < 0, 0, held + need))
