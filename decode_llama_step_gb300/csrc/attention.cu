@@ -737,6 +737,8 @@ extern "C" int dls_attention_status(const int32_t* status, void* cuda_stream) {
     return dls::report_error(DLS_ERR_CUDA, "attention status: reading the status word failed");
   if (v & dls::kTimeout)
     return dls::report_error(DLS_ERR_TIMEOUT, "attention: a bounded wait ran out device_status=0x%x", v);
+  if (v == dls::kNoRoom)
+    return dls::report_error(DLS_ERR_CAPACITY, "attention: device_status=0x%x (16=a request left out for want of pages or rows)", v);
   if (v)
     return dls::report_error(DLS_ERR_STATE, "attention: device_status=0x%x (1=missing page 4=length outside "
                              "1..page_tokens*max_pages)", v);

@@ -29,6 +29,7 @@ enum StatusBits : int32_t {
   kBadToken = 2,  // token id outside [0, vocab)
   kBadPos = 4,    // position outside the rope table / context
   kTimeout = 8,   // a bounded wait on an mbarrier ran out
+  kNoRoom = 16,   // a request was left out for want of free pages or rows
 };
 
 // One weight matrix in the kernels' layout: codes and fp16 scales in two

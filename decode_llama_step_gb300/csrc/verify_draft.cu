@@ -1,0 +1,344 @@
+// Verification of drafted tokens against the target's probabilities, from
+// given random numbers.
+//
+// Mathematics, per sequence: its rows are the current token and the drafts;
+// target row r gives p (and draft row r gives q, from which the token of row r
+// + 1 was drawn).  Draft x of row r + 1 stands while u[r] q(x) < p(x).  At the
+// first that does not, the token comes from w = max(p - q, 0); where all stand,
+// from w = p of the last row:
+//   token = the least t with  sum_{j <= t} w_j > v sum_j w_j.
+// Without draft probabilities the draft was certain (q(x) = 1): x stands while
+// u < p(x), and w is p without x.
+//
+// Which token it is must not depend on how the sums are formed: 128256
+// borders, most of them of unlikely tokens, lie so close that the rounding of
+// a 32-bit sum (or of p - q in 32 bits) moves the pick past some of them.  So
+// p and q become whole numbers of 2^-60, exact for all of a float's 24 bits
+// from 2^-36 on, and everything after is integer arithmetic: sums in any order
+// give the same bits, and v sum w is compared exactly (its floor, against
+// whole sums).  u q(x) < p(x) is exact in a double.
+//
+// What bounds it: the bytes of one row of p and one of q a sequence; the rows
+// of drafts that stand are never read but at one token.  A cluster of CTAs
+// takes a sequence, each a slice of the vocabulary: sums, exchanged through
+// distributed shared memory, then the CTA whose slice holds the border finds
+// the warp, the lane and the token by prefix sums of the (cached) slice.
+#include <cuda_bf16.h>
+#include <math.h>
+
+#include "../../include/dls.h"
+#include "kernels.h"
+
+namespace dls {
+
+namespace {
+
+constexpr int VTHREADS = 512;
+constexpr int VWARPS = VTHREADS / 32;
+constexpr int kMaxCluster = 8;
+typedef unsigned long long u64_t;
+
+struct VerifyArgs {
+  const int32_t *tokens, *cu_q, *kv_len;
+  const float *accept, *pick;
+  const void *target, *draft;
+  long long target_stride, draft_stride;
+  int32_t *out_tokens, *n_accepted, *kv_len_out, *status;
+  int n_tokens, n_seqs, vocab;
+  int wide;  // rows of both lie alike to 16 bytes (or there is no draft)
+};
+
+__device__ __forceinline__ float as_float(float x) { return x; }
+__device__ __forceinline__ float as_float(__half x) { return __half2float(x); }
+__device__ __forceinline__ float as_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+// p in whole numbers of 2^-60, cut off; outside [0, 1] the nearer end, NaN 0.
+__device__ __forceinline__ u64_t fixed60(float p) {
+  const unsigned b = __float_as_uint(fminf(fmaxf(p, 0.f), 1.f)), e = b >> 23;
+  // 1.f at e = 127; below the normal range the hidden bit is wrong, and the shift takes everything away
+  const unsigned hi = ((b & 0x7fffffu) | 0x800000u) << 5;  // mantissa * 2^37, upper word: p = 1 is 2^60
+  u64_t r;
+  asm("shr.u64 %0, %1, %2;" : "=l"(r) : "l"((u64_t)hi << 32), "r"(127u - e));
+  return r;
+}
+
+// floor(v s) below s, v in [0, 1)
+__device__ __forceinline__ u64_t part_of(u64_t s, float v) {
+  const unsigned b = __float_as_uint(fminf(fmaxf(v, 0.f), 0x1.fffffep-1f)), e = b >> 23;
+  const unsigned m = e ? (b & 0x7fffffu) | 0x800000u : b & 0x7fffffu;
+  const unsigned sh = 150u - (e ? e : 1u);  // v = m 2^-sh, 24 <= sh
+  const u64_t lo = s * m, hi = __umul64hi(s, m);
+  if (sh < 64) return (hi << (64 - sh)) | (lo >> sh);
+  return sh < 128 ? hi >> (sh - 64) : 0;
+}
+
+// A row in pieces of V elements: piece k holds elements k V - off ..., off such
+// that pieces lie at 16-byte boundaries (V = 1: single elements).
+template <typename T, int V>
+struct Piece16 {
+  float x[V];
+  __device__ __forceinline__ void load(const T* row, int first, int vocab) {
+    if constexpr (V > 1) {
+      if (first >= 0 && first + V <= vocab) {
+        const uint4 w = __ldg(reinterpret_cast<const uint4*>(row + first));
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[i] = __uint_as_float(u[i]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const unsigned short h = (unsigned short)(i & 1 ? u[i >> 1] >> 16 : u[i >> 1]);
+            if constexpr (__is_same(T, __half)) x[i] = __half2float(__ushort_as_half(h));
+            else x[i] = __uint_as_float((uint32_t)h << 16);
+          }
+        }
+        return;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) x[i] = first + i >= 0 && first + i < vocab ? as_float(row[first + i]) : 0.f;
+  }
+};
+
+// Weight of an element: of p alone, of p without token x, or of what p has over q.
+enum What { ALONE, WITHOUT, OVER };
+
+template <typename T, int V>
+__device__ __forceinline__ void weigh(const T* p, const T* q, int first, int vocab, int what, int x, u64_t (&w)[V], u64_t* plain) {
+  Piece16<T, V> a, b;
+  a.load(p, first, vocab);
+  if (what == OVER) b.load(q, first, vocab);
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const u64_t fp = fixed60(a.x[i]);
+    if (plain) *plain += fp;
+    w[i] = fp;
+    if (what == OVER) {
+      const u64_t fq = fixed60(b.x[i]);
+      w[i] = fp > fq ? fp - fq : 0;
+    } else if (what == WITHOUT && first + i == x) {
+      w[i] = 0;
+    }
+  }
+}
+
+__device__ __forceinline__ u64_t warp_sum64(u64_t v) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+template <typename T, int V>
+__global__ void __launch_bounds__(VTHREADS) verify_kernel(const __grid_constant__ VerifyArgs a) {
+  __shared__ u64_t warp_sums[VWARPS][2];
+  __shared__ __align__(16) u64_t cta_sum[2];
+  __shared__ u64_t all[kMaxCluster][2];
+  __shared__ int s_stop;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  unsigned rank, ctas;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ctas));
+  const int b = blockIdx.x / ctas;
+  const int start = a.cu_q[b], end = a.cu_q[b + 1];
+  const bool bad = start < 0 || end < start || end > a.n_tokens;
+  if (bad || start == end) {  // (the whole cluster alike)
+    if (rank == 0 && tid == 0) {
+      a.n_accepted[b] = 0;
+      if (a.kv_len_out) a.kv_len_out[b] = a.kv_len[b];
+      if (bad && a.status) atomicOr(a.status, kBadPos);
+    }
+    return;
+  }
+  const T *target = static_cast<const T*>(a.target), *draft = static_cast<const T*>(a.draft);
+
+  // the first row whose draft does not stand, or the last row
+  if (warp == 0) {
+    int stop = end - 1;
+    bool strange = false;
+    for (int r = start; r < end - 1; r += 32) {
+      const int row = r + lane;
+      bool falls = false;
+      if (row < end - 1) {
+        const int x = a.tokens[row + 1];
+        const bool in = x >= 0 && x < a.vocab;
+        strange |= !in;
+        double p = 0., q = 1.;
+        if (in) {
+          p = as_float(target[(size_t)row * a.target_stride + x]);
+          if (draft) q = as_float(draft[(size_t)row * a.draft_stride + x]);
+        }
+        falls = !(in && (double)a.accept[row] * q < p);
+      }
+      const unsigned hit = __ballot_sync(0xffffffffu, falls);
+      if (hit) {
+        stop = r + __ffs(hit) - 1;
+        break;
+      }
+    }
+    if (lane == 0) s_stop = stop;
+    if (strange && rank == 0 && a.status) atomicOr(a.status, kBadToken);
+  }
+  __syncthreads();
+  const int stop = s_stop;
+  const bool refused = stop < end - 1;
+  if (rank == 0) {
+    for (int r = start + tid; r < end; r += VTHREADS)
+      if (r != stop) a.out_tokens[r] = r < stop ? a.tokens[r + 1] : -1;
+    if (tid == 0) {
+      a.n_accepted[b] = stop - start;
+      if (a.kv_len_out) a.kv_len_out[b] = a.kv_len[b] - (end - 1 - stop);
+    }
+  }
+
+  // sums: warp's run of pieces inside the CTA's slice of the row
+  const T* const p = target + (size_t)stop * a.target_stride;
+  const T* const q = draft ? draft + (size_t)stop * a.draft_stride : nullptr;
+  const int what = !refused ? ALONE : draft ? OVER : WITHOUT;
+  const int x = refused ? a.tokens[stop + 1] : -1;
+  const int off = V > 1 ? (int)((reinterpret_cast<uintptr_t>(p) & 15) / sizeof(T)) : 0;
+  const int pieces = (a.vocab + off + V - 1) / V;
+  const int per_warp = (pieces + (int)ctas * VWARPS - 1) / ((int)ctas * VWARPS);
+  const int c0 = (int)min((long long)(rank * VWARPS + warp) * per_warp, (long long)pieces), c1 = min(c0 + per_warp, pieces);
+  u64_t sum = 0, plain = 0;
+#pragma unroll 4
+  for (int c = c0 + lane; c < c1; c += 32) {
+    u64_t w[V];
+    weigh<T, V>(p, q, c * V - off, a.vocab, what, x, w, &plain);
+#pragma unroll
+    for (int i = 0; i < V; ++i) sum += w[i];
+  }
+  sum = warp_sum64(sum);
+  plain = warp_sum64(plain);
+  if (lane == 0) warp_sums[warp][0] = sum, warp_sums[warp][1] = plain;
+  __syncthreads();
+  if (warp == 0) {
+    u64_t s = lane < VWARPS ? warp_sums[lane][0] : 0, t = lane < VWARPS ? warp_sums[lane][1] : 0;
+    s = warp_sum64(s);
+    t = warp_sum64(t);
+    if (lane == 0) cta_sum[0] = s, cta_sum[1] = t;
+  }
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  if (tid < (int)ctas * 2) {
+    uint32_t at;
+    u64_t v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(&cta_sum[tid & 1])), "r"(tid >> 1));
+    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(at) : "memory");
+    all[tid >> 1][tid & 1] = v;
+  }
+  // (the sums of this CTA may be read until everyone has arrived here)
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  u64_t total = 0, before = 0;
+  int col = 0;
+  for (int k = 0; k < (int)ctas; ++k) {
+    if (k == (int)rank) before = total;
+    total += all[k][0];
+  }
+  int how = what;
+  if (total == 0) {  // nothing over the draft's: p itself
+    col = 1, how = ALONE;
+    for (int k = 0; k < (int)ctas; ++k) {
+      if (k == (int)rank) before = total;
+      total += all[k][1];
+    }
+  }
+  if (total == 0) {
+    if (rank == 0 && tid == 0) {
+      a.out_tokens[stop] = -1;
+      if (a.status) atomicOr(a.status, kBadToken);
+    }
+    return;
+  }
+  const u64_t border = part_of(total, a.pick[b]);
+  // the warp whose run passes the border
+  for (int w = 0; w < warp; ++w) before += warp_sums[w][col];
+  if (!(before <= border && before + warp_sums[warp][col] > border)) return;
+  for (int c = c0; c < c1; c += 32) {
+    u64_t w[V], mine = 0;
+    if (c + lane < c1) {
+      weigh<T, V>(p, q, (c + lane) * V - off, a.vocab, how, x, w, nullptr);
+#pragma unroll
+      for (int i = 0; i < V; ++i) mine += w[i];
+    }
+    u64_t pre = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const u64_t y = __shfl_up_sync(0xffffffffu, pre, o);
+      if (lane >= o) pre += y;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, before + pre > border);
+    if (hit) {
+      if (lane == __ffs(hit) - 1) {
+        u64_t at = before + pre - mine;
+        int t = (c + lane) * V - off;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          at += w[i];
+          if (at <= border) ++t;
+        }
+        a.out_tokens[stop] = t;
+      }
+      return;
+    }
+    before += __shfl_sync(0xffffffffu, pre, 31);
+  }
+}
+
+template <typename T>
+cudaError_t launch_verify(const VerifyArgs& a, unsigned ctas, cudaStream_t s) {
+  cudaLaunchConfig_t c{};
+  cudaLaunchAttribute at[1];
+  c.gridDim = dim3(ctas * (unsigned)a.n_seqs), c.blockDim = dim3(VTHREADS), c.stream = s;
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = ctas, at[0].val.clusterDim.y = 1, at[0].val.clusterDim.z = 1;
+  c.attrs = at, c.numAttrs = 1;
+  return a.wide ? cudaLaunchKernelEx(&c, verify_kernel<T, 16 / (int)sizeof(T)>, a) : cudaLaunchKernelEx(&c, verify_kernel<T, 1>, a);
+}
+
+}  // namespace
+
+}  // namespace dls
+
+extern "C" int dls_verify_draft(const dls_verify_draft_desc* d, void* cuda_stream) {
+  using namespace dls;
+  if (!d) return report_error(DLS_ERR_ARG, "verify_draft: desc=NULL");
+  const int size = d->prob_type == DLS_F32 ? 4 : d->prob_type == DLS_F16 || d->prob_type == DLS_BF16 ? 2 : 0;
+  if (!size) return report_error(DLS_ERR_ARG, "verify_draft: prob_type=%d", d->prob_type);
+  if (d->n_tokens < 0 || d->n_seqs < 0 || d->n_seqs > 1 << 24 || d->vocab < 1 || d->vocab > 1 << 30)
+    return report_error(DLS_ERR_ARG, "verify_draft: n_tokens=%d n_seqs=%d (at most 2^24) vocab=%d (1 to 2^30)", d->n_tokens, d->n_seqs, d->vocab);
+  if (d->target_stride < d->vocab || d->target_stride > 1ll << 32 || (d->draft && (d->draft_stride < d->vocab || d->draft_stride > 1ll << 32)))
+    return report_error(DLS_ERR_ARG, "verify_draft: target_stride=%lld draft_stride=%lld (vocab=%d to 2^32)", (long long)d->target_stride,
+                        (long long)d->draft_stride, d->vocab);
+  if (!aligned_to(d->status, 4)) return report_error(DLS_ERR_ARG, "verify_draft: status=%p", (void*)d->status);
+  if (d->n_seqs == 0) return empty_call(d->status, cuda_stream, "verify_draft");
+  if (!d->cu_q || !d->n_accepted || (!d->kv_len != !d->kv_len_out))
+    return report_error(DLS_ERR_ARG, "verify_draft: cu_q=%p n_accepted=%p kv_len=%p kv_len_out=%p (both lengths, or neither)",
+                        (const void*)d->cu_q, (void*)d->n_accepted, (const void*)d->kv_len, (void*)d->kv_len_out);
+  if (d->n_tokens && (!d->tokens || !d->target || !d->accept || !d->pick || !d->out_tokens))
+    return report_error(DLS_ERR_ARG, "verify_draft: tokens=%p target=%p accept=%p pick=%p out_tokens=%p", (const void*)d->tokens, d->target,
+                        (const void*)d->accept, (const void*)d->pick, (void*)d->out_tokens);
+  const void* words[] = {d->tokens, d->cu_q, d->accept, d->pick, d->kv_len, d->out_tokens, d->n_accepted, d->kv_len_out};
+  for (const void* w : words)
+    if (!aligned_to(w, 4)) return report_error(DLS_ERR_ARG, "verify_draft: %p is not aligned to its 4-byte elements", w);
+  if (!aligned_to(d->target, size) || !aligned_to(d->draft, size))
+    return report_error(DLS_ERR_ARG, "verify_draft: target=%p draft=%p are not aligned to their elements", d->target, d->draft);
+  if (d->out_tokens && d->out_tokens == d->tokens) return report_error(DLS_ERR_ARG, "verify_draft: out_tokens cannot be tokens");
+  VerifyArgs a{};
+  a.tokens = d->tokens, a.cu_q = d->cu_q, a.kv_len = d->kv_len, a.accept = d->accept, a.pick = d->pick;
+  a.target = d->target, a.draft = d->draft, a.target_stride = d->target_stride, a.draft_stride = d->draft_stride;
+  a.out_tokens = d->out_tokens, a.n_accepted = d->n_accepted, a.kv_len_out = d->kv_len_out, a.status = d->status;
+  a.n_tokens = d->n_tokens, a.n_seqs = d->n_seqs, a.vocab = d->vocab;
+  // rows r of both begin at the same place of a 16-byte piece for every r
+  a.wide = !d->draft || (!((reinterpret_cast<uintptr_t>(d->target) ^ reinterpret_cast<uintptr_t>(d->draft)) & 15) &&
+                         !(((d->target_stride - d->draft_stride) * size) & 15));
+  unsigned ctas = kMaxCluster;
+  while (ctas > 1 && ((long long)(ctas / 2) * d->n_seqs >= 304 || d->vocab < 2048 * (int)ctas)) ctas /= 2;
+  cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
+  cudaError_t e = cudaSuccess;
+  if (a.status) e = cudaMemsetAsync(a.status, 0, sizeof(int32_t), s);
+  if (e == cudaSuccess)
+    e = d->prob_type == DLS_F32 ? launch_verify<float>(a, ctas, s) : d->prob_type == DLS_F16 ? launch_verify<__half>(a, ctas, s)
+                                                                                              : launch_verify<__nv_bfloat16>(a, ctas, s);
+  if (e != cudaSuccess) return report_error(DLS_ERR_CUDA, "verify_draft: cuda=%s", cudaGetErrorString(e));
+  return DLS_OK;
+}

@@ -90,6 +90,10 @@ _SIGS = {
     "dls_kv_append": (ctypes.c_int, [vp, vp]),
     "dls_attention_chunk": (ctypes.c_int, [vp, vp]),
     "dls_attention_chunk_workspace_bytes": (ctypes.c_uint64, [i32]),
+    "dls_kv_reserve": (ctypes.c_int, [vp, vp]),
+    "dls_kv_append8": (ctypes.c_int, [vp, vp]),
+    "dls_attention_chunk8": (ctypes.c_int, [vp, vp]),
+    "dls_verify_draft": (ctypes.c_int, [vp, vp]),
     "dls_kquant_packed_bytes": (ctypes.c_uint64, [i32, i32, i32]),
     "dls_kquant_pack": (ctypes.c_int, [i32, vp, i32, i32, vp, vp]),
     "dls_kquant_gemv": (ctypes.c_int, [i32, vp, i32, i32, vp, vp, vp, vp]),
@@ -401,6 +405,146 @@ def attention_chunk(q, k_pages, v_pages, page_table, cu_q, kv_len, o, workspace,
                                  _array(status, "status", _torch.int32, (1,), device), qs, os_, n, seqs, heads, kvh, hd, pt,
                                  pages, most, kv_type, 1 if causal else 0, window, scale)
     _call((_lib or load()).dls_attention_chunk, desc, stream, device)
+
+
+# --- the paged cache in 8 bits, and a step whose lengths stay on the device
+
+DLS_E4M3, DLS_I8 = 4, 5
+_KV_RESERVE = struct.Struct("@14P5i")
+_KV_APPEND8 = struct.Struct("@6P2q6P12if")
+_ATTENTION_CHUNK8 = struct.Struct("@11PQP2q13if")
+_VERIFY_DRAFT = struct.Struct("@11P2q4i")
+_code_types = {}
+
+
+def _codes(k_pages, v_pages, k_scales, v_scales, device):
+    """(code type, block_tokens, scales' pointers) of pools of codes."""
+    if not _code_types:
+        _types()
+        _code_types.update({_torch.float8_e4m3fn: DLS_E4M3, _torch.int8: DLS_I8})
+    code, shape, grid = _code_types.get(k_pages.dtype), k_pages.shape, k_scales.shape
+    if code is None:
+        raise ValueError(f"k_pages: type {k_pages.dtype} (float8_e4m3fn or int8)")
+    if len(shape) != 4 or len(grid) != 3 or grid[:2] != shape[:2] or not grid[2] or shape[2] % grid[2]:
+        raise ValueError(f"k_scales: shape {tuple(grid)} ([pages, kv_heads, page_tokens / block_tokens] of pages {tuple(shape)})")
+    f32 = _torch.float32
+    return (code, shape[2] // grid[2], _array(k_scales, "k_scales", f32, grid, device),
+            _array(v_scales, "v_scales", f32, grid, device))
+
+
+def kv_reserve(new_len, kv_len, held, page_table, free_pages, free_count, kv_len_out, held_out, free_count_out, cu_q,
+               page_tokens, *, positions=None, slots=None, seq_ids=None, max_rows=None, status=None, stream=None):
+    """Pages and rows of a batch from its requests' lengths (device int32 [sequences]): new_len tokens join kv_len ones
+    (negative: the request is over, its pages go back on the stack free_pages, whose free_count lowest entries are
+    free).  Fresh pages go into page_table [sequences, pages], rows into cu_q [sequences + 1] and, where given,
+    positions, slots (page * page_tokens + offset) and seq_ids [rows].  kv_len_out, held_out and free_count_out may be
+    their inputs.  max_rows: the arrays' length where one is given.  stream None is the default stream, as in
+    qk_norm_rope."""
+    _dtypes or _types()
+    i32_, device = _torch.int32, new_len.get_device()
+    if page_table.dim() != 2:
+        raise ValueError(f"page_table: shape {tuple(page_table.shape)} ([sequences, pages])")
+    n, most = page_table.shape
+    one = positions if positions is not None else slots if slots is not None else seq_ids
+    if one is not None:
+        if max_rows is None:
+            max_rows = one.shape[0]
+        elif max_rows > one.shape[0]:
+            raise ValueError(f"max_rows: {max_rows}, the arrays hold {one.shape[0]}")
+        rows = tuple(one.shape)
+    else:
+        rows = ()
+        if max_rows is None:
+            raise ValueError("max_rows, or one of positions, slots and seq_ids")
+    if free_pages.dim() != 1:
+        raise ValueError(f"free_pages: shape {tuple(free_pages.shape)} ([pages])")
+    pages = free_pages.shape[0]
+    desc = _KV_RESERVE.pack(
+        _array(new_len, "new_len", i32_, (n,), device), _array(kv_len, "kv_len", i32_, (n,), device),
+        _array(held, "held", i32_, (n,), device), _array(page_table, "page_table", i32_, (n, most), device),
+        _array(free_pages, "free_pages", i32_, (pages,), device), _array(free_count, "free_count", i32_, (1,), device),
+        _array(kv_len_out, "kv_len_out", i32_, (n,), device), _array(held_out, "held_out", i32_, (n,), device),
+        _array(free_count_out, "free_count_out", i32_, (1,), device), _array(cu_q, "cu_q", i32_, (n + 1,), device),
+        _array(positions, "positions", i32_, rows, device), _array(slots, "slots", i32_, rows, device),
+        _array(seq_ids, "seq_ids", i32_, rows, device), _array(status, "status", i32_, (1,), device), n, max_rows,
+        page_tokens, pages, most)
+    _call((_lib or load()).dls_kv_reserve, desc, stream, device)
+
+
+def kv_append8(k, v, k_pages, v_pages, k_scales, v_scales, page_table, cu_q, kv_len, inv_freq, *, k_norm=None, eps=1e-5,
+               pairing="adjacent", status=None, stream=None):
+    """Append a ragged chunk's keys (normed where k_norm is given, rotated by their cache position) and values
+    [tokens, kv_heads, head_dim] to pages of codes (float8_e4m3fn or int8), with a scale for each block of tokens and
+    head: k_scales and v_scales, fp32 [pages, kv_heads, page_tokens / block_tokens].  cu_q: device int32
+    [sequences + 1], kv_len: device int32 [sequences], the new tokens counted.  stream None is the default stream, as
+    in qk_norm_rope."""
+    typ, device = _dtype(k, "k"), k.get_device()
+    code, block, ksp, vsp = _codes(k_pages, v_pages, k_scales, v_scales, device)
+    pages, kvh, pt, hd, kpp, vpp, table, most, cu, kl, seqs = _pools(k_pages, v_pages, page_table, cu_q, kv_len, device)
+    n, tin = _dims(k, "k")[0], k.dtype
+    kp, ks = _rows(k, "k", n, kvh, hd, tin, device)
+    vptr, vs = _rows(v, "v", n, kvh, hd, tin, device)
+    keep, fp, rot = _inv_freq(inv_freq)
+    desc = _KV_APPEND8.pack(kp, vptr, kpp, vpp, ksp, vsp, ks, vs, _array(k_norm, "k_norm", _torch.float32, (hd,), device),
+                            table, cu, kl, fp, _array(status, "status", _torch.int32, (1,), device), n, seqs, kvh, hd, rot,
+                            _pairing(pairing), typ, code, pt, block, pages, most, eps)
+    _call((_lib or load()).dls_kv_append8, desc, stream, device)
+
+
+def attention_chunk8(q, k_pages, v_pages, k_scales, v_scales, page_table, cu_q, kv_len, o, workspace, *, lse=None, scale=0.0,
+                     causal=True, window=0, status=None, stream=None):
+    """attention_chunk over pages of codes (float8_e4m3fn or int8) with a scale for each block of tokens and head; q and
+    o [tokens, heads, head_dim] in float16 or bfloat16.  workspace: as attention_chunk's, which may be the same one."""
+    typ, device = _dtype(q, "q"), q.get_device()
+    code, block, ksp, vsp = _codes(k_pages, v_pages, k_scales, v_scales, device)
+    pages, kvh, pt, hd, kpp, vpp, table, most, cu, kl, seqs = _pools(k_pages, v_pages, page_table, cu_q, kv_len, device)
+    n, heads, _ = _dims(q, "q")
+    qp, qs = _rows(q, "q", n, heads, hd, q.dtype, device)
+    op, os_ = _rows(o, "o", n, heads, hd, q.dtype, device)
+    if not workspace.is_contiguous() or workspace.get_device() != device:
+        raise ValueError(f"workspace: on {workspace.device}: contiguous, and all tensors on one CUDA device")
+    desc = _ATTENTION_CHUNK8.pack(qp, kpp, vpp, ksp, vsp, table, cu, kl, op,
+                                  _array(lse, "lse", _torch.float32, (n, heads), device), workspace.data_ptr(),
+                                  workspace.nbytes, _array(status, "status", _torch.int32, (1,), device), qs, os_, n, seqs,
+                                  heads, kvh, hd, pt, block, pages, most, typ, code, 1 if causal else 0, window, scale)
+    _call((_lib or load()).dls_attention_chunk8, desc, stream, device)
+
+
+def _prob_rows(t, name, n, vocab, dtype, device):
+    """(pointer, elements between rows) of probabilities [n, vocab] whose rows are contiguous; None -> (0, 0)."""
+    if t is None:
+        return 0, 0
+    shape, stride = t.shape, t.stride()
+    if shape != (n, vocab) or t.dtype != dtype:
+        raise ValueError(f"{name}: {t.dtype} {tuple(shape)}, wanted {dtype} {(n, vocab)}")
+    if stride[1] != 1 and vocab > 1:
+        raise ValueError(f"{name}: a row's probabilities must be contiguous (strides {stride})")
+    if t.get_device() != device:
+        raise ValueError(f"{name}: on {t.device}: all tensors must be on one CUDA device")
+    return t.data_ptr(), (stride[0] if n > 1 else vocab)
+
+
+def verify_draft(tokens, target, cu_q, accept, pick, out_tokens, n_accepted, *, draft=None, kv_len=None, kv_len_out=None,
+                 status=None, stream=None):
+    """Drafted tokens against the target's probabilities [rows, vocab] (float32, float16 or bfloat16), from given random
+    numbers: accept fp32 [rows], pick fp32 [sequences].  tokens, out_tokens: int32 [rows], a sequence's rows its current
+    token and its drafts; draft: the probabilities that row r + 1's token was drawn from in row r, None for certain
+    ones.  n_accepted: int32 [sequences]; kv_len_out (may be kv_len) = kv_len less the drafts that do not stand."""
+    if len(target.shape) != 2:
+        raise ValueError(f"target: shape {tuple(target.shape)} ([rows, vocab])")
+    typ, device = _dtype(target, "target"), target.get_device()
+    n, vocab = target.shape
+    seqs = n_accepted.shape[0] if n_accepted.dim() == 1 else -1
+    i32_, f32 = _torch.int32, _torch.float32
+    tp, ts = _prob_rows(target, "target", n, vocab, target.dtype, device)
+    dp, ds = _prob_rows(draft, "draft", n, vocab, target.dtype, device)
+    desc = _VERIFY_DRAFT.pack(
+        _array(tokens, "tokens", i32_, (n,), device), tp, dp, _array(cu_q, "cu_q", i32_, (seqs + 1,), device),
+        _array(accept, "accept", f32, (n,), device), _array(pick, "pick", f32, (seqs,), device),
+        _array(kv_len, "kv_len", i32_, (seqs,), device), _array(out_tokens, "out_tokens", i32_, (n,), device),
+        _array(n_accepted, "n_accepted", i32_, (seqs,), device), _array(kv_len_out, "kv_len_out", i32_, (seqs,), device),
+        _array(status, "status", i32_, (1,), device), ts, ds, n, seqs, vocab, typ)
+    _call((_lib or load()).dls_verify_draft, desc, stream, device)
 
 
 DLS_Q4_K = 12

@@ -360,9 +360,10 @@ size_t dls_attention_workspace_bytes(int32_t n_batch, int32_t n_heads, int32_t n
 
 /* Wait for cuda_stream, read the status word of a standalone attention call
  * and turn it into a status code: DLS_OK (0), DLS_ERR_TIMEOUT (bit 8: a
- * bounded wait ran out), DLS_ERR_STATE (bits 1 or 4: a missing page or a bad
- * length; the output is not meaningful), with the flags in
- * dls_last_error(NULL). */
+ * bounded wait ran out), DLS_ERR_STATE (bits 1, 2 or 4: a missing page, a bad
+ * token or a bad length; the output is not meaningful), DLS_ERR_CAPACITY (bit
+ * 16 alone: dls_kv_reserve left a request out for want of pages or rows), with
+ * the flags in dls_last_error(NULL). */
 int dls_attention_status(const int32_t* status, void* cuda_stream);
 
 /* Allocation-free dls_attention_decode.  The pages have no counterpart of
@@ -577,6 +578,179 @@ typedef struct dls_attention_chunk_desc {
 int dls_attention_chunk(const dls_attention_chunk_desc* d, void* cuda_stream);
 /* Workspace bytes (0 for a bad head_dim). */
 uint64_t dls_attention_chunk_workspace_bytes(int32_t head_dim);
+
+/* ---- the paged cache in 8 bits, and a step whose lengths stay on the device ----- */
+
+/* A serving step over a cache held in 8 bits: pages reserved and rows laid out
+ * from the requests' lengths, keys and values quantised into their blocks,
+ * attention over the codes, drafted tokens verified (SwarmKV page, sections
+ * 4 and 10: branches continue over a bounded pool of pages; the engine page,
+ * sections 3.5 and 5.3: drafted tokens verified by the full model).  What is
+ * common to the calls of the section before holds here too; every length is
+ * read on the device, so one captured graph can run step after step:
+ *   dls_kv_reserve -> (projections, dls_qk_norm_rope) -> dls_kv_append8 ->
+ *   dls_attention_chunk8 -> ... -> dls_verify_draft -> dls_kv_reserve ...
+ * The pools hold one byte a value, [n_pages][n_kv_heads][page_tokens][head_dim],
+ * and a scale for each block of block_tokens tokens and KV head, fp32
+ * [n_pages][n_kv_heads][page_tokens / block_tokens]: value = scale * code. */
+
+/* Codes (added to dls_dtype's numbers): OCP e4m3 (4 bits of exponent, 3 of
+ * mantissa, up to 448, no infinity), or whole numbers -127..127. */
+#define DLS_E4M3 4
+#define DLS_I8 5
+
+/* Pages and rows of a batch from its requests' lengths.  new_len[b] is the
+ * number of new tokens of sequence b (0: not in this batch); negative: the
+ * request is over and its pages go back.  In the order of the sequences:
+ *  - the pages of requests that are over go on top of the stack free_pages
+ *    (its free_count lowest entries are the free pages) and serve this call;
+ *  - a request that needs pages beyond the `held` ones it has takes them from
+ *    the top; where they run out, it and every later request that needs one is
+ *    left out (requests that need none are not);
+ *  - rows are given to those that remain while max_rows lasts; the first that
+ *    does not fit and every later one is left out.
+ * Left-out requests keep their state and have no rows (cu_q[b + 1] = cu_q[b]).
+ * Row r of sequence b stands at positions[r] = kv_len[b] + r - cu_q[b], in slot
+ * slots[r] = page * page_tokens + offset (-1 where the table names no page of
+ * the pool), seq_ids[r] = b.  Rows from cu_q[n_seqs] on are left as they are.
+ * kv_len_out counts the new tokens, as the other calls want it; it, held_out
+ * and free_count_out may be their inputs.  held[b] may be more than kv_len[b]
+ * needs (dls_verify_draft takes tokens back, never pages).
+ * status: bit 4 for lengths that do not fit (kv_len, held or free_count outside
+ * their range, held below what kv_len needs, kv_len + new_len above page_tokens *
+ * max_pages; such a request is left out, and is not given back if over; or more
+ * pages coming back than the stack holds, of which the rest is dropped), bit 16 when a
+ * request was left out for want of pages or rows, bit 1 for a slot of -1. */
+typedef struct dls_kv_reserve_desc {
+  const int32_t* new_len;    /* device [n_seqs] */
+  const int32_t* kv_len;     /* device [n_seqs]: cached tokens */
+  const int32_t* held;       /* device [n_seqs]: entries of its table row that are its pages */
+  int32_t* page_table;       /* device [n_seqs][max_pages]; fresh pages are entered */
+  int32_t* free_pages;       /* device [n_pages] */
+  const int32_t* free_count; /* device [1] */
+  int32_t* kv_len_out;
+  int32_t* held_out;
+  int32_t* free_count_out;
+  int32_t* cu_q;             /* device [n_seqs + 1] */
+  int32_t* positions;        /* device [max_rows], or NULL */
+  int32_t* slots;
+  int32_t* seq_ids;
+  int32_t* status;
+  int32_t n_seqs;            /* 0..DLS_MAX_CHUNK_SEQS */
+  int32_t max_rows;          /* 0..2^30 */
+  int32_t page_tokens;       /* 16, 32, 64, 128 or 256 */
+  int32_t n_pages, max_pages; /* times page_tokens below 2^31 */
+} dls_kv_reserve_desc;
+int dls_kv_reserve(const dls_kv_reserve_desc* d, void* cuda_stream);
+
+/* dls_kv_append into pools of codes: K normed (where k_norm is given) and
+ * rotated, V as it is, both divided by their block's scale and rounded once
+ * (to the nearest, ties to even).  The scale is a power of two, 2^-64 to 2^64:
+ * the least under which the largest magnitude of the block's rows fits the
+ * codes.  A block that already holds earlier tokens of the sequence keeps its scale
+ * (any positive one) unless the new rows need a larger one; then its earlier
+ * codes are divided by the growth and rounded again.  NaN becomes NaN (e4m3) or 0 and does not count for
+ * the scale, an infinity the largest code.  Codes and scales of blocks that
+ * get no row are left as they are.  (dls_qk_norm_rope takes q, at
+ * dls_kv_reserve's positions.) */
+typedef struct dls_kv_append8_desc {
+  const void* k;            /* in_type [n_tokens][n_kv_heads][head_dim] */
+  const void* v;
+  void* k_pages;            /* pools of codes */
+  void* v_pages;
+  float* k_scales;          /* device fp32 [n_pages][n_kv_heads][page_tokens / block_tokens] */
+  float* v_scales;
+  int64_t k_stride, v_stride;
+  const float* k_norm;      /* device fp32 [head_dim], or NULL */
+  const int32_t* page_table; /* device [n_seqs][max_pages] */
+  const int32_t* cu_q;
+  const int32_t* kv_len;
+  const double* inv_freq;   /* HOST [rot_dim / 2] */
+  int32_t* status;
+  int32_t n_tokens;         /* 0..2^30 */
+  int32_t n_seqs;           /* 0..2^30 */
+  int32_t n_kv_heads;
+  int32_t head_dim, rot_dim, pairing; /* as in dls_kv_append */
+  int32_t in_type;          /* dls_dtype */
+  int32_t code_type;        /* DLS_E4M3 or DLS_I8 */
+  int32_t page_tokens;      /* 16, 32, 64, 128 or 256 */
+  int32_t block_tokens;     /* the same, at most page_tokens */
+  int32_t n_pages, max_pages;
+  float eps;
+} dls_kv_append8_desc;
+int dls_kv_append8(const dls_kv_append8_desc* d, void* cuda_stream);
+
+/* dls_attention_chunk over pools of codes: the same rows, masks, guarantees
+ * and workspace (one serves both calls, not at the same time).  q and o are
+ * q_type.  Scales may be any from 2^-64 to 2^64 (others, and NaN, count as the nearer end);
+ * codes enter the products exactly, the softmax weights times V's scale are
+ * rounded to q_type.  NaN codes count as the other call's NaN. */
+typedef struct dls_attention_chunk8_desc {
+  const void* q;            /* q_type [n_tokens][n_heads][head_dim], rotated */
+  const void* k_pages;      /* pools of codes */
+  const void* v_pages;
+  const float* k_scales;    /* device fp32 [n_pages][n_kv_heads][page_tokens / block_tokens] */
+  const float* v_scales;
+  const int32_t* page_table; /* device [n_seqs][max_pages] */
+  const int32_t* cu_q;
+  const int32_t* kv_len;
+  void* o;                  /* q_type [n_tokens][n_heads][head_dim] */
+  float* lse;               /* device fp32 [n_tokens][n_heads], or NULL */
+  void* workspace;          /* dls_attention_chunk_workspace_bytes(head_dim) */
+  uint64_t workspace_bytes;
+  int32_t* status;
+  int64_t q_stride, o_stride;
+  int32_t n_tokens, n_seqs, n_heads, n_kv_heads, head_dim; /* as in dls_attention_chunk */
+  int32_t page_tokens;      /* 16, 32, 64, 128 or 256 */
+  int32_t block_tokens;     /* the same, at most page_tokens */
+  int32_t n_pages, max_pages;
+  int32_t q_type;           /* DLS_F16 or DLS_BF16 */
+  int32_t code_type;        /* DLS_E4M3 or DLS_I8 */
+  int32_t causal, window;
+  float scale;              /* > 0; 0 = 1 / sqrt(head_dim) */
+} dls_attention_chunk8_desc;
+int dls_attention_chunk8(const dls_attention_chunk8_desc* d, void* cuda_stream);
+
+/* Drafted tokens against the target's probabilities, from given random
+ * numbers.  Sequence b's rows cu_q[b] .. cu_q[b + 1] - 1 are what a verify pass
+ * ran on: its current token, then its drafts.  target row r holds the target's
+ * probabilities after tokens[r], draft row r those that tokens[r + 1] was drawn
+ * from (a sequence's last draft row is not read).  tokens[r + 1] stands while
+ * accept[r] * draft[r][x] < target[r][x] for it and all before it.  Then one
+ * more token is taken, from the target's probabilities of the last row where
+ * all drafts stand, else from max(target - draft, 0) of the row of the first
+ * that does not: the least t whose running sum exceeds pick[b] times the whole.
+ * draft = NULL: the drafts were certain (greedy): x stands while accept < target[x], and
+ * the residual is the target's without x.  Sums are exact in units of 2^-60, so
+ * the token does not depend on how they are formed.  A residual without weight
+ * gives way to the target's row; a row without any gives -1 and status bit 2.
+ *  out_tokens: the standing drafts from row cu_q[b] on, the token taken, -1 in
+ *   the sequence's other rows; rows of no sequence are left as they are.
+ *  n_accepted[b]: drafts that stand (0 for a sequence without rows).
+ *  kv_len_out[b] = kv_len[b] less the drafts that do not (may be kv_len).
+ * Probabilities count as 0..1 (NaN as 0), a row's sum should be at most 8;
+ * random numbers as 0 <= x < 1 (NaN as 0).  A drafted token outside
+ * [0, vocab) does not stand and sets status bit 2; bit 4 marks a cu_q that does
+ * not fit, whose sequence has n_accepted 0 and no out_tokens. */
+typedef struct dls_verify_draft_desc {
+  const int32_t* tokens;    /* device [n_tokens] */
+  const void* target;       /* prob_type [n_tokens][vocab] */
+  const void* draft;        /* prob_type [n_tokens][vocab], or NULL */
+  const int32_t* cu_q;      /* device [n_seqs + 1] */
+  const float* accept;      /* device [n_tokens] */
+  const float* pick;        /* device [n_seqs] */
+  const int32_t* kv_len;    /* device [n_seqs], or NULL (both) */
+  int32_t* out_tokens;      /* device [n_tokens]; not tokens */
+  int32_t* n_accepted;      /* device [n_seqs] */
+  int32_t* kv_len_out;
+  int32_t* status;
+  int64_t target_stride, draft_stride; /* elements from one row to the next */
+  int32_t n_tokens;         /* rows, padding included */
+  int32_t n_seqs;           /* 0..2^24 */
+  int32_t vocab;            /* 1..2^30 */
+  int32_t prob_type;        /* dls_dtype */
+} dls_verify_draft_desc;
+int dls_verify_draft(const dls_verify_draft_desc* d, void* cuda_stream);
 
 /* ---- test and profiling hooks ------------------------------------------------ */
 
