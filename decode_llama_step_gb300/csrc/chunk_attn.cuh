@@ -53,6 +53,8 @@
 #include <cuda_bf16.h>
 #include <math.h>
 
+#include <type_traits>
+
 #include "../../include/dls.h"
 #include "kernels.h"
 #include "tc.cuh"
@@ -131,11 +133,13 @@ struct CCfg {
   static constexpr bool kTogether = HDP == 64;
   static constexpr int kUses = kTogether ? 1 : 2;  // ring uses of a key tile
   static constexpr int kStage = kTogether ? 2 * kKV : kKV;
-  // Codes arrive in a ring of their own, half the size a use; what is left
-  // of shared memory then holds three stages of operands.
-  static constexpr int NST = CODE ? 3 : 4;
+  // Codes arrive in a ring of their own, half the size a use.  What is in
+  // flight from memory is what that ring holds, so it takes what operands can
+  // spare: two of their stages (one for K, one for V) are enough for the
+  // products of wide heads, which take as long as converting the next.
+  static constexpr int NST = !CODE ? 4 : kTogether ? 3 : 2;
   static constexpr int kRaw = CODE ? kStage / 2 : 0;
-  static constexpr int NRAW = kTogether ? 5 : 3;
+  static constexpr int NRAW = 5;
   static constexpr int kKVOff = 2 * kQ;
   static constexpr int kXOff = kKVOff + NST * kStage;  // 8 KB a slot: its output rows on their way out, or statistics being joined
   static constexpr int kRawOff = kXOff + 2 * 8192;
@@ -155,7 +159,8 @@ struct CMisc {
   int abort, last[2];
 };
 struct CodeMisc : CMisc {
-  uint64_t raw_full[5], raw_empty[5];
+  uint64_t raw_full[5], raw_empty[5], q_ready;
+  int8_t q_exp[2][2][128];                        // powers of two that a piece's rows were multiplied by (bf16 q), pieces in turn
   float raw_scale[5][2][8];                       // of a raw stage with keys: of K and of V, for 16 keys each
   __align__(16) float scale[kScaleRing][3][8];     // c * K's, log2 of V's, 1 / V's
 };
@@ -481,71 +486,31 @@ __device__ __forceinline__ int ring_k(int mode, int i) { return mode == PAIR ? 2
 
 // ---- codes as 16-bit operands ---------------------------------------------------------------
 
-// Sixteen codes to sixteen values of T, both exactly: e4m3 has four bits of
-// mantissa and 2^-9 to 448, whole numbers up to 128 fit the eight bits of bf16.
-template <typename T, int CODE>
-struct Operand;
-template <int CODE, typename F>
-__device__ __forceinline__ void make_words(const uint4& w, uint4 (&e)[2], F&& four) {
-  four(w.x, e[0].x, e[0].y);
-  four(w.y, e[0].z, e[0].w);
-  four(w.z, e[1].x, e[1].y);
-  four(w.w, e[1].z, e[1].w);
-}
-__device__ __forceinline__ uint32_t e4m3_f16x2(uint16_t c) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(c));
-  return h;
-}
-template <>
-struct Operand<__half, DLS_E4M3> {
-  static __device__ __forceinline__ void make(const uint4& w, uint4 (&e)[2]) {
-    make_words<DLS_E4M3>(w, e, [](uint32_t c, uint32_t& lo, uint32_t& hi) {
-      lo = e4m3_f16x2((uint16_t)c);
-      hi = e4m3_f16x2((uint16_t)(c >> 16));
-    });
-  }
-};
-template <>
-struct Operand<__nv_bfloat16, DLS_E4M3> {
-  static __device__ __forceinline__ void make(const uint4& w, uint4 (&e)[2]) {
-    make_words<DLS_E4M3>(w, e, [](uint32_t c, uint32_t& lo, uint32_t& hi) {
-      const uint32_t a = e4m3_f16x2((uint16_t)c), b = e4m3_f16x2((uint16_t)(c >> 16));
-      const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&a)), y = __half22float2(*reinterpret_cast<const __half2*>(&b));
-      lo = Kind<__nv_bfloat16>::pack(x.x, x.y);
-      hi = Kind<__nv_bfloat16>::pack(y.x, y.y);
-    });
-  }
-};
-template <>
-struct Operand<__half, DLS_I8> {
-  // byte b + 128 under 0x64 is the half 1024 + 128 + b
-  static __device__ __forceinline__ void make(const uint4& w, uint4 (&e)[2]) {
-    make_words<DLS_I8>(w, e, [](uint32_t c, uint32_t& lo, uint32_t& hi) {
-      const uint32_t u = c ^ 0x80808080u, bias = 0x64806480u;  // 1152
-      const uint32_t x = __byte_perm(u, 0x64646464u, 0x4140), y = __byte_perm(u, 0x64646464u, 0x4342);
+// Sixteen codes to sixteen halves, exactly.  Both kinds of codes fit a half,
+// so products over codes are in fp16 whatever q's type is (q in bf16: see the
+// converting warps), and the weights keep a half's eleven bits.
+template <int CODE>
+__device__ __forceinline__ void codes_to_half(const uint4& w, uint4 (&e)[2]) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+  uint32_t h[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (CODE == DLS_E4M3) {
+      asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h[2 * i]) : "h"((uint16_t)u[i]));
+      asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h[2 * i + 1]) : "h"((uint16_t)(u[i] >> 16)));
+    } else {
+      // byte b + 128 under 0x64 is the half 1024 + 128 + b
+      const uint32_t c = u[i] ^ 0x80808080u, bias = 0x64806480u;  // 1152
+      const uint32_t x = __byte_perm(c, 0x64646464u, 0x4140), y = __byte_perm(c, 0x64646464u, 0x4342);
       const __half2 b = *reinterpret_cast<const __half2*>(&bias);
       const __half2 p = __hsub2(*reinterpret_cast<const __half2*>(&x), b), q = __hsub2(*reinterpret_cast<const __half2*>(&y), b);
-      lo = *reinterpret_cast<const uint32_t*>(&p);
-      hi = *reinterpret_cast<const uint32_t*>(&q);
-    });
+      h[2 * i] = *reinterpret_cast<const uint32_t*>(&p);
+      h[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&q);
+    }
   }
-};
-template <>
-struct Operand<__nv_bfloat16, DLS_I8> {
-  // the low seven bits under 0x43 are the bfloat16 128 + them; less 128, or 256 of a negative one
-  static __device__ __forceinline__ uint32_t two(uint32_t t) {
-    const uint32_t m = t & 0xff7fff7fu, s = t & 0xff80ff80u;
-    const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&m), *reinterpret_cast<const __nv_bfloat162*>(&s));
-    return *reinterpret_cast<const uint32_t*>(&d);
-  }
-  static __device__ __forceinline__ void make(const uint4& w, uint4 (&e)[2]) {
-    make_words<DLS_I8>(w, e, [](uint32_t c, uint32_t& lo, uint32_t& hi) {
-      lo = two(__byte_perm(c, 0x43434343u, 0x4140));
-      hi = two(__byte_perm(c, 0x43434343u, 0x4342));
-    });
-  }
-};
+  e[0] = make_uint4(h[0], h[1], h[2], h[3]);
+  e[1] = make_uint4(h[4], h[5], h[6], h[7]);
+}
 
 // ---- the kernel ----------------------------------------------------------------------------
 
@@ -652,10 +617,11 @@ __device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, int key0,
 // for 16 keys each.  With the score c s = sc[0] * (q . codes) the weight
 // handed to the product is p * V's scale = 2^(c s + log2 V's scale - R), whose
 // largest is what the reference follows, so it keeps its bits in 16 whatever
-// the scales are; l takes p back from it.
-template <typename T, bool HALVES>
-__device__ __forceinline__ void softmax_codes(uint32_t tS, uint32_t tO, int key0, const Row& row, const float (&sc)[3][8], bool first, int hd,
-                                              float& R, float& l, uint32_t p_half, int lane) {
+// the scales are; l takes p back from it.  cq: what the row's q was multiplied
+// by, taken back.
+template <bool HALVES>
+__device__ __forceinline__ void softmax_codes(uint32_t tS, uint32_t tO, int key0, const Row& row, const float (&sc)[3][8], float cq, bool first,
+                                              int hd, float& R, float& l, uint32_t p_half, int lane) {
   const bool ragged = __any_sync(0xffffffffu, row.ok && (key0 < row.lo || key0 + BK > row.hi));
   uint32_t v[128];
   tmem_read_by_32(tS, v);
@@ -670,7 +636,7 @@ __device__ __forceinline__ void softmax_codes(uint32_t tS, uint32_t tO, int key0
       y = max3(y, __uint_as_float(v[16 * g + i + 2]), __uint_as_float(v[16 * g + i + 3]));
     }
     x = max3(x, __uint_as_float(v[16 * g + 14]), __uint_as_float(v[16 * g + 15]));
-    m = fmaxf(m, fmaf(fmaxf(x, y), sc[0][g], sc[1][g]));
+    m = fmaxf(m, fmaf(fmaxf(x, y), fmaxf(sc[0][g] * cq, 0x1p-126f), sc[1][g]));
   }
   follow_max(m, row, first, tO, hd, R, l);
   const float nr = kShift - (R == -INFINITY ? 0.f : R);
@@ -680,7 +646,7 @@ __device__ __forceinline__ void softmax_codes(uint32_t tS, uint32_t tO, int key0
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int g = 2 * k + h;
-      const float c = sc[0][g], r = nr + sc[1][g];
+      const float c = fmaxf(sc[0][g] * cq, 0x1p-126f), r = nr + sc[1][g];
       const f2_t c2 = pk2(c, c), r2 = pk2(r, r);
       f2_t sum = pk2(0.f, 0.f);
 #pragma unroll
@@ -688,7 +654,7 @@ __device__ __forceinline__ void softmax_codes(uint32_t tS, uint32_t tO, int key0
         const float2 x = upk2(ffma2(pk2(__uint_as_float(v[16 * g + 2 * i]), __uint_as_float(v[16 * g + 2 * i + 1])), c2, r2));
         const float a = ex2(x.x), b = ex2(x.y);
         sum = fadd2(sum, pk2(a, b));
-        w[8 * h + i] = Kind<T>::pack(a, b);
+        w[8 * h + i] = Kind<__half>::pack(a, b);
       }
       const float2 s = upk2(sum);
       l = fmaf(s.x + s.y, sc[2][g], l);
@@ -848,6 +814,8 @@ __global__ void __launch_bounds__(kThreads<CODE>, 1) chunk_kernel(const __grid_c
                                                             const __grid_constant__ CUtensorMap tm_v,
                                                             const __grid_constant__ ChunkArgs a) {
   using C = CCfg<HDP, CODE>;
+  using W = typename std::conditional<CODE != 0, __half, T>::type;  // of the products' operands
+  constexpr bool kTurnQ = !std::is_same<W, T>::value;
   using Misc = typename MiscOf<CODE>::type;
   constexpr int NST = C::NST;
   extern __shared__ __align__(1024) uint8_t csm[];
@@ -886,6 +854,7 @@ __global__ void __launch_bounds__(kThreads<CODE>, 1) chunk_kernel(const __grid_c
         mbar_init(smem_u32(&sh.raw_full[i]), 33);  // the copy's bytes, and each lane's scales
         mbar_init(smem_u32(&sh.raw_empty[i]), 4);
       }
+      mbar_init(smem_u32(&sh.q_ready), 4);
     }
     sh.abort = 0;
     mbar_fence_init();
@@ -912,7 +881,7 @@ __global__ void __launch_bounds__(kThreads<CODE>, 1) chunk_kernel(const __grid_c
 
   if (warp < 4) {
     // (what the block was launched with, 168 or 128 a thread, is shared out anew)
-    if constexpr (CODE != 0) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    if constexpr (CODE != 0) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     else asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == 0) {
       // ---------------- copies: Q tiles, and K/V tiles piece by piece of a page
@@ -943,6 +912,7 @@ __global__ void __launch_bounds__(kThreads<CODE>, 1) chunk_kernel(const __grid_c
         ++nq;
         q_out = true;
         const int32_t* table = a.page_table + (size_t)p.b * a.max_pages;
+        [[maybe_unused]] int entries_at = -(1 << 30), entry = -1;
         // ring use: key tile j's K, its V, or both
         auto coded_tile = [&](int j, bool is_v) {
           if constexpr (CODE != 0) {
@@ -953,34 +923,43 @@ __global__ void __launch_bounds__(kThreads<CODE>, 1) chunk_kernel(const __grid_c
             uint32_t dst = qbase + C::kRawOff + s * C::kRaw;
             if (lane == 0) mbar_expect_tx(bar, (C::kTogether ? 2 : 1) * BK * row);
             __syncwarp();
-            constexpr int kPer = C::kTogether ? 2 : 1;
-            if (lane < npc * kPer) {
-              const int x = lane / kPer;
-              if (C::kTogether) is_v = lane % kPer, dst += is_v ? BK * row : 0;
-              const int key = j * BK + x * pr;
-              int y = a.pool_rows;  // past the end of the pool: the copy fills zeros
-              if (key < p.kl && key + pr > p.lo) {
-                const int page = table[key >> a.page_shift];
-                if (page >= 0 && page < a.n_pages)
-                  y = ((page * a.n_kv + p.kvh) << a.page_shift) + (key & ((1 << a.page_shift) - 1));
-                else if (a.status)
-                  atomicOr(a.status, kBadPage);
-              }
-              tma_load_2d(dst + x * pr * row, is_v ? &tm_v : &tm_k, 0, y, bar);
+            // the table's entries, 32 at a time (a load of its own for every tile would stand before its copies)
+            const int first = (j * BK) >> a.page_shift, last = ((j + 1) * BK - 1) >> a.page_shift;
+            if (first < entries_at || last >= entries_at + 32) {
+              entries_at = first - (last - first + 1);  // V of the tile before is still to come
+              const int e = entries_at + lane;
+              entry = -1;
+              if (e >= 0 && (long long)e << a.page_shift < p.kl && (long long)(e + 1) << a.page_shift > p.lo) entry = table[e];
             }
-            if ((C::kTogether || !is_v) && lane < 16) {  // with the keys: both scales of every 16 of them (no page: 0)
+            constexpr int kPer = C::kTogether ? 2 : 1;
+            {
+              const int x = lane / kPer;
+              const bool v = C::kTogether ? lane % kPer : is_v;
+              const int key = j * BK + x * pr;
+              const int page = __shfl_sync(0xffffffffu, entry, ((key >> a.page_shift) - entries_at) & 31);
+              if (lane < npc * kPer) {
+                int y = a.pool_rows;  // past the end of the pool: the copy fills zeros
+                if (key < p.kl && key + pr > p.lo) {
+                  if (page >= 0 && page < a.n_pages)
+                    y = ((page * a.n_kv + p.kvh) << a.page_shift) + (key & ((1 << a.page_shift) - 1));
+                  else if (a.status)
+                    atomicOr(a.status, kBadPage);
+                }
+                tma_load_2d(dst + (C::kTogether && v ? BK * row : 0) + x * pr * row, v ? &tm_v : &tm_k, 0, y, bar);
+              }
+            }
+            if (C::kTogether || !is_v) {  // with the keys: both scales of every 16 of them (no page: 0)
               const int key = j * BK + (lane & 7) * 16;
+              const int page = __shfl_sync(0xffffffffu, entry, ((key >> a.page_shift) - entries_at) & 31);
               const float* from = lane < 8 ? a.k_scales : a.v_scales;
               int bytes = 0;
-              if (key < p.kl && key + 16 > p.lo) {
-                const int page = table[key >> a.page_shift];
-                if (page >= 0 && page < a.n_pages) {
-                  from += ((size_t)((page * a.n_kv + p.kvh)) << (a.page_shift - a.block_shift)) + ((key & ((1 << a.page_shift) - 1)) >> a.block_shift);
-                  bytes = 4;
-                }
+              if (key < p.kl && key + 16 > p.lo && page >= 0 && page < a.n_pages) {
+                from += ((size_t)((page * a.n_kv + p.kvh)) << (a.page_shift - a.block_shift)) + ((key & ((1 << a.page_shift) - 1)) >> a.block_shift);
+                bytes = 4;
               }
-              asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(&sh.raw_scale[s][lane >> 3][lane & 7])), "l"(from), "r"(bytes)
-                           : "memory");
+              if (lane < 16)
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(&sh.raw_scale[s][lane >> 3][lane & 7])), "l"(from), "r"(bytes)
+                             : "memory");
             }
             asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
             ++u;
@@ -1028,8 +1007,8 @@ __global__ void __launch_bounds__(kThreads<CODE>, 1) chunk_kernel(const __grid_c
       __syncwarp();
     } else if (warp == 1) {
       // ---------------- MMA issue (the whole warp, converged: see umma_f16_warp)
-      const uint32_t id_s = umma_idesc_f16(128, BK) | Kind<T>::kIdesc;
-      const uint32_t id_o = umma_idesc_f16_bmn(128, a.head_dim) | Kind<T>::kIdesc;
+      const uint32_t id_s = umma_idesc_f16(128, BK) | Kind<W>::kIdesc;
+      const uint32_t id_o = umma_idesc_f16_bmn(128, a.head_dim) | Kind<W>::kIdesc;
       const int ksteps = a.head_dim / 16;
       constexpr bool T2 = C::kTogether;
       int u0 = 0, nq = 0;        // ring position of the piece, Q tiles seen
@@ -1086,7 +1065,9 @@ __global__ void __launch_bounds__(kThreads<CODE>, 1) chunk_kernel(const __grid_c
         if (lane == 0) mbar_arrive(smem_u32(&sh.pq_empty[k % QDEPTH]));
         __syncwarp();
         if (n > 0) {
-          if (!(ok = wait(sh.q_full, nq))) break;
+          if constexpr (kTurnQ) ok = wait(sh.q_ready, nq);
+          else ok = wait(sh.q_full, nq);
+          if (!ok) break;
           ++nq;
           const int u = u0;
           u0 += C::kUses * n;
@@ -1213,73 +1194,124 @@ __global__ void __launch_bounds__(kThreads<CODE>, 1) chunk_kernel(const __grid_c
     }
   } else if (CODE != 0 && warp >= 12) {
     if constexpr (CODE != 0) {
-      // ---------------- codes to 16-bit operands (exact), in the layout that the copies of 16-bit pages have
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+      // ---------------- codes to halves (exact), in the layout that the copies of 16-bit pages have
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
       constexpr int NRAW = C::NRAW;
       const int ct = tid - 12 * 32, nc = a.head_dim / 16;  // 16-byte pieces of a key
       const unsigned inv_nc = (65536 + nc - 1) / nc;        // x / nc = x * inv_nc >> 16 for x < 1024
-      int u = 0, nt = 0;                                    // ring uses, key tiles seen
+      const bool even = (nc & (nc - 1)) == 0;
+      int u = 0, nt = 0, nq = 0;                            // ring uses, key tiles, Q tiles seen
       bool ok = true;
       for (int k = 0; ok; ++k) {
         if (!(ok = __all_sync(0xffffffffu, cwait(smem_u32(&sh.pq_full[k % QDEPTH]), (k / QDEPTH) & 1, ab)))) break;
         const Piece& q = sh.pq[k % QDEPTH];
-        const int mode = q.mode, n = q.jb - q.ja, ja = q.ja, kl = q.kl, lo = q.lo;
+        const int mode = q.mode, n = q.jb - q.ja, ja = q.ja, kl = q.kl, lo = q.lo, tokens = q.n;
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&sh.pq_empty[k % QDEPTH]));
         if (mode == END) break;
+        if (kTurnQ && n > 0) {
+          // q in bf16: a row times the power of two that puts its largest
+          // value next to 2^15 is a row of halves, exactly but for what lies
+          // 2^38 below that value; the softmax takes the power back
+          if (!(ok = __all_sync(0xffffffffu, cwait(smem_u32(&sh.q_full), nq & 1, ab)))) break;
+          for (int s = 0; s < (mode == PAIR ? 2 : 1); ++s) {
+            const int rows = min(mode == PAIR ? tokens - s * a.tpq : tokens, a.tpq) * a.group;
+            if (ct >= rows) continue;
+            const uint32_t at = qbase + s * C::kQ + ct * 128;
+            uint32_t most = 0;
+            for (int j = 0; j < a.head_dim / 8; ++j) {
+              const uint4 w = lds128(at + (j >> 3) * (128 * 128) + (((j & 7) ^ (ct & 7)) << 4));
+              const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+              for (int i = 0; i < 4; ++i) most = max(most, max(x[i] << 16 & 0x7fff0000u, x[i] & 0x7fff0000u));
+            }
+            const int e = most >= 0x7f800000u || !most ? 0 : min(14 - ((int)(most >> 23) - 127), 100);
+            const float f = __uint_as_float((unsigned)(e + 127) << 23);
+            for (int j = 0; j < a.head_dim / 8; ++j) {
+              const uint32_t y = at + (j >> 3) * (128 * 128) + (((j & 7) ^ (ct & 7)) << 4);
+              const uint4 w = lds128(y);
+              auto two = [&](uint32_t x) { return Kind<__half>::pack(__uint_as_float(x << 16) * f, __uint_as_float(x & 0xffff0000u) * f); };
+              sts128(y, make_uint4(two(w.x), two(w.y), two(w.z), two(w.w)));
+            }
+            sh.q_exp[nq & 1][s][ct] = (int8_t)e;
+          }
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&sh.q_ready));
+          ++nq;
+        }
 #pragma unroll 1
         for (int x = 0; x < C::kUses * n; ++x, ++u) {
           const RingUse r = C::kTogether ? RingUse{x, false} : ring_use(mode, x, n);
-          ok = __all_sync(0xffffffffu, cwait(smem_u32(&sh.raw_full[u % NRAW]), (u / NRAW) & 1, ab) &&
-                                           (u < NST || cwait(smem_u32(&sh.empty[u % NST]), ((u / NST) - 1) & 1, ab)));
-          if (!ok) break;
-          if (C::kTogether || !r.is_v) {
-            // A stage being free says that all key tiles but the last three
-            // have had their second product, and so their softmax: with NST
-            // stages of K and V in turn the one that this tile takes held a
-            // use of a tile two before it (three, where both are in one
-            // stage or both slots work ahead), so this ring place is free.
-            if (ct < 8) {
-              const float sk = fminf(fmaxf(sh.raw_scale[u % NRAW][0][ct], 0x1p-64f), 0x1p64f);
-              const float sv = fminf(fmaxf(sh.raw_scale[u % NRAW][1][ct], 0x1p-64f), 0x1p64f);
+          const int rs = u % NRAW, key0 = (ja + r.tile) * BK;
+          if (!(ok = __all_sync(0xffffffffu, cwait(smem_u32(&sh.raw_full[rs]), (u / NRAW) & 1, ab)))) break;
+          const uint32_t from = qbase + C::kRawOff + rs * C::kRaw, to = kvbase + (u % NST) * C::kStage;
+          auto stage_free = [&] { return u < NST || cwait(smem_u32(&sh.empty[u % NST]), ((u / NST) - 1) & 1, ab); };
+          // (read before the stage is handed back)
+          const bool keys = C::kTogether || !r.is_v;
+          float sk = 0.f, sv = 0.f;
+          if (keys && ct < 8) sk = sh.raw_scale[rs][0][ct], sv = sh.raw_scale[rs][1][ct];
+          auto scales = [&] {
+            // The operand stage being free, all key tiles but the last three
+            // have had their second product, and so their softmax: this place
+            // of the ring is free.
+            if (keys && ct < 8) {
+              sk = fminf(fmaxf(sk, 0x1p-64f), 0x1p64f);
+              sv = fminf(fmaxf(sv, 0x1p-64f), 0x1p64f);
               float(&to)[3][8] = sh.scale[nt % kScaleRing];
-              to[0][ct] = a.c * sk;
+              to[0][ct] = fmaxf(a.c * sk, 0x1p-126f);  // (never 0: a masked score is -infinity times it)
               to[1][ct] = log2f(sv);
               to[2][ct] = 1.f / sv;
             }
-            ++nt;
-          }
-          const uint32_t from = qbase + C::kRawOff + (u % NRAW) * C::kRaw, to = kvbase + (u % NST) * C::kStage;
-          const int key0 = (ja + r.tile) * BK;
-          auto convert = [&](uint32_t src, uint32_t dst, bool is_v) {
-            const int total = BK * nc;
-            // rows of V that no query may see can hold anything: 0 * NaN would reach every row through the product
-            const bool ragged = is_v && (key0 + BK > kl || key0 < lo);
-#pragma unroll 2
-            for (int i = ct; i < total; i += 128) {
-              const int row = (int)((unsigned)i * inv_nc >> 16), c = i - row * nc;
-              uint4 w = lds128(src + i * 16);
-              uint4 e[2];
-              Operand<T, CODE>::make(w, e);
-              if (ragged && (key0 + row >= kl || key0 + row < lo)) e[0] = e[1] = make_uint4(0, 0, 0, 0);
-              // 16-byte chunk j of a row at j ^ (row & 7) of its 128 bytes; the upper half's lanes go in the other
-              // order, so that eight lanes of a row of 128 meet eight different bank groups
-              const uint32_t at = dst + (c >> 2) * (BK * 128) + row * 128;
-              const int swap = c >> 2 & 1, j0 = (2 * c + swap) & 7, j1 = (2 * c + 1 - swap) & 7;
-              sts128(at + ((j0 ^ (row & 7)) << 4), swap ? e[1] : e[0]);
-              sts128(at + ((j1 ^ (row & 7)) << 4), swap ? e[0] : e[1]);
-            }
+            nt += keys;
           };
-          if (C::kTogether) {
-            convert(from, to, false);
-            convert(from + BK * a.head_dim, to + C::kKV, true);
+          // 16-byte chunk j of a row lies at j ^ (row & 7) of its 128 bytes; the upper half's lanes store their two chunks in
+          // the other order, so that eight lanes of a row of 128 meet eight different bank groups
+          auto put = [&](uint32_t dst, int row, int c, const uint4& w, bool zero) {
+            uint4 e[2];
+            codes_to_half<CODE>(w, e);
+            if (zero) e[0] = e[1] = make_uint4(0, 0, 0, 0);
+            const uint32_t at = dst + (c >> 2) * (BK * 128) + row * 128;
+            const int swap = c >> 2 & 1, j0 = (2 * c + swap) & 7, j1 = (2 * c + 1 - swap) & 7;
+            sts128(at + ((j0 ^ (row & 7)) << 4), swap ? e[1] : e[0]);
+            sts128(at + ((j1 ^ (row & 7)) << 4), swap ? e[0] : e[1]);
+          };
+          // rows of V that no query may see can hold anything: 0 * NaN would reach every row through the product
+          const bool ragged = (C::kTogether || r.is_v) && (key0 + BK > kl || key0 < lo);
+          auto hidden = [&](int row) { return key0 + row >= kl || key0 + row < lo; };
+          bool freed = false;
+          if (even && !ragged) {
+            // a thread's pieces lie in one column, 128 / nc rows apart (a multiple of 8: the swizzle is the same for all)
+            const int row0 = ct / nc, c = ct - row0 * nc, step = 128 / nc;
+            constexpr int kAll = C::kTogether ? 2 : 1;  // K and V, one behind the other
+            uint4 w[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (i < kAll * nc) w[i] = lds128(from + (ct + 128 * i) * 16);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sh.raw_empty[rs]));
+            freed = true;
+            if (!(ok = __all_sync(0xffffffffu, stage_free()))) break;
+            scales();
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (i < kAll * nc) put(to + (i < nc ? 0 : C::kKV), row0 + step * (i < nc ? i : i - nc), c, w[i], false);
           } else {
-            convert(from, to, r.is_v);
+            if (!(ok = __all_sync(0xffffffffu, stage_free()))) break;
+            scales();
+            const int total = (C::kTogether ? 2 : 1) * BK * nc;
+#pragma unroll 1
+            for (int i = ct; i < total; i += 128) {
+              const bool second = i >= BK * nc;
+              const int at = second ? i - BK * nc : i, row = (int)((unsigned)at * inv_nc >> 16);
+              const bool v = C::kTogether ? second : r.is_v;
+              put(to + (second ? C::kKV : 0), row, at - row * nc, lds128(from + i * 16), v && ragged && hidden(row));
+            }
           }
           fence_async_smem();
           __syncwarp();
           if (lane == 0) {
-            mbar_arrive(smem_u32(&sh.raw_empty[u % NRAW]));
+            if (!freed) mbar_arrive(smem_u32(&sh.raw_empty[rs]));
             mbar_arrive(smem_u32(&sh.full[u % NST]));
           }
         }
@@ -1294,7 +1326,7 @@ __global__ void __launch_bounds__(kThreads<CODE>, 1) chunk_kernel(const __grid_c
     const uint32_t tl = (uint32_t)(quarter * 32) << 16;
     const uint32_t tS = tmem + tl + slot * 128, tO = tmem + tl + 256 + slot * HDP;
     const int hd = a.head_dim, G = a.group;
-    int u0 = 0, ns = 0, nx = 0, tiles = 0;
+    int u0 = 0, ns = 0, nx = 0, tiles = 0, pieces = 0;
     int no[2] = {0, 0};  // phases of o_full passed
     bool ok = true;
     for (int k = 0;; ++k) {
@@ -1304,9 +1336,10 @@ __global__ void __launch_bounds__(kThreads<CODE>, 1) chunk_kernel(const __grid_c
       const Piece& p = sh.pq[k % QDEPTH];
       if (p.mode == END) break;
       const int n = p.jb - p.ja, u = u0;
-      [[maybe_unused]] const int nt0 = tiles;  // key tiles before this piece's
+      [[maybe_unused]] const int nt0 = tiles, nq = pieces;  // key tiles and Q tiles before this piece's
       u0 += C::kUses * n;
       tiles += n;
+      pieces += n > 0;
       const Steps st = slot_steps(a, p, slot);
       const int tok0 = p.mode == PAIR ? slot * a.tpq : 0;
       const int ntok = p.mode == PAIR ? min(p.n - tok0, a.tpq) : p.n;
@@ -1322,6 +1355,7 @@ __global__ void __launch_bounds__(kThreads<CODE>, 1) chunk_kernel(const __grid_c
         row.lo = a.window && pos >= a.window ? pos - a.window + 1 : 0;
       }
       float R = -INFINITY, l = 0.f;
+      [[maybe_unused]] float cq = 1.f;
       for (int i = 0; i < st.count; ++i) {
         const int j = st.first + i * st.stride;
         ok = __all_sync(0xffffffffu, ok && cwait(smem_u32(&sh.s_full[slot]), ns & 1, ab));
@@ -1344,8 +1378,10 @@ __global__ void __launch_bounds__(kThreads<CODE>, 1) chunk_kernel(const __grid_c
         }
         const uint32_t h0 = smem_u32(&sh.p_full[slot][0]), h1 = smem_u32(&sh.p_full[slot][1]);
         if (busy) {
+          if constexpr (kTurnQ)
+            if (i == 0) cq = __uint_as_float((unsigned)(127 - sh.q_exp[nq & 1][p.mode == PAIR ? slot : 0][tw]) << 23);
           if constexpr (CODE != 0)
-            softmax_codes<T, !C::kTogether>(tS, tO, j * BK, row, sh.scale[(nt0 + j - p.ja) % kScaleRing], i == 0, hd, R, l, h0, lane);
+            softmax_codes<!C::kTogether>(tS, tO, j * BK, row, sh.scale[(nt0 + j - p.ja) % kScaleRing], cq, i == 0, hd, R, l, h0, lane);
           else
             softmax_tile<T, !C::kTogether>(tS, tO, j * BK, row, a.c, i == 0, hd, R, l, h0, lane);
           hand_over(h1, lane);
