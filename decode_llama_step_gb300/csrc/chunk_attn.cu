@@ -29,7 +29,7 @@ int device_ready(cudaError_t* err) {
     if ((*err = cudaFuncSetAttribute(f[i], cudaFuncAttributeMaxDynamicSharedMemorySize, chunk_smem<128, 0>())) != cudaSuccess) return 0;
     if ((*err = cudaFuncSetAttribute(h[i], cudaFuncAttributeMaxDynamicSharedMemorySize, chunk_smem<64, 0>())) != cudaSuccess) return 0;
   }
-  if ((*err = chunk_codes_setup()) != cudaSuccess) return 0;
+  if ((*err = chunk_codes_setup()) != cudaSuccess || (*err = few_codes_setup()) != cudaSuccess) return 0;
   return sms[dev] = n;
 }
 
@@ -95,7 +95,7 @@ int attend(const dls_attention_chunk8_desc* d, const char* what, void* cuda_stre
   a.page_shift = pt == 16 ? 4 : pt == 32 ? 5 : pt == 64 ? 6 : pt == 128 ? 7 : 8;
   a.n_pages = d->n_pages, a.max_pages = d->max_pages, a.pool_rows = d->n_pages * d->n_kv_heads * pt;
   a.causal = d->causal, a.window = d->window;
-  a.tpq = tpq, a.inv_group = (65536 + a.group - 1) / a.group;
+  a.tpq = tpq, a.tile_tokens = 2 * tpq, a.inv_group = (65536 + a.group - 1) / a.group;
   a.c = (d->scale > 0.f ? d->scale : 1.0f / sqrtf((float)hd)) * 1.4426950408889634f;
   // a lane of the planning warp walks at most 4 sequences and 8 more tiles; its sums fit 32 bits.
   // One token over 2048: 15.5 us with the warp's plan, 16.2 with the block's; 64 over up to 8192 (5301 on average) 218 and 220 us.
@@ -105,6 +105,24 @@ int attend(const dls_attention_chunk8_desc* d, const char* what, void* cuda_stre
   const CUtensorMapDataType dt = d->q_type == DLS_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const uint32_t pr = pt < BK ? pt : BK;
   CUtensorMap tq, tk, tv;
+  // Few rows a sequence: the kernel without operands of 128 rows.  The number
+  // of rows alone is known here, so a batch may hold a longer sequence all the
+  // same; its tiles then read their keys once for every sixteen rows, and all
+  // the batch's tiles are no more than those of equal sequences.
+  const bool few = d->code_type && (hd == 64 || hd == 128) && a.group <= kFewRows && (long long)d->n_tokens * a.group <= kFewRows * (long long)d->n_seqs;
+  if (few) {
+    const int rows = (long long)d->n_tokens * a.group <= 8 * (long long)d->n_seqs && a.group <= 8 ? 8 : kFewRows;
+    a.tile_tokens = rows / a.group;
+    a.small_plan = d->n_seqs <= 128 && d->n_tokens <= 128 * a.tile_tokens && (long long)d->max_pages * pt <= 1 << 24;
+    const CUtensorMapSwizzle sw = hd == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+    if (!make_tmap_2d(&tk, CU_TENSOR_MAP_DATA_TYPE_UINT8, d->k_pages, hd, a.pool_rows, hd, hd, 16, sw) ||
+        !make_tmap_2d(&tv, CU_TENSOR_MAP_DATA_TYPE_UINT8, d->v_pages, hd, a.pool_rows, hd, hd, 16, sw))
+      return report_error(DLS_ERR_CUDA, "%s: tensor map (head_dim=%d)", what, hd);
+    if (a.status) e = cudaMemsetAsync(a.status, 0, sizeof(int32_t), s);
+    if (e == cudaSuccess)
+      e = launch_few_codes(tk, tv, a, d->q, d->q_stride, d->q_type == DLS_F16, d->code_type, sms < MAXC ? sms : MAXC, s);
+    return e == cudaSuccess ? DLS_OK : report_error(DLS_ERR_CUDA, "%s: cuda=%s", what, cudaGetErrorString(e));
+  }
   const uint64_t dims[3] = {(uint64_t)hd, (uint64_t)d->n_heads, (uint64_t)d->n_tokens};
   const uint64_t strides[2] = {(uint64_t)hd * 2, (uint64_t)d->q_stride * 2};
   const uint32_t box[3] = {64, (uint32_t)a.group, (uint32_t)a.tpq};

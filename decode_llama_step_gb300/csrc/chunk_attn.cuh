@@ -73,6 +73,7 @@ struct ChunkArgs {
   int page_shift, n_pages, max_pages, pool_rows;
   int causal, window;
   int tpq;      // tokens of a slot: 128 / group
+  int tile_tokens;  // tokens of a tile of work: both slots', or a few (few_attn8.cu)
   unsigned inv_group;  // ceil(2^16 / group): r / group = r * inv_group >> 16 for r < 128
   float c;      // scale * log2(e)
   int small_plan;  // few sequences and tiles: one warp plans
@@ -270,17 +271,18 @@ struct Tile {
   int mode, n, pos0, lo, j0, keys, units;  // keys: key tiles to do; units: kTileCost and the key tiles (one at least)
 };
 
+template <int COST>
 __device__ __forceinline__ Tile tile_of(const ChunkArgs& a, int ql, int kl, int t) {
   Tile x;
-  const int i0 = t * 2 * a.tpq;
-  x.n = min(2 * a.tpq, ql - i0);
+  const int i0 = t * a.tile_tokens;
+  x.n = min(a.tile_tokens, ql - i0);
   x.mode = x.n > a.tpq ? PAIR : SPLIT;
   x.pos0 = kl - ql + i0;
   const int hi = a.causal ? min(max(x.pos0 + x.n, 0), kl) : kl;
   x.lo = a.window && x.pos0 >= a.window ? min(x.pos0 - a.window + 1, hi) : 0;
   x.j0 = x.lo / BK;
   x.keys = hi > x.lo ? (hi + BK - 1) / BK - x.j0 : 0;
-  x.units = kTileCost + max(x.keys, 1);
+  x.units = COST + max(x.keys, 1);
   return x;
 }
 
@@ -314,9 +316,9 @@ __device__ __noinline__ long long quotient(long long x, long long y) {
 // The CTA's range of key tiles and where it begins (all threads).  Short
 // loops, not unrolled: every CTA runs this once, and what it costs is
 // instruction fetches and latencies.
-template <int THREADS>
-__device__ __noinline__ void plan(const ChunkArgs& a, int4* info, CMisc& sh) {
-  const int tid = threadIdx.x, tp = 2 * a.tpq;
+template <int THREADS, int COST, int MIN, typename Misc>
+__device__ __noinline__ void plan(const ChunkArgs& a, int4* info, Misc& sh) {
+  const int tid = threadIdx.x, tp = a.tile_tokens;
   const int per_s = (a.n_seqs + THREADS - 1) / THREADS;
   const int s0 = min(tid * per_s, a.n_seqs), s1 = min(s0 + per_s, a.n_seqs);
   long long mine = 0, total;
@@ -355,7 +357,7 @@ __device__ __noinline__ void plan(const ChunkArgs& a, int4* info, CMisc& sh) {
 #pragma unroll 1
       while (b + 1 < a.n_seqs && info[b + 1].x <= t) ++b;
       const int4 f = info[b];
-      const int st = tile_of(a, f.y, f.z, t - f.x).units;
+      const int st = tile_of<COST>(a, f.y, f.z, t - f.x).units;
       if (stop >= 0 && sum + st > stop) {
         sh.off0 = (int)(stop - sum);
         sh.b0 = b;
@@ -370,7 +372,7 @@ __device__ __noinline__ void plan(const ChunkArgs& a, int4* info, CMisc& sh) {
     }
     if (pass) break;
     pre = block_scan<THREADS / 32>(sum, sh.scan, &total);
-    const long long all = total * a.n_kv, per = max(quotient(all + gridDim.x - 1, gridDim.x), (long long)kMinSteps);
+    const long long all = total * a.n_kv, per = max(quotient(all + gridDim.x - 1, gridDim.x), (long long)MIN);
     r0 = min(per * blockIdx.x, all);
     const long long r1 = min(r0 + per, all);
     if (tid == 0) {
@@ -390,9 +392,10 @@ __device__ __noinline__ void plan(const ChunkArgs& a, int4* info, CMisc& sh) {
 // The same by one warp, without a barrier, for few sequences and tiles: the
 // other warps are at their posts meanwhile.  A lane takes consecutive
 // sequences.  Returns the range; where it begins goes to the last arguments.
+template <int COST, int MIN>
 __device__ __forceinline__ void plan_warp(const ChunkArgs& a, int lane, long long& r0, long long& r1, long long& per, int& b0, int& t0,
                                           int& off0, int& kvh0, Seq& seq0) {
-  const int per_s = (a.n_seqs + 31) / 32, tp = 2 * a.tpq;
+  const int per_s = (a.n_seqs + 31) / 32, tp = a.tile_tokens;
   const int s0 = min(lane * per_s, a.n_seqs), s1 = min(s0 + per_s, a.n_seqs);
   unsigned pre = 0, total = 0, stop = 0;
   bool seek = false;
@@ -409,7 +412,7 @@ __device__ __forceinline__ void plan_warp(const ChunkArgs& a, int lane, long lon
       bad |= s.bad;
 #pragma unroll 1
       for (int t = 0; t * tp < s.ql; ++t) {
-        const unsigned st = tile_of(a, s.ql, s.kl, t).units;
+        const unsigned st = tile_of<COST>(a, s.ql, s.kl, t).units;
         if (seek && sum + st > stop) {
           b0 = b, t0 = t, off0 = (int)(stop - sum), seq0 = s;
           found = true;
@@ -429,7 +432,7 @@ __device__ __forceinline__ void plan_warp(const ChunkArgs& a, int lane, long lon
     total = __shfl_sync(0xffffffffu, pre, 31);
     pre -= sum;
     const long long all = (long long)total * a.n_kv;
-    per = max(quotient(all + gridDim.x - 1, gridDim.x), (long long)kMinSteps);
+    per = max(quotient(all + gridDim.x - 1, gridDim.x), (long long)MIN);
     r0 = min(per * blockIdx.x, all);
     r1 = min(r0 + per, all);
     if (r0 >= r1) return;
@@ -447,6 +450,55 @@ __device__ __forceinline__ void plan_warp(const ChunkArgs& a, int lane, long lon
   seq0.start = __shfl_sync(0xffffffffu, seq0.start, from);
   seq0.ql = __shfl_sync(0xffffffffu, seq0.ql, from);
   seq0.kl = __shfl_sync(0xffffffffu, seq0.kl, from);
+}
+
+// Where a CTA stands in its range.
+struct Cursor {
+  long long pos, end, per;
+  int b, t, off, kvh;
+  Seq s;
+};
+// The next piece of the range (mode END: none), by a whole warp alike.
+template <int COST>
+__device__ __forceinline__ Piece next_piece(const ChunkArgs& a, Cursor& c) {
+  Piece p;
+  p.mode = END;
+  while (c.pos < c.end) {
+    const Tile x = tile_of<COST>(a, c.s.ql, c.s.kl, c.t);
+    const int take = (int)min((long long)(x.units - c.off), c.end - c.pos);
+    const int u0 = max(c.off - COST, 0), u1 = c.off + take - COST;  // key tiles of it here
+    const long long first = c.pos - c.off + COST;                   // position of the tile's first key tile
+    if (u1 > u0) {
+      p.mode = x.mode;
+      p.b = c.b;
+      p.kvh = c.kvh;
+      p.row0 = c.s.start + c.t * a.tile_tokens;
+      p.n = x.n;
+      p.pos0 = x.pos0;
+      p.kl = c.s.kl;
+      p.lo = x.lo;
+      p.ja = x.j0 + u0;
+      p.jb = x.keys ? x.j0 + u1 : p.ja;
+      p.c0 = (int)quotient(first, c.per);
+      p.np = (int)quotient(first + (x.units - COST) - 1, c.per) - p.c0 + 1;
+      p.idx = (int)blockIdx.x - p.c0;
+    }
+    c.pos += take;
+    c.off += take;
+    if (c.off == x.units) {
+      c.off = 0;
+      if (++c.t * a.tile_tokens >= c.s.ql && c.pos < c.end) {
+        c.t = 0;
+#pragma unroll 1
+        do {
+          if (++c.b == a.n_seqs) c.b = 0, ++c.kvh;
+          c.s = seq_get(a, c.b);
+        } while (c.s.ql == 0);
+      }
+    }
+    if (u1 > u0) break;
+  }
+  return p;
 }
 
 // Key tiles of a slot inside a piece: first, first + stride, ... (count of them).
@@ -869,7 +921,7 @@ __global__ void __launch_bounds__(kThreads<CODE>, 1) chunk_kernel(const __grid_c
     tmem_relinquish();
   }
   if (!a.small_plan) {
-    plan<kThreads<CODE>>(a, reinterpret_cast<int4*>(csm + pad), sh);
+    plan<kThreads<CODE>, kTileCost, kMinSteps>(a, reinterpret_cast<int4*>(csm + pad), sh);
     // its scratch (generic proxy) is overwritten by TMA from here on
     fence_async_smem();
   }
@@ -1132,56 +1184,18 @@ __global__ void __launch_bounds__(kThreads<CODE>, 1) chunk_kernel(const __grid_c
       __syncwarp();
     } else if (warp == 2) {
       // ---------------- the CTA's pieces
-      long long pos, end, per;
-      int b, t, off, kvh;
-      Seq s;
+      Cursor at;
       if (a.small_plan) {
-        plan_warp(a, lane, pos, end, per, b, t, off, kvh, s);
+        plan_warp<kTileCost, kMinSteps>(a, lane, at.pos, at.end, at.per, at.b, at.t, at.off, at.kvh, at.s);
       } else {
-        pos = sh.range0, end = sh.range1, per = sh.per;
-        b = sh.b0, t = sh.t0, off = sh.off0, kvh = sh.kvh0;
-        s.start = sh.start0, s.ql = sh.ql0, s.kl = sh.kl0;
+        at.pos = sh.range0, at.end = sh.range1, at.per = sh.per;
+        at.b = sh.b0, at.t = sh.t0, at.off = sh.off0, at.kvh = sh.kvh0;
+        at.s.start = sh.start0, at.s.ql = sh.ql0, at.s.kl = sh.kl0;
       }
       bool ok = true;
       int k = 0;
       for (;;) {
-        Piece p;
-        p.mode = END;
-        while (pos < end) {
-          const Tile x = tile_of(a, s.ql, s.kl, t);
-          const int take = (int)min((long long)(x.units - off), end - pos);
-          const int u0 = max(off - kTileCost, 0), u1 = off + take - kTileCost;  // key tiles of it here
-          const long long first = pos - off + kTileCost;                       // position of the tile's first key tile
-          if (u1 > u0) {
-            p.mode = x.mode;
-            p.b = b;
-            p.kvh = kvh;
-            p.row0 = s.start + t * 2 * a.tpq;
-            p.n = x.n;
-            p.pos0 = x.pos0;
-            p.kl = s.kl;
-            p.lo = x.lo;
-            p.ja = x.j0 + u0;
-            p.jb = x.keys ? x.j0 + u1 : p.ja;
-            p.c0 = (int)quotient(first, per);
-            p.np = (int)quotient(first + (x.units - kTileCost) - 1, per) - p.c0 + 1;
-            p.idx = (int)blockIdx.x - p.c0;
-          }
-          pos += take;
-          off += take;
-          if (off == x.units) {
-            off = 0;
-            if (++t * 2 * a.tpq >= s.ql && pos < end) {
-              t = 0;
-#pragma unroll 1
-              do {
-                if (++b == a.n_seqs) b = 0, ++kvh;
-                s = seq_get(a, b);
-              } while (s.ql == 0);
-            }
-          }
-          if (u1 > u0) break;
-        }
+        const Piece p = next_piece<kTileCost>(a, at);
         if (k >= QDEPTH && !(ok = __all_sync(0xffffffffu, cwait(smem_u32(&sh.pq_empty[k % QDEPTH]), ((k / QDEPTH) - 1) & 1, ab)))) break;
         if (lane == 0) {
           sh.pq[k % QDEPTH] = p;
@@ -1565,5 +1579,11 @@ using ChunkFn = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap
 cudaError_t chunk_codes_setup();
 cudaError_t launch_chunk_codes(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const ChunkArgs& a, int code, bool half,
                                int ctas, cudaStream_t s);
+
+// The same for tiles of few rows (few_attn8.cu): head_dim 64 or 128, at most 16 rows a tile, c's tile_tokens.
+constexpr int kFewRows = 16;
+cudaError_t few_codes_setup();
+cudaError_t launch_few_codes(const CUtensorMap& tk, const CUtensorMap& tv, const ChunkArgs& c, const void* q, long long q_stride, bool half,
+                             int code, int ctas, cudaStream_t s);
 
 }  // namespace dls

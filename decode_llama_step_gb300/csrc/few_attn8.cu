@@ -1,0 +1,502 @@
+// Attention over pages of 8-bit codes for few rows: at most sixteen rows (new
+// tokens x query heads of a KV head) a tile of work, as single tokens and
+// short verify passes have them.
+//
+// The mathematics and the division of the work are those of chunk_attn.cuh.
+// There a tile of codes is converted in shared memory for the 5th-generation
+// tensor core, whose operands of 128 rows lie there: it is written by the copy,
+// read and written twice as wide by the conversion and read by the product, 1536
+// cycles of shared memory's 128 bytes a cycle for 128 keys of 128, as long as
+// HBM takes to bring them (745 cycles a 16 KB), and the chain copy -
+// conversion - product - softmax - product passes through barriers at every
+// step.  Sixteen rows need no such operands.  Here a warp takes sixteen keys at
+// a time for itself: codes come from memory into its own ring by TMA, go to
+// registers once (conflict-free through the copy's swizzle), are converted
+// there and are the fragments of the warp-wide product m16n8k16 as they lie:
+//   S = Q K^T  lane 4r + c holds dimensions [32 c, 32 c + 32) of key r: four
+//              codes of them are its part of a k-step, q's fragments follow
+//   O += P V   lane 4r + c holds dimensions [16 r, 16 r + 16) of keys 2c,
+//              2c + 1, 2c + 8, 2c + 9: byte permutes pair the keys
+// (head_dim 128; half of each at 64).  The scores' fragment is the weights'.
+// Eight such warps work on 128 keys; each keeps its own (R, l, O), joined in
+// shared memory at the end of a piece and, where a tile was cut, through the
+// workspace in range order.
+#include <type_traits>
+
+#include "chunk_attn.cuh"
+
+namespace dls {
+
+namespace {
+
+constexpr int FWARPS = 8;
+constexpr int FTHREADS = (FWARPS + 1) * 32;
+constexpr int FK = 16;             // keys of a warp's step; FWARPS * FK = BK
+static_assert(FWARPS * FK == BK, "a key tile is a round of the warps");
+constexpr int kFewCost = 1;        // what a tile of work costs beyond its key tiles, in key tiles
+constexpr int kFewSteps = 1;       // key tiles of a range at least
+
+template <int HD, bool WIDE>
+struct FCfg {
+  static constexpr int kRows = WIDE ? 16 : 8;
+  static constexpr int kPart = FK * HD;              // bytes of a step's K or V
+  static constexpr int kStage = 2 * kPart;
+  static constexpr int NST = 16384 / kStage;         // 16 KB in flight a warp, 128 KB an SM
+  static constexpr int kMergeOff = FWARPS * NST * kStage;
+  static constexpr int kMiscOff = kMergeOff + FWARPS * kRows * HD * 4;
+};
+struct FMisc {
+  uint64_t full[FWARPS][8], empty[FWARPS][8], pq_full[QDEPTH], pq_empty[QDEPTH];
+  Piece pq[QDEPTH];
+  float scale[FWARPS][8][2];     // of a stage: K's and V's
+  float R[FWARPS][16], l[FWARPS][16];
+  long long scan[FWARPS + 1];
+  long long range0, range1, per;
+  int b0, t0, off0, kvh0, start0, ql0, kl0;
+  int abort, last;
+};
+template <int HD, bool WIDE>
+constexpr int few_smem() {
+  return FCfg<HD, WIDE>::kMiscOff + (int)sizeof(FMisc) + 1024;
+}
+static_assert(few_smem<128, true>() <= 227 * 1024, "shared memory");
+static_assert(DLS_MAX_CHUNK_SEQS * 16 <= FCfg<64, false>::kMergeOff, "plan scratch");
+
+struct FewArgs {
+  ChunkArgs c;
+  const void* q;
+  long long q_stride;
+  int q_bf16;
+};
+
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Two codes (the lower or upper half of a word) to two halves.
+template <int CODE, bool UPPER>
+__device__ __forceinline__ uint32_t two_halves(uint32_t w) {
+  uint32_t h;
+  if constexpr (CODE == DLS_E4M3) {
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)(UPPER ? w >> 16 : w)));
+  } else {
+    const uint32_t x = __byte_perm(w ^ 0x80808080u, 0x64646464u, UPPER ? 0x4342 : 0x4140), bias = 0x64806480u;  // see codes_to_half
+    const __half2 p = __hsub2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&bias));
+    h = *reinterpret_cast<const uint32_t*>(&p);
+  }
+  return h;
+}
+
+__device__ __forceinline__ bool all_warps(bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.and.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)ok), "n"(FWARPS * 32)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void meet() { named_bar(1, FWARPS * 32); }
+
+// A lane's dimensions of one row of q as halves: words 2 s and 2 s + 1 belong
+// to k-step s.  A bf16 row is multiplied by a power of two that makes it
+// halves (see the converting warps of chunk_attn.cuh); cq takes it back.
+template <int HD>
+__device__ __forceinline__ void load_q(const FewArgs& a, bool live, size_t at, uint32_t (&w)[HD / 8], float& cq) {
+  const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at);
+#pragma unroll
+  for (int i = 0; i < HD / 32; ++i) {
+    const uint4 x = live ? p[i] : make_uint4(0, 0, 0, 0);
+    w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
+  }
+  cq = 1.f;
+  if (a.q_bf16) {
+    uint32_t most = 0;
+#pragma unroll
+    for (int i = 0; i < HD / 8; ++i) most = max(most, max(w[i] << 16 & 0x7fff0000u, w[i] & 0x7fff0000u));
+    most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
+    most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
+    const int e = most >= 0x7f800000u || !most ? 0 : min(14 - ((int)(most >> 23) - 127), 100);
+    const float f = __uint_as_float((unsigned)(e + 127) << 23);
+    cq = __uint_as_float((unsigned)(127 - e) << 23);
+#pragma unroll
+    for (int i = 0; i < HD / 8; ++i) w[i] = Kind<__half>::pack(__uint_as_float(w[i] << 16) * f, __uint_as_float(w[i] & 0xffff0000u) * f);
+  }
+}
+
+template <int HD, int CODE, bool WIDE>
+__global__ void __launch_bounds__(FTHREADS, 1) few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                                                          const __grid_constant__ FewArgs fa) {
+  using C = FCfg<HD, WIDE>;
+  constexpr int NST = C::NST, HDP = HD;
+  const ChunkArgs& a = fa.c;
+  extern __shared__ __align__(1024) uint8_t fsm[];
+  const uint32_t raw = smem_u32(fsm), pad = (1024u - (raw & 1023u)) & 1023u, base = raw + pad;
+  FMisc& sh = *reinterpret_cast<FMisc*>(fsm + pad + C::kMiscOff);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  int* const ab = &sh.abort;
+
+  if (warp < FWARPS && lane < NST) {
+    mbar_init(smem_u32(&sh.full[warp][lane]), 3);   // the copies' bytes, two scales
+    mbar_init(smem_u32(&sh.empty[warp][lane]), 1);
+  }
+  if (warp == FWARPS && lane < QDEPTH) {
+    mbar_init(smem_u32(&sh.pq_full[lane]), 1);
+    mbar_init(smem_u32(&sh.pq_empty[lane]), FWARPS);
+  }
+  if (tid == FTHREADS - 1) {
+    prefetch_tmap(&tm_k);
+    prefetch_tmap(&tm_v);
+    sh.abort = 0;
+  }
+  mbar_fence_init();
+  if (!a.small_plan) {
+    plan<FTHREADS, kFewCost, kFewSteps>(a, reinterpret_cast<int4*>(fsm + pad), sh);
+    fence_async_smem();  // its scratch is overwritten by copies from here on
+  }
+  __syncthreads();
+
+  if (warp == FWARPS) {
+    // ---------------- the list of pieces, and their copies: lane 4 w + part for warp w (K, V, K's scale, V's scale)
+    Cursor at;
+    if (a.small_plan) {
+      plan_warp<kFewCost, kFewSteps>(a, lane, at.pos, at.end, at.per, at.b, at.t, at.off, at.kvh, at.s);
+    } else {
+      at.pos = sh.range0, at.end = sh.range1, at.per = sh.per;
+      at.b = sh.b0, at.t = sh.t0, at.off = sh.off0, at.kvh = sh.kvh0;
+      at.s.start = sh.start0, at.s.ql = sh.ql0, at.s.kl = sh.kl0;
+    }
+    const int w = lane >> 2, part = lane & 3;
+    bool ok = true;
+    int u = 0;
+    for (int k = 0; ok; ++k) {
+      const Piece p = next_piece<kFewCost>(a, at);
+      if (k >= QDEPTH && !(ok = __all_sync(0xffffffffu, cwait(smem_u32(&sh.pq_empty[k % QDEPTH]), ((k / QDEPTH) - 1) & 1, ab)))) break;
+      if (lane == 0) {
+        sh.pq[k % QDEPTH] = p;
+        mbar_arrive(smem_u32(&sh.pq_full[k % QDEPTH]));
+      }
+      __syncwarp();
+      if (p.mode == END) break;
+      const int32_t* table = a.page_table + (size_t)p.b * a.max_pages;
+      int entries_at = -(1 << 30), entry = -1;
+#pragma unroll 1
+      for (int j = p.ja; j < p.jb; ++j, ++u) {
+        const int first = (j * BK) >> a.page_shift, last = ((j + 1) * BK - 1) >> a.page_shift;
+        if (last >= entries_at + 32) {  // the table's entries, 32 at a time
+          entries_at = first;
+          const int e = entries_at + lane;
+          entry = -1;
+          if ((long long)e << a.page_shift < p.kl && (long long)(e + 1) << a.page_shift > p.lo) entry = table[e];
+        }
+        const int s = u % NST, key = j * BK + w * FK;
+        const int page = __shfl_sync(0xffffffffu, entry, ((key >> a.page_shift) - entries_at) & 31);
+        if (u >= NST && !(ok = __all_sync(0xffffffffu, cwait(smem_u32(&sh.empty[w][s]), ((u / NST) - 1) & 1, ab)))) break;
+        const uint32_t bar = smem_u32(&sh.full[w][s]);
+        if (part == 0) mbar_expect_tx(bar, C::kStage);
+        __syncwarp();
+        const bool seen = key < p.kl && key + FK > p.lo, good = seen && page >= 0 && page < a.n_pages;
+        if (seen && !good && part == 0 && a.status) atomicOr(a.status, kBadPage);
+        const int head = page * a.n_kv + p.kvh, in_page = key & ((1 << a.page_shift) - 1);
+        if (part < 2) {
+          const int y = good ? (head << a.page_shift) + in_page : a.pool_rows;  // past the end of the pool: the copy fills zeros
+          tma_load_2d(base + (w * NST + s) * C::kStage + part * C::kPart, part ? &tm_v : &tm_k, 0, y, bar);
+        } else {
+          const float* from = part == 2 ? a.k_scales : a.v_scales;
+          if (good) from += ((size_t)head << (a.page_shift - a.block_shift)) + (in_page >> a.block_shift);
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(&sh.scale[w][s][part - 2])), "l"(from), "r"(good ? 4 : 0)
+                       : "memory");
+          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+        }
+      }
+    }
+    // no copy may be in flight when the CTA ends
+    __syncwarp();
+    for (int x = u > NST ? u - NST : 0; x < u; ++x) cwait(smem_u32(&sh.full[w][x % NST]), (x / NST) & 1, ab, false);
+    if (!ok && a.status && lane == 0) atomicOr(a.status, kTimeout);
+    return;
+  }
+
+  // ---------------- the warps' own keys
+  const int r = lane >> 2, c = lane & 3, G = a.group;
+  float* const merge = reinterpret_cast<float*>(fsm + pad + C::kMergeOff);
+  int u0 = 0;
+  bool ok = true;
+  for (int k = 0;; ++k) {
+    ok = ok && cwait(smem_u32(&sh.pq_full[k % QDEPTH]), (k / QDEPTH) & 1, ab);
+    if (!(ok = all_warps(ok))) break;  // (and everyone has read the last piece's sums)
+    const Piece p = sh.pq[k % QDEPTH];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&sh.pq_empty[k % QDEPTH]));
+    if (p.mode == END) break;
+    const int n_rows = p.n * G;
+    // the lane's rows: r, and r + 8 of a wide tile
+    Row row[2];
+    uint32_t qa[WIDE ? 2 : 1][HD / 8];
+    float cq[2] = {1.f, 1.f}, R[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+    for (int h = 0; h < (WIDE ? 2 : 1); ++h) {
+      const int x = r + 8 * h, tok = token_of(a, x), pos = p.pos0 + tok;
+      row[h].ok = x < n_rows;
+      row[h].hi = !row[h].ok ? 0x7fffffff : a.causal ? min(max(pos + 1, 0), p.kl) : p.kl;
+      row[h].lo = row[h].ok && a.window && pos >= a.window ? pos - a.window + 1 : 0;
+      const size_t qrow = row[h].ok ? (size_t)(p.row0 + tok) * fa.q_stride + (size_t)(p.kvh * G + x - tok * G) * HD + (HD / 4) * c : 0;
+      load_q<HD>(fa, row[h].ok, qrow, qa[h], cq[h]);
+    }
+    float o[HD / 8][4];
+#pragma unroll
+    for (int i = 0; i < HD / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+
+    const int n = p.jb - p.ja;
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+      const int u = u0 + i, s = u % NST, key0 = (p.ja + i) * BK + warp * FK;
+      ok = __all_sync(0xffffffffu, ok && cwait(smem_u32(&sh.full[warp][s]), (u / NST) & 1, ab));
+      if (!ok) break;
+      if (key0 < p.kl && key0 + FK > p.lo) {
+        const uint32_t kt = base + (warp * NST + s) * C::kStage, vt = kt + C::kPart;
+        const bool ragged = __any_sync(0xffffffffu, (row[0].ok && (key0 < row[0].lo || key0 + FK > row[0].hi)) ||
+                                                        (WIDE && row[1].ok && (key0 < row[1].lo || key0 + FK > row[1].hi)));
+        // ---- S = Q K^T for two groups of eight keys
+        float sc[2][4] = {};
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const int key = 8 * t + r;
+#pragma unroll
+          for (int h = 0; h < HD / 64; ++h) {
+            const int chunk = HD == 128 ? (2 * c + h) ^ (key & 7) : c ^ (key >> 1 & 3);
+            const uint4 w = lds128(kt + key * HD + chunk * 16);
+            const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int st = 4 * h + e;
+              const uint32_t qf[4] = {qa[0][2 * st], WIDE ? qa[WIDE][2 * st] : 0u, qa[0][2 * st + 1], WIDE ? qa[WIDE][2 * st + 1] : 0u};
+              mma16816(sc[t], qf, two_halves<CODE, false>(x[e]), two_halves<CODE, true>(x[e]));
+            }
+          }
+        }
+        // V's codes: keys 2c, 2c + 1, 2c + 8, 2c + 9
+        constexpr int VW = HD / 32;  // words of a lane's dimensions
+        uint32_t v[4][VW];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int key = 2 * c + (e & 1) + 8 * (e >> 1);
+          if constexpr (HD == 128) {
+            const uint4 w = lds128(vt + key * HD + ((r ^ (key & 7)) << 4));
+            v[e][0] = w.x, v[e][1] = w.y, v[e][2] = w.z, v[e][3] = w.w;
+          } else {
+            asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];"
+                         : "=r"(v[e][0]), "=r"(v[e][1])
+                         : "r"(vt + key * HD + (((r >> 1) ^ (key >> 1 & 3)) << 4) + (r & 1) * 8));
+          }
+        }
+        const float sk = fminf(fmaxf(sh.scale[warp][s][0], 0x1p-64f), 0x1p64f), sv = fminf(fmaxf(sh.scale[warp][s][1], 0x1p-64f), 0x1p64f);
+        const float lsv = log2f(sv), isv = 1.f / sv;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sh.empty[warp][s]));
+        if (__builtin_expect(ragged, 0)) {
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int key = key0 + 8 * t + 2 * c + (e & 1);
+              const Row& w = row[WIDE ? e >> 1 : 0];
+              if (key < w.lo || key >= w.hi) sc[t][e] = -INFINITY;
+            }
+          // rows of V that no query may see can hold anything
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int key = key0 + 2 * c + (e & 1) + 8 * (e >> 1);
+            if (key >= p.kl || key < p.lo)
+#pragma unroll
+              for (int x = 0; x < VW; ++x) v[e][x] = 0;
+          }
+        }
+        // ---- weights: as softmax_codes
+        uint32_t pa[4] = {0, 0, 0, 0};
+        float ck[2], m[2];
+        bool grow = false;
+#pragma unroll
+        for (int h = 0; h < (WIDE ? 2 : 1); ++h) {
+          ck[h] = fmaxf(fmaxf(a.c * sk, 0x1p-126f) * cq[h], 0x1p-126f);
+          m[h] = fmaf(fmaxf(fmaxf(sc[0][2 * h], sc[0][2 * h + 1]), fmaxf(sc[1][2 * h], sc[1][2 * h + 1])), ck[h], lsv);
+          grow |= row[h].ok && m[h] > R[h] + kGrow;
+        }
+        if (__builtin_expect(__any_sync(0xffffffffu, grow), 0)) {
+#pragma unroll
+          for (int h = 0; h < (WIDE ? 2 : 1); ++h) {
+            float x = fmaxf(m[h], __shfl_xor_sync(0xffffffffu, m[h], 1));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+            if (x > R[h] + kGrow) {
+              const float f = ex2(R[h] - x);
+              R[h] = x;
+              l[h] *= f;
+#pragma unroll
+              for (int e = 0; e < HD / 8; ++e) o[e][2 * h] *= f, o[e][2 * h + 1] *= f;
+            }
+          }
+        }
+#pragma unroll
+        for (int h = 0; h < (WIDE ? 2 : 1); ++h) {
+          const float nr = kShift + lsv - (R[h] == -INFINITY ? 0.f : R[h]);
+          const float w0 = ex2(fmaf(sc[0][2 * h], ck[h], nr)), w1 = ex2(fmaf(sc[0][2 * h + 1], ck[h], nr));
+          const float w2 = ex2(fmaf(sc[1][2 * h], ck[h], nr)), w3 = ex2(fmaf(sc[1][2 * h + 1], ck[h], nr));
+          l[h] = fmaf((w0 + w1) + (w2 + w3), isv, l[h]);
+          pa[h] = Kind<__half>::pack(w0, w1);
+          pa[2 + h] = Kind<__half>::pack(w2, w3);
+        }
+        // ---- O += P V: eight dimensions a product
+#pragma unroll
+        for (int x = 0; x < VW; ++x) {
+          const uint32_t lo01 = __byte_perm(v[0][x], v[1][x], 0x5140), lo23 = __byte_perm(v[2][x], v[3][x], 0x5140);
+          const uint32_t hi01 = __byte_perm(v[0][x], v[1][x], 0x7362), hi23 = __byte_perm(v[2][x], v[3][x], 0x7362);
+          mma16816(o[4 * x], pa, two_halves<CODE, false>(lo01), two_halves<CODE, false>(lo23));
+          mma16816(o[4 * x + 1], pa, two_halves<CODE, true>(lo01), two_halves<CODE, true>(lo23));
+          mma16816(o[4 * x + 2], pa, two_halves<CODE, false>(hi01), two_halves<CODE, false>(hi23));
+          mma16816(o[4 * x + 3], pa, two_halves<CODE, true>(hi01), two_halves<CODE, true>(hi23));
+        }
+      } else {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sh.empty[warp][s]));
+      }
+    }
+    u0 += n;
+
+    // ---- the warps' shares meet.  A lane's HD / 4 dimensions of a row lie in
+    // 16-byte pieces, moved by its number against bank conflicts.
+    constexpr int kPieces = HD / 16, kRowF = HD;  // 16-byte pieces of a lane, floats of a row
+#pragma unroll
+    for (int h = 0; h < (WIDE ? 2 : 1); ++h) {
+      float s = l[h];
+      s += __shfl_xor_sync(0xffffffffu, s, 1);
+      s += __shfl_xor_sync(0xffffffffu, s, 2);
+      if (c == 0) sh.R[warp][r + 8 * h] = R[h], sh.l[warp][r + 8 * h] = s;
+      float* const to = merge + (size_t)(warp * C::kRows + r + 8 * h) * kRowF + c * (HD / 4);
+#pragma unroll
+      for (int x = 0; x < kPieces; ++x) {
+        // dimensions 4 x .. of the lane's: o[j][.] holds j and HD / 8 + j
+        const int up = x >= kPieces / 2, j = 4 * x - up * (HD / 8);
+        *reinterpret_cast<float4*>(to + ((x ^ (lane & (kPieces - 1))) << 2)) =
+            make_float4(o[j][2 * h + up], o[j + 1][2 * h + up], o[j + 2][2 * h + up], o[j + 3][2 * h + up]);
+      }
+    }
+    meet();
+    constexpr int C4 = HD / 4;  // 16-byte pieces of a row
+    float* const part = p.np > 1 ? partial_at<HDP>(a, blockIdx.x, p.idx == 0, 0) : nullptr;
+    auto put = [&](int x, int d, const float4& y) {
+      const int tok = token_of(a, x), head = p.kvh * G + x - tok * G;
+      const size_t at = (size_t)(p.row0 + tok) * a.o_stride + (size_t)head * HD + 4 * d;
+      uint2 w;
+      if (fa.q_bf16) w = make_uint2(Kind<__nv_bfloat16>::pack(y.x, y.y), Kind<__nv_bfloat16>::pack(y.z, y.w));
+      else w = make_uint2(Kind<__half>::pack(y.x, y.y), Kind<__half>::pack(y.z, y.w));
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.o) + at) = w;
+    };
+    auto put_lse = [&](int x, float M, float L) {
+      const int tok = token_of(a, x);
+      a.lse[(size_t)(p.row0 + tok) * (a.n_kv * G) + p.kvh * G + x - tok * G] = lse_of(M, L);
+    };
+    for (int it = tid; it < n_rows * C4; it += FWARPS * 32) {
+      const int x = it / C4, d = it - x * C4;
+      const int q = 4 * d / (HD / 4), piece = d - q * kPieces;
+      const int moved = (piece ^ ((4 * (x & 7) + q) & (kPieces - 1))) << 2;
+      float M = -INFINITY, L = 0.f;
+#pragma unroll
+      for (int w = 0; w < FWARPS; ++w) M = fmaxf(M, sh.R[w][x]);
+      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < FWARPS; ++w) {
+        const float f = weight(sh.R[w][x], M);
+        const float4 z = *reinterpret_cast<const float4*>(merge + (size_t)(w * C::kRows + x) * kRowF + q * (HD / 4) + moved);
+        L = fmaf(f, sh.l[w][x], L);
+        y.x = fmaf(f, z.x, y.x), y.y = fmaf(f, z.y, y.y), y.z = fmaf(f, z.z, y.z), y.w = fmaf(f, z.w, y.w);
+      }
+      if (part) {
+        __stcg(reinterpret_cast<float4*>(part + 256) + it, y);
+        if (d == 0) __stcg(part + x, M), __stcg(part + 128 + x, L);
+      } else {
+        const float inv = L > 0.f ? 1.f / L : 0.f;
+        put(x, d, make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
+        if (d == 0 && a.lse) put_lse(x, M, L);
+      }
+    }
+    if (part) {
+      // the last piece of the tile to arrive joins them all
+      meet();
+      if (tid == 0) {
+        int* cnt = a.counters + p.c0 * 2;
+        int seen;
+        asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(seen) : "l"(cnt) : "memory");
+        const bool last = seen == p.np - 1;
+        if (last) *cnt = 0;  // ready for the next call
+        sh.last = last;
+      }
+      meet();
+      if (sh.last) {
+        float *sw = merge, *sl = merge + MAXC * 16;
+        for (int x = tid; x < p.np * n_rows; x += FWARPS * 32) {
+          const int i = x / n_rows;
+          const float* from = partial_at<HDP>(a, p.c0 + i, i == 0, 0) + (x - i * n_rows);
+          sw[x] = __ldcg(from);
+          sl[x] = __ldcg(from + 128);
+        }
+        meet();
+        for (int it = tid; it < n_rows * C4; it += FWARPS * 32) {
+          const int x = it / C4, d = it - x * C4;
+          float M = -INFINITY, L = 0.f;
+#pragma unroll 4
+          for (int i = 0; i < p.np; ++i) M = fmaxf(M, sw[i * n_rows + x]);
+          float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+          for (int i = 0; i < p.np; ++i) {
+            const float4 z = __ldcg(reinterpret_cast<const float4*>(partial_at<HDP>(a, p.c0 + i, i == 0, 0) + 256) + it);
+            const float f = weight(sw[i * n_rows + x], M);
+            L = fmaf(f, sl[i * n_rows + x], L);
+            y.x = fmaf(f, z.x, y.x), y.y = fmaf(f, z.y, y.y), y.z = fmaf(f, z.z, y.z), y.w = fmaf(f, z.w, y.w);
+          }
+          const float inv = L > 0.f ? 1.f / L : 0.f;
+          put(x, d, make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
+          if (d == 0 && a.lse) put_lse(x, M, L);
+        }
+      }
+    }
+  }
+  if (!ok && a.status && lane == 0) atomicOr(a.status, kTimeout);
+}
+
+using FewFn = void (*)(const CUtensorMap, const CUtensorMap, const FewArgs);
+
+template <int HD, int CODE>
+FewFn few_fn(bool wide) {
+  return wide ? few_kernel<HD, CODE, true> : few_kernel<HD, CODE, false>;
+}
+FewFn few_fn(int hd, int code, bool wide) {
+  if (hd == 128) return code == DLS_E4M3 ? few_fn<128, DLS_E4M3>(wide) : few_fn<128, DLS_I8>(wide);
+  return code == DLS_E4M3 ? few_fn<64, DLS_E4M3>(wide) : few_fn<64, DLS_I8>(wide);
+}
+int few_bytes(int hd, bool wide) {
+  return hd == 128 ? (wide ? few_smem<128, true>() : few_smem<128, false>()) : (wide ? few_smem<64, true>() : few_smem<64, false>());
+}
+
+}  // namespace
+
+cudaError_t few_codes_setup() {
+  for (int i = 0; i < 8; ++i) {
+    const int hd = i & 1 ? 64 : 128;
+    const cudaError_t e =
+        cudaFuncSetAttribute(few_fn(hd, i & 2 ? DLS_I8 : DLS_E4M3, i & 4), cudaFuncAttributeMaxDynamicSharedMemorySize, few_bytes(hd, i & 4));
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+cudaError_t launch_few_codes(const CUtensorMap& tk, const CUtensorMap& tv, const ChunkArgs& c, const void* q, long long q_stride, bool half,
+                             int code, int ctas, cudaStream_t s) {
+  FewArgs a{c, q, q_stride, !half};
+  const bool wide = a.c.tile_tokens * a.c.group > 8;
+  few_fn(a.c.head_dim, code, wide)<<<ctas, FTHREADS, few_bytes(a.c.head_dim, wide), s>>>(tk, tv, a);
+  return cudaGetLastError();
+}
+
+}  // namespace dls

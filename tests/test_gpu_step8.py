@@ -712,6 +712,94 @@ def test_attention8_many_tiles_of_each_range(gpu_lib, heads, kvh, hd, page, bloc
     close_attend(B, o, lse, attend64(B, q, heads, hd ** -0.5, True, 0))
 
 
+FEW = [  # few rows a sequence: heads x new tokens of a KV head's group up to eight, or sixteen
+    ([(1, 1)], 4, 1), ([(1, 300), (1, 16), (1, 17), (1, 15), (1, 129)], 8, 1), ([(1, 2500), (1, 1), (1, 777)], 16, 1),
+    ([(1, 1000)] * 5, 3, 3), ([(2, 400), (2, 2), (1, 90)], 4, 1), ([(4, 600), (3, 50), (4, 4), (0, 9), (5, 1300)], 8, 2),
+    ([(16, 900), (9, 40)], 2, 2), ([(1, 333)] * 40, 12, 1), ([(5, 4101)] + [(3, 700 + b) for b in range(7)], 6, 2),
+    ([(0, 5)] * 30 + [(60, 500), (1, 64)] + [(0, 0)] * 30, 2, 1),   # a long one among empty ones
+    ([(1, 40 + 3 * b) for b in range(300)], 10, 2),                  # planned by the block
+]
+
+
+@pytest.mark.parametrize("lengths,heads,kvh", FEW, ids=lambda x: f"{len(x)}seqs" if isinstance(x, list) else str(x))
+@pytest.mark.parametrize("hd,page,block,typ,code", [(128, 64, 64, "bf16", "e4m3"), (64, 16, 16, "f16", "i8"), (128, 16, 16, "f16", "e4m3"),
+                                                    (64, 256, 32, "bf16", "e4m3"), (128, 128, 32, "bf16", "i8")])
+def test_attention8_few_rows(gpu_lib, lengths, heads, kvh, hd, page, block, typ, code):
+    check_attend(lengths, heads, kvh, hd, page, block, typ, code, first=1, pad=2)
+
+
+@pytest.mark.parametrize("window", [1, 5, 16, 17, 130])
+def test_attention8_few_rows_windows(gpu_lib, window):
+    check_attend([(1, 1000), (2, 300), (1, 33), (3, 3), (1, 1)], 8, 2, 128, 32, 16, "f16", "e4m3", window=window)
+    check_attend([(1, 1000), (2, 300), (1, 33), (3, 3), (1, 1)], 4, 2, 64, 16, 16, "bf16", "i8", window=window)
+
+
+def test_attention8_few_rows_without_keys_and_every_key(gpu_lib):
+    check_attend([(2, 1), (1, 0), (3, 2), (1, 50)], 4, 2, 64, 32, 16, "bf16", "e4m3")
+    check_attend([(2, 1), (1, 0), (3, 2), (1, 50)], 4, 2, 128, 32, 32, "f16", "i8", window=1)
+    check_attend([(2, 700), (3, 40), (1, 1), (2, 0)], 4, 2, 128, 64, 64, "bf16", "e4m3", causal=False)
+
+
+@pytest.mark.parametrize("scale", [1e-3, 0.5, 4.0])
+def test_attention8_few_rows_scales_of_scores(gpu_lib, scale):
+    check_attend([(1, 777), (2, 400)], 4, 2, 64, 64, 16, "bf16", "e4m3", scale=scale)
+    check_attend([(1, 777), (2, 400)], 4, 2, 128, 64, 32, "f16", "e4m3", scale=scale)
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("lengths,heads", [([(1, 9000)], 16), ([(3, 5000), (1, 3001)], 16)])
+def test_attention8_rising_scores(gpu_lib, hd, lengths, heads):
+    """Keys whose scores grow along the sequence: the running maximum moves at every step, by little and by much."""
+    for step in (0.02, 0.5):
+        B = Batch8(lengths, 2, hd, 64, 64, "e4m3", 9)
+        B.fill()
+        B.ks.fill_(1 / 64)
+        for b, (_, kl) in enumerate(lengths):
+            p, s = B.slots(b, 0, kl)
+            rise = (torch.arange(kl, device="cuda") * step * 0.1 * 0.5).clamp(max=440)
+            B.k.view(torch.uint8)[p, :, s, 0] = rise.to(CODES["e4m3"]).view(torch.uint8)[:, None]
+        q = torch.randn(B.rows, heads, hd, generator=B.g, device="cuda").bfloat16()
+        q[..., 0] = 8.0 * 64
+        o, lse = torch.empty_like(q), torch.empty(B.rows, heads, device="cuda")
+        dls.attention_chunk8(q, B.k, B.v, B.ks, B.vs, B.table, B.cu_q, B.kv_len, o, workspace(hd), lse=lse, scale=0.05)
+        close_attend(B, o, lse, attend64(B, q, heads, 0.05, True, 0))
+
+
+@pytest.mark.parametrize("rows", [1, 40])
+@pytest.mark.parametrize("size", [1e-30, 1e-6, 3e4, 1e30])
+def test_attention8_bf16_rows_of_any_size(gpu_lib, rows, size):
+    """bf16 holds rows of q that halves do not: their scores are what the formula gives all the same."""
+    B = Batch8([(rows, 300)], 1, 64, 16, 16, "e4m3", 19)
+    B.fill()
+    q = torch.randn(rows, 4, 64, generator=B.g, device="cuda")
+    q[:, 1] = 0.0
+    q[:, 2, 5] = 1e-4
+    q = (q * size).bfloat16()
+    o, lse = torch.empty_like(q), torch.empty(rows, 4, device="cuda")
+    scale = min(max(0.1 / size, 1e-28), 1e28)
+    dls.attention_chunk8(q, B.k, B.v, B.ks, B.vs, B.table, B.cu_q, B.kv_len, o, workspace(64), lse=lse, scale=scale)
+    close_attend(B, o, lse, attend64(B, q, 4, float(np.float32(scale)), True, 0))
+
+
+@pytest.mark.parametrize("lengths,heads,kvh,hd", [([(5, 4101), (1, 3661), (4, 1803), (2, 2951)], 8, 2, 128), ([(1, 2000 + 5 * b) for b in range(70)], 8, 1, 64),
+                                                  ([(1, 2000 + 5 * b) for b in range(70)], 16, 2, 128)])
+def test_attention8_few_rows_repeated(gpu_lib, lengths, heads, kvh, hd):
+    """Several pieces in each CTA's range, cut tiles among them, repeated: the same bits."""
+    B = Batch8(lengths, kvh, hd, 32, 32, "e4m3", 16)
+    B.fill()
+    q = (2 * torch.randn(B.rows, heads, hd, generator=B.g, device="cuda")).half()
+    o, first, ws = torch.empty_like(q), torch.empty_like(q), workspace(hd)
+    args = q, B.k, B.v, B.ks, B.vs, B.table, B.cu_q, B.kv_len
+    dls.attention_chunk8(*args, first, ws)
+    for _ in range(20):
+        dls.attention_chunk8(*args, o, ws)
+        assert torch.equal(o, first)
+    x = q.clone()
+    dls.attention_chunk8(x, *args[1:], x, ws)
+    assert torch.equal(x, first)
+    close_attend(B, o, None, attend64(B, q, heads, hd ** -0.5, True, 0))
+
+
 @pytest.mark.parametrize("typ", ["f16", "bf16"])
 def test_attention8_every_code(gpu_lib, typ):
     """One key a sequence: its value is the output, for every code that is a number."""
