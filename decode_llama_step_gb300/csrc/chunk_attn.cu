@@ -115,8 +115,8 @@ int attend(const dls_attention_chunk8_desc* d, const char* what, void* cuda_stre
     a.tile_tokens = rows / a.group;
     a.small_plan = d->n_seqs <= 128 && d->n_tokens <= 128 * a.tile_tokens && (long long)d->max_pages * pt <= 1 << 24;
     const CUtensorMapSwizzle sw = hd == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
-    if (!make_tmap_2d(&tk, CU_TENSOR_MAP_DATA_TYPE_UINT8, d->k_pages, hd, a.pool_rows, hd, hd, 16, sw) ||
-        !make_tmap_2d(&tv, CU_TENSOR_MAP_DATA_TYPE_UINT8, d->v_pages, hd, a.pool_rows, hd, hd, 16, sw))
+    if (!make_tmap_2d(&tk, CU_TENSOR_MAP_DATA_TYPE_UINT8, d->k_pages, hd, a.pool_rows, hd, hd, pr, sw) ||
+        !make_tmap_2d(&tv, CU_TENSOR_MAP_DATA_TYPE_UINT8, d->v_pages, hd, a.pool_rows, hd, hd, pr, sw))
       return report_error(DLS_ERR_CUDA, "%s: tensor map (head_dim=%d)", what, hd);
     if (a.status) e = cudaMemsetAsync(a.status, 0, sizeof(int32_t), s);
     if (e == cudaSuccess)

@@ -10,7 +10,7 @@
 // HBM takes to bring them (745 cycles a 16 KB), and the chain copy -
 // conversion - product - softmax - product passes through barriers at every
 // step.  Sixteen rows need no such operands.  Here a warp takes sixteen keys at
-// a time for itself: codes come from memory into its own ring by TMA, go to
+// a time for itself: codes come from memory into a ring by TMA, go to
 // registers once (conflict-free through the copy's swizzle), are converted
 // there and are the fragments of the warp-wide product m16n8k16 as they lie:
 //   S = Q K^T  lane 4r + c holds dimensions [32 c, 32 c + 32) of key r: four
@@ -39,16 +39,16 @@ constexpr int kFewSteps = 1;       // key tiles of a range at least
 template <int HD, bool WIDE>
 struct FCfg {
   static constexpr int kRows = WIDE ? 16 : 8;
-  static constexpr int kPart = FK * HD;              // bytes of a step's K or V
+  static constexpr int kPart = BK * HD;              // bytes of a key tile's K or V
   static constexpr int kStage = 2 * kPart;
-  static constexpr int NST = 16384 / kStage;         // 16 KB in flight a warp, 128 KB an SM
-  static constexpr int kMergeOff = FWARPS * NST * kStage;
+  static constexpr int NST = 131072 / kStage;        // 128 KB in flight an SM
+  static constexpr int kMergeOff = NST * kStage;
   static constexpr int kMiscOff = kMergeOff + FWARPS * kRows * HD * 4;
 };
 struct FMisc {
-  uint64_t full[FWARPS][8], empty[FWARPS][8], pq_full[QDEPTH], pq_empty[QDEPTH];
+  uint64_t full[8], empty[8], pq_full[QDEPTH], pq_empty[QDEPTH];
   Piece pq[QDEPTH];
-  float scale[FWARPS][8][2];     // of a stage: K's and V's
+  float scale[8][2][FWARPS];     // of a stage: K's and V's for each warp's keys
   float R[FWARPS][16], l[FWARPS][16];
   long long scan[FWARPS + 1];
   long long range0, range1, per;
@@ -138,9 +138,9 @@ __global__ void __launch_bounds__(FTHREADS, 1) few_kernel(const __grid_constant_
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int* const ab = &sh.abort;
 
-  if (warp < FWARPS && lane < NST) {
-    mbar_init(smem_u32(&sh.full[warp][lane]), 3);   // the copies' bytes, two scales
-    mbar_init(smem_u32(&sh.empty[warp][lane]), 1);
+  if (warp == 0 && lane < NST) {
+    mbar_init(smem_u32(&sh.full[lane]), 1 + 2 * FWARPS);  // the copies' bytes, the scales
+    mbar_init(smem_u32(&sh.empty[lane]), FWARPS);
   }
   if (warp == FWARPS && lane < QDEPTH) {
     mbar_init(smem_u32(&sh.pq_full[lane]), 1);
@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(FTHREADS, 1) few_kernel(const __grid_constant_
   __syncthreads();
 
   if (warp == FWARPS) {
-    // ---------------- the list of pieces, and their copies: lane 4 w + part for warp w (K, V, K's scale, V's scale)
+    // ---------------- the list of pieces, and their copies
     Cursor at;
     if (a.small_plan) {
       plan_warp<kFewCost, kFewSteps>(a, lane, at.pos, at.end, at.per, at.b, at.t, at.off, at.kvh, at.s);
@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(FTHREADS, 1) few_kernel(const __grid_constant_
       at.b = sh.b0, at.t = sh.t0, at.off = sh.off0, at.kvh = sh.kvh0;
       at.s.start = sh.start0, at.s.ql = sh.ql0, at.s.kl = sh.kl0;
     }
-    const int w = lane >> 2, part = lane & 3;
+    const int pr = min(1 << a.page_shift, BK), npc = BK / pr;  // keys of a copy, copies of a K or V tile
     bool ok = true;
     int u = 0;
     for (int k = 0; ok; ++k) {
@@ -191,30 +191,42 @@ __global__ void __launch_bounds__(FTHREADS, 1) few_kernel(const __grid_constant_
           entry = -1;
           if ((long long)e << a.page_shift < p.kl && (long long)(e + 1) << a.page_shift > p.lo) entry = table[e];
         }
-        const int s = u % NST, key = j * BK + w * FK;
-        const int page = __shfl_sync(0xffffffffu, entry, ((key >> a.page_shift) - entries_at) & 31);
-        if (u >= NST && !(ok = __all_sync(0xffffffffu, cwait(smem_u32(&sh.empty[w][s]), ((u / NST) - 1) & 1, ab)))) break;
-        const uint32_t bar = smem_u32(&sh.full[w][s]);
-        if (part == 0) mbar_expect_tx(bar, C::kStage);
+        const int s = u % NST;
+        if (u >= NST && !(ok = __all_sync(0xffffffffu, cwait(smem_u32(&sh.empty[s]), ((u / NST) - 1) & 1, ab)))) break;
+        const uint32_t bar = smem_u32(&sh.full[s]), dst = base + s * C::kStage;
+        if (lane == 0) mbar_expect_tx(bar, C::kStage);
         __syncwarp();
-        const bool seen = key < p.kl && key + FK > p.lo, good = seen && page >= 0 && page < a.n_pages;
-        if (seen && !good && part == 0 && a.status) atomicOr(a.status, kBadPage);
-        const int head = page * a.n_kv + p.kvh, in_page = key & ((1 << a.page_shift) - 1);
-        if (part < 2) {
-          const int y = good ? (head << a.page_shift) + in_page : a.pool_rows;  // past the end of the pool: the copy fills zeros
-          tma_load_2d(base + (w * NST + s) * C::kStage + part * C::kPart, part ? &tm_v : &tm_k, 0, y, bar);
-        } else {
-          const float* from = part == 2 ? a.k_scales : a.v_scales;
-          if (good) from += ((size_t)head << (a.page_shift - a.block_shift)) + (in_page >> a.block_shift);
-          asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(&sh.scale[w][s][part - 2])), "l"(from), "r"(good ? 4 : 0)
-                       : "memory");
+        {
+          const int x = lane >> 1, v = lane & 1, key = j * BK + x * pr;
+          const int page = __shfl_sync(0xffffffffu, entry, ((key >> a.page_shift) - entries_at) & 31);
+          if (x < npc) {
+            int y = a.pool_rows;  // past the end of the pool: the copy fills zeros
+            if (key < p.kl && key + pr > p.lo) {
+              if (page >= 0 && page < a.n_pages)
+                y = ((page * a.n_kv + p.kvh) << a.page_shift) + (key & ((1 << a.page_shift) - 1));
+              else if (a.status)
+                atomicOr(a.status, kBadPage);
+            }
+            tma_load_2d(dst + v * C::kPart + x * pr * HD, v ? &tm_v : &tm_k, 0, y, bar);
+          }
+        }
+        const int w = lane & 7, v = lane >> 3 & 1, key = j * BK + w * FK;
+        const int page = __shfl_sync(0xffffffffu, entry, ((key >> a.page_shift) - entries_at) & 31);
+        if (lane < 2 * FWARPS) {  // both scales of each warp's keys (no page: 0)
+          const float* from = v ? a.v_scales : a.k_scales;
+          int bytes = 0;
+          if (key < p.kl && key + FK > p.lo && page >= 0 && page < a.n_pages) {
+            from += ((size_t)(page * a.n_kv + p.kvh) << (a.page_shift - a.block_shift)) + ((key & ((1 << a.page_shift) - 1)) >> a.block_shift);
+            bytes = 4;
+          }
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(&sh.scale[s][v][w])), "l"(from), "r"(bytes) : "memory");
           asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
         }
       }
     }
     // no copy may be in flight when the CTA ends
     __syncwarp();
-    for (int x = u > NST ? u - NST : 0; x < u; ++x) cwait(smem_u32(&sh.full[w][x % NST]), (x / NST) & 1, ab, false);
+    for (int x = u > NST ? u - NST : 0; x < u; ++x) cwait(smem_u32(&sh.full[x % NST]), (x / NST) & 1, ab, false);
     if (!ok && a.status && lane == 0) atomicOr(a.status, kTimeout);
     return;
   }
@@ -253,10 +265,10 @@ __global__ void __launch_bounds__(FTHREADS, 1) few_kernel(const __grid_constant_
 #pragma unroll 1
     for (int i = 0; i < n; ++i) {
       const int u = u0 + i, s = u % NST, key0 = (p.ja + i) * BK + warp * FK;
-      ok = __all_sync(0xffffffffu, ok && cwait(smem_u32(&sh.full[warp][s]), (u / NST) & 1, ab));
+      ok = __all_sync(0xffffffffu, ok && cwait(smem_u32(&sh.full[s]), (u / NST) & 1, ab));
       if (!ok) break;
       if (key0 < p.kl && key0 + FK > p.lo) {
-        const uint32_t kt = base + (warp * NST + s) * C::kStage, vt = kt + C::kPart;
+        const uint32_t kt = base + s * C::kStage + warp * FK * HD, vt = kt + C::kPart;
         const bool ragged = __any_sync(0xffffffffu, (row[0].ok && (key0 < row[0].lo || key0 + FK > row[0].hi)) ||
                                                         (WIDE && row[1].ok && (key0 < row[1].lo || key0 + FK > row[1].hi)));
         // ---- S = Q K^T for two groups of eight keys
@@ -292,10 +304,10 @@ __global__ void __launch_bounds__(FTHREADS, 1) few_kernel(const __grid_constant_
                          : "r"(vt + key * HD + (((r >> 1) ^ (key >> 1 & 3)) << 4) + (r & 1) * 8));
           }
         }
-        const float sk = fminf(fmaxf(sh.scale[warp][s][0], 0x1p-64f), 0x1p64f), sv = fminf(fmaxf(sh.scale[warp][s][1], 0x1p-64f), 0x1p64f);
+        const float sk = fminf(fmaxf(sh.scale[s][0][warp], 0x1p-64f), 0x1p64f), sv = fminf(fmaxf(sh.scale[s][1][warp], 0x1p-64f), 0x1p64f);
         const float lsv = log2f(sv), isv = 1.f / sv;
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sh.empty[warp][s]));
+        if (lane == 0) mbar_arrive(smem_u32(&sh.empty[s]));
         if (__builtin_expect(ragged, 0)) {
 #pragma unroll
           for (int t = 0; t < 2; ++t)
@@ -359,7 +371,7 @@ __global__ void __launch_bounds__(FTHREADS, 1) few_kernel(const __grid_constant_
         }
       } else {
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sh.empty[warp][s]));
+        if (lane == 0) mbar_arrive(smem_u32(&sh.empty[s]));
       }
     }
     u0 += n;
