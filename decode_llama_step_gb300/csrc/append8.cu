@@ -14,11 +14,18 @@
 // With the tightest scale each new maximum would round all of them anew.  It
 // costs whole-number codes up to one bit, e4m3 ones nothing.
 //
-// What bounds it: bytes for prompts, latency for single tokens.  A unit of work
-// is a block, a head and K or V: four warps for a block with many new rows, one
-// for a few.  Blocks are found by the row that begins them: a CTA looks over a
-// window of `window` rows (1 to 32, about the rows of a sequence), so the grid
-// follows from the number of rows alone and the lengths stay on the device.
+// What bounds it: bytes for prompts, latency for single tokens.  Blocks are
+// found by the row that begins them: a CTA looks over a window of `window`
+// rows (1 to 32, about the rows of a sequence), so the grid follows from the
+// number of rows alone and the lengths stay on the device.  The CTA's warps
+// share a block's angles (cos and sin of its rows in shared memory: worked out
+// for each head they took as long as everything else).  A unit of work is a
+// block, a head and K or V, and a warp takes it by itself: its rows once for
+// the largest magnitude, and again (from L1 or L2) for the codes, but for the
+// last few, which it still has.  The norm's factor of a row is taken into both
+// at the end.  All warps on one unit, rows in registers in between: a third
+// fewer instructions, half the warps, a barrier a unit, 44 us against 2x for
+// the chunks of a prefill batch.
 #include "kernels.h"
 #include "rope.cuh"
 
@@ -26,7 +33,7 @@ namespace dls {
 
 namespace {
 
-constexpr int ATHREADS = 128;
+constexpr int ATHREADS = 256;
 constexpr int AWARPS = ATHREADS / 32;
 
 struct App8Args {
@@ -42,6 +49,7 @@ struct App8Args {
   int lanes_log2;      // lanes of a row (power of two >= head_dim / 16)
   int window;          // rows that a CTA looks over
   int heads;           // heads of a CTA
+  int angle_rows;      // rows whose angles are held: a block's, or 0 where they are too many
   float eps, inv_hd;
   unsigned long long turn[kMaxPairs];
 };
@@ -96,11 +104,10 @@ __device__ __forceinline__ float scale_for(float amax) {
 }
 
 template <typename IN, int CODE, bool HALVES>
-__global__ void __launch_bounds__(ATHREADS) append8_kernel(const __grid_constant__ App8Args a) {
-  __shared__ float s_max[2][AWARPS];
+__global__ void __launch_bounds__(ATHREADS, 4) append8_kernel(const __grid_constant__ App8Args a) {
+  extern __shared__ float angles[];  // cos [angle_rows][rot_dim / 2], then sin
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const bool is_v = blockIdx.y & 1;
-  const int head0 = (int)(blockIdx.y >> 1) * a.heads, head1 = min(head0 + a.heads, a.n_kv);
+  const int head0 = (int)blockIdx.y * a.heads, n_units = 2 * (min(head0 + a.heads, a.n_kv) - head0);
   const int hd = a.head_dim, block = 1 << a.block_shift;
 
   if (a.status && blockIdx.x == 0 && blockIdx.y == 0 && warp == 0) {
@@ -113,31 +120,42 @@ __global__ void __launch_bounds__(ATHREADS) append8_kernel(const __grid_constant
     if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(a.status, kBadPos);
   }
 
-  // the lane's row of the window: its sequence, position and page, and whether it begins a block
-  const int w0 = blockIdx.x * a.window, row = w0 + lane;
-  const int s0 = seq_of(a.cu_q, a.n_seqs, w0, lane);
-  int b;
+  // the frequencies, read as memory: as a constant, lanes with one each take turns
+  __shared__ unsigned long long s_turn[kMaxPairs];
   {
-    const int c = s0 + 1 + lane <= a.n_seqs ? a.cu_q[s0 + 1 + lane] : 0x7fffffff;
-    b = s0;
-    if (__shfl_sync(0xffffffffu, c, 31) >= w0 + a.window) {
-      for (int i = 0; i < a.window; ++i) {
-        const int n = __popc(__ballot_sync(0xffffffffu, c <= w0 + i));
-        if (lane == i) b = s0 + n;
-      }
-    } else {  // many empty sequences among them
-      int lo = s0, hi = a.n_seqs;  // the first sequence from s0 on that ends behind the row
-      while (lo < hi) {
-        const int mid = lo + (hi - lo) / 2;
-        if (a.cu_q[mid + 1] <= row) lo = mid + 1;
-        else hi = mid;
-      }
-      b = lo;
+    const unsigned long long* turn = a.turn;
+    asm volatile("" : "+l"(turn));
+    if (threadIdx.x < a.rot_dim >> 1) s_turn[threadIdx.x] = turn[threadIdx.x];
+  }
+
+  // the lane's row of the window: its sequence, position and page, and whether it begins a block.  32 sequences from the
+  // window's first on are looked at together, their lengths with them (each load waited for is 0.4 us)
+  const int w0 = blockIdx.x * a.window, row = w0 + lane;
+  const int s0 = a.n_seqs <= 32 ? 0 : seq_of(a.cu_q, a.n_seqs, w0, lane);
+  const bool some = s0 + lane < a.n_seqs;
+  int start = some ? a.cu_q[s0 + lane] : 0, end = some ? a.cu_q[s0 + lane + 1] : 0x7fffffff, kl = some ? a.kv_len[s0 + lane] : 0, b;
+  if (a.n_seqs <= 32 || __shfl_sync(0xffffffffu, end, 31) >= w0 + a.window) {
+    int at = 0;
+    for (int i = 0; i < a.window; ++i) {
+      const int n = __popc(__ballot_sync(0xffffffffu, end <= w0 + i));
+      if (lane == i) at = n;
     }
+    b = s0 + at;  // (at = 32: behind the last sequence)
+    start = __shfl_sync(0xffffffffu, start, at & 31);
+    end = __shfl_sync(0xffffffffu, end, at & 31);
+    kl = __shfl_sync(0xffffffffu, kl, at & 31);
+  } else {  // many empty sequences among them
+    int lo = s0, hi = a.n_seqs;  // the first sequence from s0 on that ends behind the row
+    while (lo < hi) {
+      const int mid = lo + (hi - lo) / 2;
+      if (a.cu_q[mid + 1] <= row) lo = mid + 1;
+      else hi = mid;
+    }
+    b = lo;
+    if (b < a.n_seqs) start = a.cu_q[b], end = a.cu_q[b + 1], kl = a.kv_len[b];
   }
   int pos = 0, page = -1, n_rows = 0;
   if (lane < a.window && row < a.n_tokens && b < a.n_seqs) {
-    const int start = a.cu_q[b], end = a.cu_q[b + 1], kl = a.kv_len[b];
     const long long room = (long long)a.max_pages << a.page_shift;
     // as in the 16-bit append: only these keep the position inside the sequence, whatever cu_q holds
     if (row >= start && row < end && start >= 0 && end <= a.n_tokens && kl >= end - start && kl <= room) {
@@ -157,169 +175,162 @@ __global__ void __launch_bounds__(ATHREADS) append8_kernel(const __grid_constant
   if (!todo) return;
 
   const int lph = 1 << a.lanes_log2, c = lane & (lph - 1), sub = lane >> a.lanes_log2, rps = 32 >> a.lanes_log2;
-  const bool live = 16 * c < hd, rot = 16 * c < a.rot_dim && !is_v;
-  const bool turns = 16 * c < a.rot_dim;
-  const int ea = turns ? 8 * c : 16 * c, eb = turns ? (a.rot_dim >> 1) + 8 * c : 16 * c + 8;  // the lane's two vectors
-  const IN* const src = static_cast<const IN*>(is_v ? a.v : a.k);
-  const long long stride = is_v ? a.v_stride : a.k_stride;
-  uint8_t* const pages = is_v ? a.v_pages : a.k_pages;
-  float* const scales = is_v ? a.v_scales : a.k_scales;
-  const float* const norm = is_v ? nullptr : a.k_norm;
-
-  // values of the lane's sixteen elements: normed, rotated
-  auto finish = [&](float (&xa)[8], float (&xb)[8], int at) {
-    if (norm) {
-      float ss = 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(xa[e], xa[e], fmaf(xb[e], xb[e], ss));
-      for (int o = lph >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      if (live) {
-        Vec8<float> na, nb;
-        na.load(norm + ea);
-        nb.load(norm + eb);
-        float wa[8], wb[8];
-        na.get(wa);
-        nb.get(wb);
-        const float r = rsqrtf(ss * a.inv_hd + a.eps);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) xa[e] *= r * wa[e], xb[e] *= r * wb[e];
-      }
-    }
-    if (rot) {
-      float cs[8], sn[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int pair = HALVES ? 8 * c + e : (e < 4 ? 4 * c + e : (a.rot_dim >> 2) + 4 * c + e - 4);
-        const unsigned long long f = (unsigned long long)(long long)at * a.turn[pair & (kMaxPairs - 1)];
-        sincospif((float)(int)(f >> 32) * 4.656612873077393e-10f, &sn[e], &cs[e]);  // 2^-31: half turns
-      }
-      if (HALVES) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float x = xa[e], y = xb[e];
-          xa[e] = x * cs[e] - y * sn[e];
-          xb[e] = x * sn[e] + y * cs[e];
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float x = xa[2 * e], y = xa[2 * e + 1];
-          xa[2 * e] = x * cs[e] - y * sn[e];
-          xa[2 * e + 1] = x * sn[e] + y * cs[e];
-          x = xb[2 * e], y = xb[2 * e + 1];
-          xb[2 * e] = x * cs[e + 4] - y * sn[e + 4];
-          xb[2 * e + 1] = x * sn[e + 4] + y * cs[e + 4];
-        }
-      }
-    }
+  const int pairs = a.rot_dim >> 1;
+  const bool live = 16 * c < hd, turns = 16 * c < a.rot_dim;
+  const int ea = turns ? 8 * c : 16 * c, eb = turns ? pairs + 8 * c : 16 * c + 8;  // the lane's two vectors
+  auto turned = [&](int at, int pair, float* sine, float* cosine) {
+    const unsigned long long f = (unsigned long long)(long long)at * s_turn[pair];
+    sincospif((float)(int)(f >> 32) * 4.656612873077393e-10f, sine, cosine);  // 2^-31: half turns
   };
 
-  // one block and head: by one warp, or by all of them (wn = 1 or AWARPS, this one the wi-th)
-  auto unit = [&](auto keep, int wn, int wi, int turn_of, int row0, int pos0, int m, int pg, int head) {
-    constexpr int KEEP = decltype(keep)::value;
-    const int off = pos0 & (block - 1);
-    const size_t first = (((size_t)pg * a.n_kv + head) << a.page_shift) + (pos0 & ((1 << a.page_shift) - 1)) - off;  // block's slot 0
-    float* const scale_at = scales + (first >> a.block_shift);
-    uint8_t* const out = pages + first * hd;
-    float old = off ? *scale_at : 0.f;
-    const int steps = (m + wn * rps - 1) / (wn * rps);
-    auto index = [&](int step) { return (step * wn + wi) * rps + sub; };
-    auto fetch = [&](int step, float (&xa)[8], float (&xb)[8]) {
-      const int i = index(step);
+  for (; todo; todo &= todo - 1) {
+    const int from = __ffs(todo) - 1;
+    const int row0 = w0 + from, pos0 = __shfl_sync(0xffffffffu, pos, from), m = __shfl_sync(0xffffffffu, n_rows, from);
+    const int pg = __shfl_sync(0xffffffffu, page, from), off = pos0 & (block - 1);
+    if (pairs) __syncthreads();  // the frequencies are there, the last block's angles used
+    if (a.angle_rows && pairs) {
+      for (int pair = lane; pair < pairs; pair += 32)
+#pragma unroll 2
+        for (int i = warp; i < m; i += AWARPS) turned(pos0 + i, pair, &angles[(a.angle_rows + i) * pairs + pair], &angles[i * pairs + pair]);
+      __syncthreads();
+    }
+#pragma unroll 1
+    for (int index = warp; index < n_units; index += AWARPS) {
+      const bool is_v = index & 1;
+      const int head = head0 + (index >> 1);
+      const long long stride = is_v ? a.v_stride : a.k_stride;
+      const IN* const src = static_cast<const IN*>(is_v ? a.v : a.k) + (size_t)row0 * stride + (size_t)head * hd;
+      const size_t first = (((size_t)pg * a.n_kv + head) << a.page_shift) + (pos0 & ((1 << a.page_shift) - 1)) - off;  // block's slot 0
+      uint8_t* const out = (is_v ? a.v_pages : a.k_pages) + first * hd;
+      float* const scale_at = (is_v ? a.v_scales : a.k_scales) + (first >> a.block_shift);
+      float old = off ? *scale_at : 0.f;
+      Vec8<IN> va, vb;
+      // (lanes past the block's rows take its last one again: it changes no maximum)
+      auto fetch = [&](int s) {
+        const IN* const p = src + min(s + sub, m - 1) * stride;
+        if (live) va.load(p + ea), vb.load(p + eb);
+      };
+      float xa[8], xb[8], r = 1.f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) xa[e] = xb[e] = 0.f;
-      if (live && i < m) {
-        const IN* const p = src + (size_t)(row0 + i) * stride + (size_t)head * hd;
-        Vec8<IN> va, vb;
-        va.load(p + ea);
-        vb.load(p + eb);
-        va.get(xa);
-        vb.get(xb);
-      }
-    };
-    float xa[KEEP][8], xb[KEEP][8];
-    float amax = 0.f;
-    auto most = [&](const float (&u)[8], const float (&v)[8]) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fmaxf(fabsf(u[e]), fabsf(v[e])));
-    };
-#pragma unroll
-    for (int s = 0; s < KEEP; ++s) fetch(s, xa[s], xb[s]);
-#pragma unroll
-    for (int s = 0; s < KEEP; ++s)
-      if (s < steps) {
-        finish(xa[s], xb[s], pos0 + index(s));
-        most(xa[s], xb[s]);
-      }
-#pragma unroll 1
-    for (int s = KEEP; s < steps; ++s) {
-      float u[8], v[8];
-      fetch(s, u, v);
-      finish(u, v, pos0 + index(s));
-      most(u, v);
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    if (wn > 1) {  // (two sets of maxima: a warp may begin the next unit while another still reads these)
-      if (lane == 0) s_max[turn_of & 1][warp] = amax;
-      __syncthreads();
-#pragma unroll
-      for (int w = 0; w < AWARPS; ++w) amax = fmaxf(amax, s_max[turn_of & 1][w]);
-    }
-    const float need = scale_for<CODE>(fminf(amax, 3.402823466e38f));
-    float scale = need;
-    if (off) {
-      old = fminf(fmaxf(old, 0x1p-64f), 0x1p64f);  // (also of a scale that is none)
-      scale = fmaxf(old, need);
-      if (scale > old) {
-        const float f = old / scale;
-        for (int i = (wi * 32 + lane) * 16; i < off * hd; i += wn * 512) {
-          uint4 w = *reinterpret_cast<const uint4*>(out + i);
-          uint32_t* const u = reinterpret_cast<uint32_t*>(&w);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            float x[4];
-            Coder<CODE>::values(u[k], x);
-            u[k] = Coder<CODE>::four(x[0] * f, x[1] * f, x[2] * f, x[3] * f);
-          }
-          *reinterpret_cast<uint4*>(out + i) = w;
+      // the fetched row's values but for its norm's factor r; `next`: the row fetched after it, none past the end
+      auto values = [&](int s, int next) {
+        if (live) {
+          va.get(xa);
+          vb.get(xb);
         }
-      }
-    }
-    if (wi == 0 && lane == 0) *scale_at = scale;
-    const float inv = 1.f / scale;
-    auto store = [&](int step, const float (&u)[8], const float (&v)[8]) {
-      const int i = index(step);
-      if (!live || i >= m) return;
-      uint8_t* const p = out + (size_t)(off + i) * hd;
-      *reinterpret_cast<uint2*>(p + ea) = make_uint2(Coder<CODE>::four(u[0] * inv, u[1] * inv, u[2] * inv, u[3] * inv),
-                                                     Coder<CODE>::four(u[4] * inv, u[5] * inv, u[6] * inv, u[7] * inv));
-      *reinterpret_cast<uint2*>(p + eb) = make_uint2(Coder<CODE>::four(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
-                                                     Coder<CODE>::four(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv));
-    };
+        if (next < m) fetch(next);
+        if (is_v) return;
+        if (a.k_norm) {
+          float ss = 0.f;
 #pragma unroll
-    for (int s = 0; s < KEEP; ++s)
-      if (s < steps) store(s, xa[s], xb[s]);
-#pragma unroll 1
-    for (int s = KEEP; s < steps; ++s) {
-      float u[8], v[8];
-      fetch(s, u, v);
-      finish(u, v, pos0 + index(s));
-      store(s, u, v);
-    }
-  };
+          for (int e = 0; e < 8; ++e) ss = fmaf(xa[e], xa[e], fmaf(xb[e], xb[e], ss));
+          for (int o = lph >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+          r = rsqrtf(ss * a.inv_hd + a.eps);
+          if (live) {
+            Vec8<float> na, nb;
+            na.load(a.k_norm + ea);
+            nb.load(a.k_norm + eb);
+            float wa[8], wb[8];
+            na.get(wa);
+            nb.get(wb);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) xa[e] *= wa[e], xb[e] *= wb[e];
+          }
+        }
+        if (turns) {
+          // (pairs 8 c .. of the halves pairing; 4 c .. of each vector in the adjacent one)
+          const int i = min(s + sub, m - 1), q0 = HALVES ? 8 * c : 4 * c, q1 = HALVES ? q0 + 4 : q0 + (pairs >> 1);
+          float cs[8], sn[8];
+          if (a.angle_rows) {
+            const float *const cosines = angles + i * pairs, *const sines = cosines + a.angle_rows * pairs;
+            *reinterpret_cast<float4*>(cs) = *reinterpret_cast<const float4*>(cosines + q0);
+            *reinterpret_cast<float4*>(cs + 4) = *reinterpret_cast<const float4*>(cosines + q1);
+            *reinterpret_cast<float4*>(sn) = *reinterpret_cast<const float4*>(sines + q0);
+            *reinterpret_cast<float4*>(sn + 4) = *reinterpret_cast<const float4*>(sines + q1);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) turned(pos0 + i, (e < 4 ? q0 : q1 - 4) + e, &sn[e], &cs[e]);
+          }
+          if (HALVES) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float x = xa[e], y = xb[e];
+              xa[e] = x * cs[e] - y * sn[e];
+              xb[e] = x * sn[e] + y * cs[e];
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              float x = xa[2 * e], y = xa[2 * e + 1];
+              xa[2 * e] = x * cs[e] - y * sn[e];
+              xa[2 * e + 1] = x * sn[e] + y * cs[e];
+              x = xb[2 * e], y = xb[2 * e + 1];
+              xb[2 * e] = x * cs[e + 4] - y * sn[e + 4];
+              xb[2 * e + 1] = x * sn[e + 4] + y * cs[e + 4];
+            }
+          }
+        }
+      };
 
-  const int few = 2 * rps;  // rows that one warp takes by itself
-  int at = 0, big = 0;
-  for (unsigned left = todo; left; left &= left - 1) {
-    const int from = __ffs(left) - 1;
-    const int row0 = w0 + from, pos0 = __shfl_sync(0xffffffffu, pos, from), m = __shfl_sync(0xffffffffu, n_rows, from);
-    const int pg = __shfl_sync(0xffffffffu, page, from);
-    for (int h = head0; h < head1; ++h) {
-      if (m <= few) {
-        if ((at++ & (AWARPS - 1)) == warp) unit(std::integral_constant<int, 2>(), 1, 0, 0, row0, pos0, m, pg, h);
-      } else {
-        unit(std::integral_constant<int, 4>(), AWARPS, warp, big++, row0, pos0, m, pg, h);
+      float amax = 0.f, scale = 0.f, inv = 0.f;
+      const int last = (m - 1) / rps * rps;
+      fetch(0);
+#pragma unroll 1
+      for (int turn_no = 0; turn_no < 2; ++turn_no) {
+        // first all rows for the magnitude, then the codes: of the last ones, which are still there, and of those before
+        if (turn_no) {
+#pragma unroll
+          for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+          scale = scale_for<CODE>(fminf(amax, 3.402823466e38f));
+          if (off) {  // earlier tokens of the block
+            old = fminf(fmaxf(old, 0x1p-64f), 0x1p64f);  // (also of a scale that is none)
+            scale = fmaxf(old, scale);
+            if (scale > old) {
+              const float f = old / scale;
+#pragma unroll 1
+              for (int i = lane * 16; i < off * hd; i += 512) {
+                uint4 w = *reinterpret_cast<const uint4*>(out + i);
+                uint32_t* const u = reinterpret_cast<uint32_t*>(&w);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  float x[4];
+                  Coder<CODE>::values(u[k], x);
+                  u[k] = Coder<CODE>::four(x[0] * f, x[1] * f, x[2] * f, x[3] * f);
+                }
+                *reinterpret_cast<uint4*>(out + i) = w;
+              }
+            }
+          }
+          if (lane == 0) *scale_at = scale;
+          inv = 1.f / scale;
+        }
+#pragma unroll 1
+        for (int s = turn_no ? last : 0;;) {
+          // (the second turn goes last, 0, 1, ...)
+          const int next = turn_no && s == last ? 0 : s + rps;
+          if (!turn_no) {
+            values(s, next);
+            float most = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) most = fmaxf(most, fmaxf(fabsf(xa[e]), fabsf(xb[e])));
+            amax = fmaxf(amax, most * r);
+            if (s == last) break;
+          } else {
+            const float f = r * inv;
+            if (live && s + sub < m) {
+              uint8_t* const p = out + (size_t)(off + s + sub) * hd;
+              *reinterpret_cast<uint2*>(p + ea) = make_uint2(Coder<CODE>::four(xa[0] * f, xa[1] * f, xa[2] * f, xa[3] * f),
+                                                             Coder<CODE>::four(xa[4] * f, xa[5] * f, xa[6] * f, xa[7] * f));
+              *reinterpret_cast<uint2*>(p + eb) = make_uint2(Coder<CODE>::four(xb[0] * f, xb[1] * f, xb[2] * f, xb[3] * f),
+                                                             Coder<CODE>::four(xb[4] * f, xb[5] * f, xb[6] * f, xb[7] * f));
+            }
+            if (next == last) break;
+            if (s == last) fetch(0);
+            values(next, next + rps);
+          }
+          s = next;
+        }
       }
     }
   }
@@ -327,8 +338,13 @@ __global__ void __launch_bounds__(ATHREADS) append8_kernel(const __grid_constant
 
 template <typename IN, int CODE>
 cudaError_t launch_append8(const App8Args& a, int pairing, dim3 grid, cudaStream_t s) {
-  if (pairing == DLS_ROPE_HALVES) append8_kernel<IN, CODE, true><<<grid, ATHREADS, 0, s>>>(a);
-  else append8_kernel<IN, CODE, false><<<grid, ATHREADS, 0, s>>>(a);
+  const int smem = a.angle_rows * a.rot_dim * 4;
+  void (*const f)(const App8Args) = pairing == DLS_ROPE_HALVES ? append8_kernel<IN, CODE, true> : append8_kernel<IN, CODE, false>;
+  if (smem > 40 * 1024) {  // beyond what a launch may ask for unannounced
+    const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, 65536);
+    if (e != cudaSuccess) return e;
+  }
+  f<<<grid, ATHREADS, smem, s>>>(a);
   return cudaGetLastError();
 }
 template <typename IN>
@@ -385,8 +401,13 @@ extern "C" int dls_kv_append8(const dls_kv_append8_desc* d, void* cuda_stream) {
   const int mean = d->n_tokens / d->n_seqs;  // rows of a sequence, about
   a.window = 1;
   while (a.window < 32 && a.window * 2 <= mean) a.window *= 2;
-  a.heads = mean < 2 ? std::min(4, d->n_kv_heads) : 1;
-  const dim3 grid((unsigned)((d->n_tokens + a.window - 1) / a.window), (unsigned)((d->n_kv_heads + a.heads - 1) / a.heads) * 2);
+  a.heads = std::min(AWARPS / 2, d->n_kv_heads);  // a unit a warp
+  const unsigned groups = (unsigned)((d->n_kv_heads + a.heads - 1) / a.heads);
+  // smaller windows where CTAs are few: the blocks that begin in one are taken one after another
+  while (a.window > 4 && (long long)(d->n_tokens / a.window) * groups < 304) a.window /= 2;
+  const unsigned windows = (unsigned)((d->n_tokens + a.window - 1) / a.window);
+  a.angle_rows = bt * a.rot_dim <= 16384 ? bt : 0;
+  const dim3 grid(windows, groups);
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
   cudaError_t e = cudaSuccess;
   if (a.status) e = cudaMemsetAsync(a.status, 0, sizeof(int32_t), s);
