@@ -93,6 +93,13 @@ struct Coder<DLS_I8> {
   }
 };
 
+__device__ __forceinline__ void scale2(float& x, float& y, f2_t f) {
+  f2_t p;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(p) : "l"(pk2(x, y)), "l"(f));
+  const float2 v = upk2(p);
+  x = v.x, y = v.y;
+}
+
 constexpr int kLeastExp = -64, kMostExp = 64;  // of a scale
 
 // 2^e for the largest magnitude of a block.
@@ -135,11 +142,11 @@ __global__ void __launch_bounds__(ATHREADS, 4) append8_kernel(const __grid_const
   const bool some = s0 + lane < a.n_seqs;
   int start = some ? a.cu_q[s0 + lane] : 0, end = some ? a.cu_q[s0 + lane + 1] : 0x7fffffff, kl = some ? a.kv_len[s0 + lane] : 0, b;
   if (a.n_seqs <= 32 || __shfl_sync(0xffffffffu, end, 31) >= w0 + a.window) {
-    int at = 0;
-    for (int i = 0; i < a.window; ++i) {
-      const int n = __popc(__ballot_sync(0xffffffffu, end <= w0 + i));
-      if (lane == i) at = n;
-    }
+    int at = 0;  // how many of the ends are not behind the row
+#pragma unroll
+    for (int step = 16; step; step >>= 1)
+      if (__shfl_sync(0xffffffffu, end, at + step - 1) <= row) at += step;
+    at += __shfl_sync(0xffffffffu, end, at) <= row;
     b = s0 + at;  // (at = 32: behind the last sequence)
     start = __shfl_sync(0xffffffffu, start, at & 31);
     end = __shfl_sync(0xffffffffu, end, at & 31);
@@ -222,9 +229,13 @@ __global__ void __launch_bounds__(ATHREADS, 4) append8_kernel(const __grid_const
         if (next < m) fetch(next);
         if (is_v) return;
         if (a.k_norm) {
-          float ss = 0.f;
+          f2_t s2 = pk2(0.f, 0.f);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) ss = fmaf(xa[e], xa[e], fmaf(xb[e], xb[e], ss));
+          for (int e = 0; e < 8; e += 2) {
+            const f2_t x = pk2(xa[e], xa[e + 1]), y = pk2(xb[e], xb[e + 1]);
+            s2 = ffma2(x, x, ffma2(y, y, s2));
+          }
+          float ss = upk2(s2).x + upk2(s2).y;
           for (int o = lph >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
           r = rsqrtf(ss * a.inv_hd + a.eps);
           if (live) {
@@ -235,7 +246,7 @@ __global__ void __launch_bounds__(ATHREADS, 4) append8_kernel(const __grid_const
             na.get(wa);
             nb.get(wb);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) xa[e] *= wa[e], xb[e] *= wb[e];
+            for (int e = 0; e < 8; e += 2) scale2(xa[e], xa[e + 1], pk2(wa[e], wa[e + 1])), scale2(xb[e], xb[e + 1], pk2(wb[e], wb[e + 1]));
           }
         }
         if (turns) {
@@ -318,12 +329,15 @@ __global__ void __launch_bounds__(ATHREADS, 4) append8_kernel(const __grid_const
             if (s == last) break;
           } else {
             const float f = r * inv;
+            const f2_t f2 = pk2(f, f);
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) scale2(xa[e], xa[e + 1], f2), scale2(xb[e], xb[e + 1], f2);
             if (live && s + sub < m) {
               uint8_t* const p = out + (size_t)(off + s + sub) * hd;
-              *reinterpret_cast<uint2*>(p + ea) = make_uint2(Coder<CODE>::four(xa[0] * f, xa[1] * f, xa[2] * f, xa[3] * f),
-                                                             Coder<CODE>::four(xa[4] * f, xa[5] * f, xa[6] * f, xa[7] * f));
-              *reinterpret_cast<uint2*>(p + eb) = make_uint2(Coder<CODE>::four(xb[0] * f, xb[1] * f, xb[2] * f, xb[3] * f),
-                                                             Coder<CODE>::four(xb[4] * f, xb[5] * f, xb[6] * f, xb[7] * f));
+              *reinterpret_cast<uint2*>(p + ea) = make_uint2(Coder<CODE>::four(xa[0], xa[1], xa[2], xa[3]),
+                                                             Coder<CODE>::four(xa[4], xa[5], xa[6], xa[7]));
+              *reinterpret_cast<uint2*>(p + eb) = make_uint2(Coder<CODE>::four(xb[0], xb[1], xb[2], xb[3]),
+                                                             Coder<CODE>::four(xb[4], xb[5], xb[6], xb[7]));
             }
             if (next == last) break;
             if (s == last) fetch(0);
