@@ -26,9 +26,12 @@ namespace dls {
 
 namespace {
 
-constexpr int RSV_THREADS = 1024;
-constexpr int RSV_WARPS = RSV_THREADS / 32;
-constexpr int kPerThread = DLS_MAX_CHUNK_SEQS / RSV_THREADS;  // sequences of a thread at most
+constexpr int kMostThreads = 1024;
+constexpr int kPerThread = DLS_MAX_CHUNK_SEQS / kMostThreads;  // sequences of a thread at most
+constexpr int kRowsLane = 4;                                   // rows of a lane at a time
+// Sums stop here, above every bound that they are held to (2^27 pages, 2^30 rows): sums cut off so stay a prefix sum,
+// and those that matter are exact.
+constexpr unsigned kCap = (1u << 30) + 1;
 
 struct ReserveArgs {
   const int32_t *new_len, *kv_len, *held, *free_count;
@@ -56,142 +59,122 @@ __device__ __forceinline__ unsigned cluster_size() {
   return r;
 }
 
-// Exclusive prefix sums of two values over the block; the totals too.
-__device__ __forceinline__ void block_scan2(long long& x, long long& y, long long& tx, long long& ty, longlong2* sums) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  long long ix = x, iy = y;
+__device__ __forceinline__ unsigned capped(unsigned a, unsigned b) { return min(a + b, kCap); }  // (both at most kCap)
+
+// Inclusive prefix sums of two values over the warp.
+__device__ __forceinline__ void warp_scan2(unsigned& x, unsigned& y, int lane) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long ux = __shfl_up_sync(0xffffffffu, ix, o), uy = __shfl_up_sync(0xffffffffu, iy, o);
-    if (lane >= o) ix += ux, iy += uy;
+    const unsigned ux = __shfl_up_sync(0xffffffffu, x, o), uy = __shfl_up_sync(0xffffffffu, y, o);
+    if (lane >= o) x = capped(x, ux), y = capped(y, uy);
   }
-  __syncthreads();  // the sums' last readers are through
-  if (lane == 31) sums[warp] = make_longlong2(ix, iy);
+}
+// Of two values a thread: the sums of the threads before, and of all.
+__device__ __forceinline__ void block_scan2(unsigned x, unsigned y, uint2& before, uint2& total, uint2* sums) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  unsigned ix = x, iy = y;
+  warp_scan2(ix, iy, lane);
+  if (lane == 31) sums[warp] = make_uint2(ix, iy);
+  const unsigned px = __shfl_up_sync(0xffffffffu, ix, 1), py = __shfl_up_sync(0xffffffffu, iy, 1);
   __syncthreads();
   // every warp scans the warps' sums by itself
-  longlong2 w = sums[lane];
-  const longlong2 mine = w;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long ux = __shfl_up_sync(0xffffffffu, w.x, o), uy = __shfl_up_sync(0xffffffffu, w.y, o);
-    if (lane >= o) w.x += ux, w.y += uy;
-  }
-  tx = __shfl_sync(0xffffffffu, w.x, 31);
-  ty = __shfl_sync(0xffffffffu, w.y, 31);
-  const long long px = __shfl_sync(0xffffffffu, w.x - mine.x, warp), py = __shfl_sync(0xffffffffu, w.y - mine.y, warp);
-  x = px + ix - x;
-  y = py + iy - y;
+  const uint2 w = lane < (int)(blockDim.x >> 5) ? sums[lane] : make_uint2(0, 0);
+  unsigned wx = w.x, wy = w.y;
+  warp_scan2(wx, wy, lane);
+  total = make_uint2(__shfl_sync(0xffffffffu, wx, 31), __shfl_sync(0xffffffffu, wy, 31));
+  const unsigned bx = __shfl_sync(0xffffffffu, wx, (warp + 31) & 31), by = __shfl_sync(0xffffffffu, wy, (warp + 31) & 31);
+  before = make_uint2(capped(warp ? bx : 0, lane ? px : 0), capped(warp ? by : 0, lane ? py : 0));
 }
-static_assert(RSV_WARPS == 32, "block_scan2 gives each warp's sum to a lane");
 
-__global__ void __launch_bounds__(RSV_THREADS, 1) reserve_kernel(const __grid_constant__ ReserveArgs a) {
-  extern __shared__ uint8_t rsm[];
-  __shared__ longlong2 sums[32];
+__global__ void __launch_bounds__(kMostThreads, 1) reserve_kernel(const __grid_constant__ ReserveArgs a) {
+  extern __shared__ __align__(16) uint8_t rsm[];
+  __shared__ uint2 sums[2][32];
+  __shared__ int s_flags, s_used, s_end;
   int* const cu = reinterpret_cast<int*>(rsm);                       // [n_seqs + 1]
   SeqRow* const rows = reinterpret_cast<SeqRow*>(cu + a.n_seqs + 1);  // [n_seqs]
-  const int tid = threadIdx.x, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31, threads = blockDim.x;
   const unsigned rank = cluster_rank(), ctas = cluster_size();
   const int page = 1 << a.page_shift;
   const long long room = (long long)a.max_pages << a.page_shift;
-  const int per = (a.n_seqs + RSV_THREADS - 1) / RSV_THREADS, b0 = min(tid * per, a.n_seqs), b1 = min(b0 + per, a.n_seqs);
+  const int per = (a.n_seqs + threads - 1) / threads, b0 = min(tid * per, a.n_seqs), b1 = min(b0 + per, a.n_seqs);
 
   int fresh[kPerThread], kv[kPerThread], held[kPerThread], need[kPerThread];
   bool grant[kPerThread];
   int flags = 0;
-  const int count_in = *a.free_count, count = min(max(count_in, 0), a.n_pages);
-  if (count != count_in) flags |= kBadPos;
-  long long give_sum = 0, need_sum = 0;
+  if (tid == 0) s_flags = s_used = s_end = 0;
+  const int count_in = *a.free_count;
 #pragma unroll
   for (int i = 0; i < kPerThread; ++i) {
-    fresh[i] = kv[i] = held[i] = need[i] = 0;
-    grant[i] = false;
-    if (b0 + i >= b1) continue;
-    fresh[i] = a.new_len[b0 + i], kv[i] = a.kv_len[b0 + i], held[i] = a.held[b0 + i];
+    fresh[i] = kv[i] = held[i] = 0;
+    if (b0 + i < b1) fresh[i] = a.new_len[b0 + i], kv[i] = a.kv_len[b0 + i], held[i] = a.held[b0 + i];
+  }
+  const int count = min(max(count_in, 0), a.n_pages);
+  if (count != count_in) flags |= kBadPos;
+  unsigned give_sum = 0, need_sum = 0;
+#pragma unroll
+  for (int i = 0; i < kPerThread; ++i) {
     // a state that cannot be: the request is left out, its pages are not given back
     const bool bad = kv[i] < 0 || kv[i] > room || held[i] < 0 || held[i] > a.max_pages || ((long long)held[i] << a.page_shift) < kv[i];
     const bool far = fresh[i] > 0 && (long long)kv[i] + fresh[i] > room;
     if (bad || far) flags |= kBadPos;
     grant[i] = !bad && !far && fresh[i] > 0;
-    if (grant[i]) need[i] = max(0, (int)(((long long)kv[i] + fresh[i] + page - 1) >> a.page_shift) - held[i]);
-    if (fresh[i] < 0 && !bad) give_sum += held[i];
-    else if (fresh[i] < 0) held[i] = 0;
-    need_sum += need[i];
+    need[i] = grant[i] ? max(0, (int)(((long long)kv[i] + fresh[i] + page - 1) >> a.page_shift) - held[i]) : 0;
+    if (fresh[i] < 0 && bad) held[i] = 0;
+    if (fresh[i] < 0) give_sum = capped(give_sum, held[i]);
+    need_sum = capped(need_sum, need[i]);
   }
-  long long give_at = give_sum, need_at = need_sum, give_total, need_total;
-  block_scan2(give_at, need_at, give_total, need_total, sums);
-  if (count + give_total > a.n_pages) flags |= kBadPos;  // (more pages than the pool has: the rest is dropped)
-  const int avail = (int)min(count + give_total, (long long)a.n_pages);
+  uint2 before, total;
+  block_scan2(give_sum, need_sum, before, total, sums[0]);
+  const unsigned give_before = before.x, need_before = before.y;
+  if (capped(count, total.x) > (unsigned)a.n_pages) flags |= kBadPos;  // (more pages than the pool has: the rest is dropped)
+  const unsigned avail = min(capped(count, total.x), (unsigned)a.n_pages);
   // pages
-  long long row_sum = 0;
-  {
-    long long at = need_at;
+  unsigned row_sum = 0, at = need_before;
 #pragma unroll
-    for (int i = 0; i < kPerThread; ++i) {
-      at += need[i];
-      if (grant[i] && need[i] && at > avail) grant[i] = false, flags |= kNoRoom;
-      if (grant[i]) row_sum += fresh[i];
-    }
+  for (int i = 0; i < kPerThread; ++i) {
+    at = capped(at, need[i]);
+    if (grant[i] && need[i] && at > avail) grant[i] = false, flags |= kNoRoom;
+    if (grant[i]) row_sum = capped(row_sum, min((unsigned)fresh[i], kCap));
   }
-  long long row_at = row_sum, zero = 0, row_total, none;
-  block_scan2(row_at, zero, row_total, none, sums);
+  block_scan2(row_sum, 0, before, total, sums[1]);
   // rows, and what is left of both
-  long long used = 0;
-  int last = 0;  // one past the thread's last row
-  {
-    long long at = row_at, pop = need_at, give = give_at;
+  unsigned pop = need_before, give = give_before;
+  int used = 0, end = 0;
+  at = before.x;
 #pragma unroll
-    for (int i = 0; i < kPerThread; ++i) {
-      if (b0 + i >= b1) continue;
-      const bool asked = grant[i];
-      if (asked) at += fresh[i];
-      if (asked && at > a.max_rows) grant[i] = false, flags |= kNoRoom;
-      SeqRow r;
-      r.kv = kv[i], r.held = held[i];
-      r.pop = fresh[i] < 0 ? (int)min(count + give, (long long)a.n_pages) : (int)max(avail - 1 - pop, -1ll);
-      rows[b0 + i] = r;
-      cu[b0 + i + 1] = grant[i] ? (int)at : -1;  // where it ends; settled below
-      if (fresh[i] < 0) give += held[i];
-      pop += need[i];
-      if (grant[i]) used += need[i], last = (int)at;
-      else need[i] = 0;
-    }
+  for (int i = 0; i < kPerThread; ++i) {
+    if (b0 + i >= b1) continue;
+    if (grant[i]) at = capped(at, min((unsigned)fresh[i], kCap));
+    const bool fits = at <= (unsigned)a.max_rows;
+    if (grant[i] && !fits) grant[i] = false, flags |= kNoRoom;
+    if (fits) end = (int)at;
+    SeqRow r;
+    r.kv = kv[i], r.held = held[i];
+    r.pop = fresh[i] < 0 ? (int)min(capped(count, give), (unsigned)a.n_pages) : pop < avail ? (int)(avail - 1 - pop) : -1;
+    rows[b0 + i] = r;
+    cu[b0 + i + 1] = fits ? (int)at : -1;  // (-1: where the last rows that fit end)
+    if (fresh[i] < 0) give = capped(give, held[i]);
+    pop = capped(pop, need[i]);
+    if (!grant[i]) need[i] = 0;
+    used += need[i];
   }
-  // totals of what was granted: pages used, and the end of the rows
-#pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    used += __shfl_xor_sync(0xffffffffu, used, o);
-    last = max(last, __shfl_xor_sync(0xffffffffu, last, o));
-    flags |= __shfl_xor_sync(0xffffffffu, flags, o);
+  used = (int)__reduce_add_sync(0xffffffffu, (unsigned)used);
+  end = (int)__reduce_max_sync(0xffffffffu, (unsigned)end);
+  flags = (int)__reduce_or_sync(0xffffffffu, (unsigned)flags);
+  if (lane == 0) {
+    atomicMax(&s_end, end);
+    if (used) atomicAdd(&s_used, used);
+    if (flags) atomicOr(&s_flags, flags);
   }
-  __shared__ int w_last[RSV_WARPS], w_flags[RSV_WARPS];
-  __shared__ long long w_used[RSV_WARPS];
-  if (lane == 0) w_last[tid >> 5] = last, w_used[tid >> 5] = used, w_flags[tid >> 5] = flags;
-  // a sequence without rows ends where the one before it does
-  __syncthreads();
-  int end = 0;  // the end of the rows before this thread's sequences
-  for (int w = 0; w < (tid >> 5); ++w) end = max(end, w_last[w]);
-  {
-    int mine = 0;
-    for (int b = b0; b < b1; ++b) mine = max(mine, cu[b + 1]);
-    int pre = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, pre, o);
-      if (lane >= o) pre = max(pre, u);
-    }
-    const int before = __shfl_up_sync(0xffffffffu, pre, 1);
-    if (lane) end = max(end, before);
-    for (int b = b0; b < b1; ++b) cu[b + 1] = end = max(end, cu[b + 1]);
-  }
-  int total = 0;
-  used = 0;
-  for (int w = 0; w < RSV_WARPS; ++w) total = max(total, w_last[w]), used += w_used[w], flags |= w_flags[w];
   if (tid == 0) cu[0] = 0;
-  __syncthreads();
+  const bool gives = __syncthreads_or(give_sum != 0);
+  const int all = s_end;
+  for (int b = b0; b < b1; ++b)
+    if (cu[b + 1] < 0) cu[b + 1] = all;
 
   // pages of ended requests go on the stack: 32 sequences a look, a warp for each of theirs
-  const int warps = ctas * RSV_WARPS, warp = rank * RSV_WARPS + (tid >> 5);
-  for (int b = warp * 32; b < a.n_seqs; b += warps * 32) {
+  const int warps = ctas * (threads >> 5), warp = rank * (threads >> 5) + (tid >> 5);
+  for (int b = warp * 32; gives && b < a.n_seqs; b += warps * 32) {
     const bool over = b + lane < a.n_seqs && a.new_len[b + lane] < 0 && rows[b + lane].held > 0;
     unsigned todo = __ballot_sync(0xffffffffu, over);
     while (todo) {
@@ -205,8 +188,10 @@ __global__ void __launch_bounds__(RSV_THREADS, 1) reserve_kernel(const __grid_co
   cluster_meet();  // (the state is read, the stack is whole)
 
   if (rank == 0) {
-    for (int i = 0; b0 + i < b1; ++i) {
+#pragma unroll
+    for (int i = 0; i < kPerThread; ++i) {
       const int b = b0 + i;
+      if (b >= b1) continue;
       const bool over = fresh[i] < 0;
       a.kv_len_out[b] = over ? 0 : kv[i] + cu[b + 1] - cu[b];
       a.held_out[b] = over ? 0 : held[i] + need[i];
@@ -214,53 +199,66 @@ __global__ void __launch_bounds__(RSV_THREADS, 1) reserve_kernel(const __grid_co
     }
     if (tid == 0) {
       a.cu_q[0] = 0;
-      *a.free_count_out = avail - (int)used;
-      if (a.status) atomicOr(a.status, flags);
+      *a.free_count_out = (int)avail - s_used;
+      if (a.status) atomicOr(a.status, s_flags);
     }
   }
 
-  // rows: a warp takes a run of them, 32 at a time
-  const long long share = ((long long)total + warps - 1) / warps;
-  const int r0 = (int)min(share * warp, (long long)total), r1 = (int)min((long long)r0 + share, (long long)total);
+  // Rows: a warp takes a run of them, a lane four neighbours at a time, which as a rule are of one sequence and
+  // one page.  (16-byte stores where the arrays allow.)
+  constexpr int kTurn = 32 * kRowsLane;
+  const int share = ((all + warps - 1) / warps + kRowsLane - 1) / kRowsLane * kRowsLane;
+  const int r0 = (int)min((long long)share * warp, (long long)all), r1 = min(r0 + share, all);
   bool bad_page = false;
-  int s = 0;
-  if (r0 < r1) {
-    int lo = 0, hi = a.n_seqs;  // the last sequence that begins at r0 or before and is not empty
+  auto seq_from = [&](int lo, int row) {  // the sequence from lo on that holds the row: the last that begins there or before
+    if (cu[lo + 1] > row) return lo;
+    int hi = a.n_seqs;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (cu[mid] <= r0) lo = mid;
+      if (cu[mid] <= row) lo = mid;
       else hi = mid;
     }
-    s = lo;
-  }
-  for (int r = r0; r < r1; r += 32) {
-    const int row = r + lane;
-    if (row < r1) {
-      if (cu[s + 1] <= row) {
-        int lo = s, hi = a.n_seqs;
-        while (hi - lo > 1) {
-          const int mid = (lo + hi) >> 1;
-          if (cu[mid] <= row) lo = mid;
-          else hi = mid;
-        }
-        s = lo;
+    return lo;
+  };
+  auto page_of = [&](int s, const SeqRow& q, int j, bool first) {  // first: the row that enters a fresh page in the table
+    if (j < q.held) return a.page_table[(size_t)s * a.max_pages + j];
+    const int x = q.pop - (j - q.held), p = x >= 0 ? a.free_pages[x] : -1;
+    if (first) a.page_table[(size_t)s * a.max_pages + j] = p;
+    return p;
+  };
+  int s = 0;
+  for (int r = r0 + lane * kRowsLane; r < r1; r += kTurn) {
+    int pos[kRowsLane], slot[kRowsLane], id[kRowsLane];
+    s = seq_from(s, r);
+    const int n = min(kRowsLane, r1 - r);
+    SeqRow q = rows[s];
+    int begin = cu[s], end_s = cu[s + 1], x = s, last = -1, p = -1;
+#pragma unroll
+    for (int i = 0; i < kRowsLane; ++i) {
+      if (i >= n) continue;
+      if (r + i >= end_s) {
+        x = seq_from(x, r + i);
+        q = rows[x], begin = cu[x], end_s = cu[x + 1], last = -1;
       }
-      const SeqRow q = rows[s];
-      const int pos = q.kv + row - cu[s], j = pos >> a.page_shift, off = pos & (page - 1);
-      int p;
-      if (j >= q.held) {
-        const int at = q.pop - (j - q.held);
-        p = at >= 0 ? a.free_pages[at] : -1;
-        if (off == 0) a.page_table[(size_t)s * a.max_pages + j] = p;
-      } else {
-        p = a.page_table[(size_t)s * a.max_pages + j];
-      }
+      const int at_pos = q.kv + r + i - begin, j = at_pos >> a.page_shift, off = at_pos & (page - 1);
+      if (j != last || off == 0) p = page_of(x, q, j, off == 0), last = j;
       const bool ok = p >= 0 && p < a.n_pages;
       bad_page |= !ok;
-      if (a.positions) a.positions[row] = pos;
-      if (a.slots) a.slots[row] = ok ? (p << a.page_shift) + off : -1;
-      if (a.seq_ids) a.seq_ids[row] = s;
+      pos[i] = at_pos, slot[i] = ok ? (p << a.page_shift) + off : -1, id[i] = x;
     }
+    auto put = [&](int32_t* to, const int (&v)[kRowsLane]) {
+      if (!to) return;
+      if (n == kRowsLane && !(reinterpret_cast<uintptr_t>(to) & 15)) {
+        *reinterpret_cast<int4*>(to + r) = make_int4(v[0], v[1], v[2], v[3]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kRowsLane; ++i)
+          if (i < n) to[r + i] = v[i];
+      }
+    };
+    put(a.positions, pos);
+    put(a.slots, slot);
+    put(a.seq_ids, id);
   }
   if (a.status && bad_page) atomicOr(a.status, kBadPage);
 }
@@ -308,7 +306,10 @@ extern "C" int dls_kv_reserve(const dls_kv_reserve_desc* d, void* cuda_stream) {
     cudaLaunchConfig_t c{};
     cudaLaunchAttribute at[1];
     const unsigned ctas = a.max_rows <= 4096 ? 1 : a.max_rows <= 16384 ? 2 : a.max_rows <= 65536 ? 4 : 8;
-    c.gridDim = dim3(ctas), c.blockDim = dim3(RSV_THREADS), c.dynamicSmemBytes = smem, c.stream = s;
+    const int wanted = std::max(a.n_seqs, a.max_rows / kRowsLane);
+    int threads = 128;
+    while (threads < kMostThreads && threads < wanted) threads *= 2;
+    c.gridDim = dim3(ctas), c.blockDim = dim3(threads), c.dynamicSmemBytes = smem, c.stream = s;
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = ctas, at[0].val.clusterDim.y = 1, at[0].val.clusterDim.z = 1;
     c.attrs = at, c.numAttrs = 1;

@@ -26,6 +26,8 @@
 #include <cuda_bf16.h>
 #include <math.h>
 
+#include <type_traits>
+
 #include "../../include/dls.h"
 #include "kernels.h"
 
@@ -73,49 +75,52 @@ __device__ __forceinline__ u64_t part_of(u64_t s, float v) {
 }
 
 // A row in pieces of V elements: piece k holds elements k V - off ..., off such
-// that pieces lie at 16-byte boundaries (V = 1: single elements).
+// that pieces lie at 16-byte boundaries (V = 1: single elements).  Whole
+// pieces are loaded as they lie; those at the ends, element by element.
 template <typename T, int V>
 struct Piece16 {
-  float x[V];
-  __device__ __forceinline__ void load(const T* row, int first, int vocab) {
-    if constexpr (V > 1) {
-      if (first >= 0 && first + V <= vocab) {
-        const uint4 w = __ldg(reinterpret_cast<const uint4*>(row + first));
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-        if constexpr (sizeof(T) == 4) {
+  typename std::conditional<(V > 1), uint4, T>::type w;
+  __device__ __forceinline__ void load(const T* row, int first) {
+    if constexpr (V > 1) w = __ldg(reinterpret_cast<const uint4*>(row + first));
+    else w = row[first];
+  }
+  __device__ __forceinline__ void get(float (&x)[V]) const {
+    if constexpr (V == 1) {
+      x[0] = as_float(w);
+    } else {
+      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+      if constexpr (sizeof(T) == 4) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) x[i] = __uint_as_float(u[i]);
-        } else {
+        for (int i = 0; i < 4; ++i) x[i] = __uint_as_float(u[i]);
+      } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const unsigned short h = (unsigned short)(i & 1 ? u[i >> 1] >> 16 : u[i >> 1]);
-            if constexpr (__is_same(T, __half)) x[i] = __half2float(__ushort_as_half(h));
-            else x[i] = __uint_as_float((uint32_t)h << 16);
-          }
+        for (int i = 0; i < 8; ++i) {
+          const unsigned short h = (unsigned short)(i & 1 ? u[i >> 1] >> 16 : u[i >> 1]);
+          if constexpr (std::is_same<T, __half>::value) x[i] = __half2float(__ushort_as_half(h));
+          else x[i] = __uint_as_float((uint32_t)h << 16);
         }
-        return;
       }
     }
-#pragma unroll
-    for (int i = 0; i < V; ++i) x[i] = first + i >= 0 && first + i < vocab ? as_float(row[first + i]) : 0.f;
   }
 };
+template <typename T, int V>
+__device__ __forceinline__ void ends(const T* row, int first, int vocab, float (&x)[V]) {
+#pragma unroll
+  for (int i = 0; i < V; ++i) x[i] = first + i >= 0 && first + i < vocab ? as_float(row[first + i]) : 0.f;
+}
 
 // Weight of an element: of p alone, of p without token x, or of what p has over q.
 enum What { ALONE, WITHOUT, OVER };
 
-template <typename T, int V>
-__device__ __forceinline__ void weigh(const T* p, const T* q, int first, int vocab, int what, int x, u64_t (&w)[V], u64_t* plain) {
-  Piece16<T, V> a, b;
-  a.load(p, first, vocab);
-  if (what == OVER) b.load(q, first, vocab);
+template <int V>
+__device__ __forceinline__ void weigh(const float (&p)[V], const float (&q)[V], int first, int what, int x, u64_t (&w)[V], u64_t& plain) {
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const u64_t fp = fixed60(a.x[i]);
-    if (plain) *plain += fp;
+    const u64_t fp = fixed60(p[i]);
+    plain += fp;
     w[i] = fp;
     if (what == OVER) {
-      const u64_t fq = fixed60(b.x[i]);
+      const u64_t fq = fixed60(q[i]);
       w[i] = fp > fq ? fp - fq : 0;
     } else if (what == WITHOUT && first + i == x) {
       w[i] = 0;
@@ -200,13 +205,51 @@ __global__ void __launch_bounds__(VTHREADS) verify_kernel(const __grid_constant_
   const int pieces = (a.vocab + off + V - 1) / V;
   const int per_warp = (pieces + (int)ctas * VWARPS - 1) / ((int)ctas * VWARPS);
   const int c0 = (int)min((long long)(rank * VWARPS + warp) * per_warp, (long long)pieces), c1 = min(c0 + per_warp, pieces);
+  const int in0 = off ? 1 : 0, in1 = (a.vocab + off) / V;  // whole pieces
   u64_t sum = 0, plain = 0;
-#pragma unroll 4
-  for (int c = c0 + lane; c < c1; c += 32) {
-    u64_t w[V];
-    weigh<T, V>(p, q, c * V - off, a.vocab, what, x, w, &plain);
+  constexpr int U = V == 8 ? 2 : 4;  // pieces in flight
+  for (int c = max(c0, in0) + lane; c < min(c1, in1); c += 32 * U) {
+    Piece16<T, V> pp[U], qq[U];
 #pragma unroll
-    for (int i = 0; i < V; ++i) sum += w[i];
+    for (int k = 0; k < U; ++k) {
+      const int at = min(c + 32 * k, in1 - 1) * V - off;
+      pp[k].load(p, at);
+      if (what == OVER) qq[k].load(q, at);
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      if (c + 32 * k >= min(c1, in1)) continue;
+      float x_p[V], x_q[V];
+      pp[k].get(x_p);
+      if (what == OVER) qq[k].get(x_q);
+      u64_t w[V];
+      weigh<V>(x_p, x_q, (c + 32 * k) * V - off, what, x, w, plain);
+#pragma unroll
+      for (int i = 0; i < V; ++i) sum += w[i];
+    }
+  }
+  auto any_piece = [&](int c, int how, u64_t (&w)[V], u64_t& all) {
+    float x_p[V], x_q[V];
+    if (c >= in0 && c < in1) {
+      Piece16<T, V> pp, qq;
+      pp.load(p, c * V - off);
+      if (how == OVER) qq.load(q, c * V - off);
+      pp.get(x_p);
+      if (how == OVER) qq.get(x_q);
+    } else {
+      ends<T, V>(p, c * V - off, a.vocab, x_p);
+      if (how == OVER) ends<T, V>(q, c * V - off, a.vocab, x_q);
+    }
+    weigh<V>(x_p, x_q, c * V - off, how, x, w, all);
+  };
+  if (lane < 2) {  // the piece before the whole ones, the one behind
+    const int c = lane ? in1 : 0;
+    if (c >= c0 && c < c1 && (lane ? in1 >= in0 : in0 > 0)) {
+      u64_t w[V];
+      any_piece(c, what, w, plain);
+#pragma unroll
+      for (int i = 0; i < V; ++i) sum += w[i];
+    }
   }
   sum = warp_sum64(sum);
   plain = warp_sum64(plain);
@@ -256,7 +299,8 @@ __global__ void __launch_bounds__(VTHREADS) verify_kernel(const __grid_constant_
   for (int c = c0; c < c1; c += 32) {
     u64_t w[V], mine = 0;
     if (c + lane < c1) {
-      weigh<T, V>(p, q, (c + lane) * V - off, a.vocab, how, x, w, nullptr);
+      u64_t none = 0;
+      any_piece(c + lane, how, w, none);
 #pragma unroll
       for (int i = 0; i < V; ++i) mine += w[i];
     }
@@ -332,7 +376,7 @@ extern "C" int dls_verify_draft(const dls_verify_draft_desc* d, void* cuda_strea
   a.wide = !d->draft || (!((reinterpret_cast<uintptr_t>(d->target) ^ reinterpret_cast<uintptr_t>(d->draft)) & 15) &&
                          !(((d->target_stride - d->draft_stride) * size) & 15));
   unsigned ctas = kMaxCluster;
-  while (ctas > 1 && ((long long)(ctas / 2) * d->n_seqs >= 304 || d->vocab < 2048 * (int)ctas)) ctas /= 2;
+  while (ctas > 1 && ((long long)ctas * d->n_seqs > 304 || d->vocab < 2048 * (int)ctas)) ctas /= 2;
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
   cudaError_t e = cudaSuccess;
   if (a.status) e = cudaMemsetAsync(a.status, 0, sizeof(int32_t), s);
