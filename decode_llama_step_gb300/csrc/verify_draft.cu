@@ -13,10 +13,13 @@
 // Which token it is must not depend on how the sums are formed: 128256
 // borders, most of them of unlikely tokens, lie so close that the rounding of
 // a 32-bit sum (or of p - q in 32 bits) moves the pick past some of them.  So
-// p and q become whole numbers of 2^-60, exact for all of a float's 24 bits
-// from 2^-36 on, and everything after is integer arithmetic: sums in any order
-// give the same bits, and v sum w is compared exactly (its floor, against
-// whole sums).  u q(x) < p(x) is exact in a double.
+// p and q become whole numbers of 2^-45 (to the nearest: 2^21 of them on the
+// random numbers' own 2^-24) and everything after is integer arithmetic: sums
+// in any order give the same bits, and v sum w is compared exactly (its floor,
+// against whole sums).  u q(x) < p(x) is exact in a double.  The conversion
+// takes two additions: p + 2 holds p's first 22 bits in its mantissa, and what
+// is left, added to 3 2^-23, the next 23 (units of 2^-60 by shifts took three times
+// the instructions, which is what bounded the call: 24 us for 64 sequences).
 //
 // What bounds it: the bytes of one row of p and one of q a sequence; the rows
 // of drafts that stand are never read but at one token.  A cluster of CTAs
@@ -35,8 +38,7 @@ namespace dls {
 
 namespace {
 
-constexpr int VTHREADS = 512;
-constexpr int VWARPS = VTHREADS / 32;
+constexpr int kMostThreadsV = 512;
 constexpr int kMaxCluster = 8;
 typedef unsigned long long u64_t;
 
@@ -54,15 +56,21 @@ __device__ __forceinline__ float as_float(float x) { return x; }
 __device__ __forceinline__ float as_float(__half x) { return __half2float(x); }
 __device__ __forceinline__ float as_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 
-// p in whole numbers of 2^-60, cut off; outside [0, 1] the nearer end, NaN 0.
-__device__ __forceinline__ u64_t fixed60(float p) {
-  const unsigned b = __float_as_uint(fminf(fmaxf(p, 0.f), 1.f)), e = b >> 23;
-  // 1.f at e = 127; below the normal range the hidden bit is wrong, and the shift takes everything away
-  const unsigned hi = ((b & 0x7fffffu) | 0x800000u) << 5;  // mantissa * 2^37, upper word: p = 1 is 2^60
-  u64_t r;
-  asm("shr.u64 %0, %1, %2;" : "=l"(r) : "l"((u64_t)hi << 32), "r"(127u - e));
-  return r;
+// Two probabilities in whole numbers of 2^-45, each as hi * 2^23 + lo; outside
+// [0, 1] the nearer end, NaN 0.
+__device__ __forceinline__ float saturated(float x) {
+  float y;
+  asm("add.sat.f32 %0, %1, 0f00000000;" : "=f"(y) : "f"(x));
+  return y;
 }
+__device__ __forceinline__ void units2(float x, float y, int (&hi)[2], int (&lo)[2]) {
+  const f2_t v = pk2(x, y), h = fadd2(v, pk2(2.f, 2.f));                // steps of 2^-22
+  const f2_t rest = fadd2(v, ffma2(h, pk2(-1.f, -1.f), pk2(2.f, 2.f)));  // exact, at most 2^-23
+  const f2_t l = fadd2(rest, pk2(0x1.8p-22f, 0x1.8p-22f));               // steps of 2^-45
+  hi[0] = __float_as_int(upk2(h).x) - 0x40000000, hi[1] = __float_as_int(upk2(h).y) - 0x40000000;
+  lo[0] = __float_as_int(upk2(l).x) - 0x34c00000, lo[1] = __float_as_int(upk2(l).y) - 0x34c00000;
+}
+__device__ __forceinline__ u64_t joined(int hi, int lo) { return (u64_t)((long long)hi * (1 << 23) + lo); }
 
 // floor(v s) below s, v in [0, 1)
 __device__ __forceinline__ u64_t part_of(u64_t s, float v) {
@@ -112,19 +120,31 @@ __device__ __forceinline__ void ends(const T* row, int first, int vocab, float (
 // Weight of an element: of p alone, of p without token x, or of what p has over q.
 enum What { ALONE, WITHOUT, OVER };
 
+// Weights of V elements, hi and lo apart, and the sums of them and of p alone.
+struct Sums {
+  int hi, lo, p_hi, p_lo;
+};
 template <int V>
-__device__ __forceinline__ void weigh(const float (&p)[V], const float (&q)[V], int first, int what, int x, u64_t (&w)[V], u64_t& plain) {
+__device__ __forceinline__ void weigh(const float (&p)[V], const float (&q)[V], int first, int what, int x, int (&hi)[V], int (&lo)[V], Sums& s) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const u64_t fp = fixed60(p[i]);
-    plain += fp;
-    w[i] = fp;
+  for (int i = 0; i < V; i += 2) {
+    const float p0 = saturated(p[i]), p1 = V > 1 ? saturated(p[i + (V > 1)]) : 0.f;
+    int h[2], l[2];
+    units2(p0, p1, h, l);
+    s.p_hi += h[0] + h[1], s.p_lo += l[0] + l[1];
     if (what == OVER) {
-      const u64_t fq = fixed60(q[i]);
-      w[i] = fp > fq ? fp - fq : 0;
-    } else if (what == WITHOUT && first + i == x) {
-      w[i] = 0;
+      const float q0 = saturated(q[i]), q1 = V > 1 ? saturated(q[i + (V > 1)]) : 0.f;
+      int g[2], k[2];
+      units2(q0, q1, g, k);
+      h[0] = p0 > q0 ? h[0] - g[0] : 0, l[0] = p0 > q0 ? l[0] - k[0] : 0;
+      h[1] = p1 > q1 ? h[1] - g[1] : 0, l[1] = p1 > q1 ? l[1] - k[1] : 0;
+    } else if (what == WITHOUT) {
+      if (first + i == x) h[0] = l[0] = 0;
+      if (first + i + 1 == x) h[1] = l[1] = 0;
     }
+    s.hi += h[0] + h[1], s.lo += l[0] + l[1];
+    hi[i] = h[0], lo[i] = l[0];
+    if (V > 1) hi[i + (V > 1)] = h[1], lo[i + (V > 1)] = l[1];
   }
 }
 
@@ -135,12 +155,12 @@ __device__ __forceinline__ u64_t warp_sum64(u64_t v) {
 }
 
 template <typename T, int V>
-__global__ void __launch_bounds__(VTHREADS) verify_kernel(const __grid_constant__ VerifyArgs a) {
-  __shared__ u64_t warp_sums[VWARPS][2];
+__global__ void __launch_bounds__(kMostThreadsV, 2) verify_kernel(const __grid_constant__ VerifyArgs a) {
+  __shared__ u64_t warp_sums[kMostThreadsV / 32][2];
   __shared__ __align__(16) u64_t cta_sum[2];
   __shared__ u64_t all[kMaxCluster][2];
   __shared__ int s_stop;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cta_warps = blockDim.x >> 5;
   unsigned rank, ctas;
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
   asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ctas));
@@ -188,7 +208,7 @@ __global__ void __launch_bounds__(VTHREADS) verify_kernel(const __grid_constant_
   const int stop = s_stop;
   const bool refused = stop < end - 1;
   if (rank == 0) {
-    for (int r = start + tid; r < end; r += VTHREADS)
+    for (int r = start + tid; r < end; r += blockDim.x)
       if (r != stop) a.out_tokens[r] = r < stop ? a.tokens[r + 1] : -1;
     if (tid == 0) {
       a.n_accepted[b] = stop - start;
@@ -203,8 +223,8 @@ __global__ void __launch_bounds__(VTHREADS) verify_kernel(const __grid_constant_
   const int x = refused ? a.tokens[stop + 1] : -1;
   const int off = V > 1 ? (int)((reinterpret_cast<uintptr_t>(p) & 15) / sizeof(T)) : 0;
   const int pieces = (a.vocab + off + V - 1) / V;
-  const int per_warp = (pieces + (int)ctas * VWARPS - 1) / ((int)ctas * VWARPS);
-  const int c0 = (int)min((long long)(rank * VWARPS + warp) * per_warp, (long long)pieces), c1 = min(c0 + per_warp, pieces);
+  const int per_warp = (pieces + (int)ctas * cta_warps - 1) / ((int)ctas * cta_warps);
+  const int c0 = (int)min((long long)(rank * cta_warps + warp) * per_warp, (long long)pieces), c1 = min(c0 + per_warp, pieces);
   const int in0 = off ? 1 : 0, in1 = (a.vocab + off) / V;  // whole pieces
   u64_t sum = 0, plain = 0;
   constexpr int U = V == 8 ? 2 : 4;  // pieces in flight
@@ -216,19 +236,20 @@ __global__ void __launch_bounds__(VTHREADS) verify_kernel(const __grid_constant_
       pp[k].load(p, at);
       if (what == OVER) qq[k].load(q, at);
     }
+    Sums s{};
 #pragma unroll
     for (int k = 0; k < U; ++k) {
       if (c + 32 * k >= min(c1, in1)) continue;
       float x_p[V], x_q[V];
       pp[k].get(x_p);
       if (what == OVER) qq[k].get(x_q);
-      u64_t w[V];
-      weigh<V>(x_p, x_q, (c + 32 * k) * V - off, what, x, w, plain);
-#pragma unroll
-      for (int i = 0; i < V; ++i) sum += w[i];
+      int hi[V], lo[V];
+      weigh<V>(x_p, x_q, (c + 32 * k) * V - off, what, x, hi, lo, s);
     }
+    sum += joined(s.hi, s.lo);  // (16 elements of at most 2^22 so far)
+    plain += joined(s.p_hi, s.p_lo);
   }
-  auto any_piece = [&](int c, int how, u64_t (&w)[V], u64_t& all) {
+  auto any_piece = [&](int c, int how, int (&hi)[V], int (&lo)[V], Sums& s) {
     float x_p[V], x_q[V];
     if (c >= in0 && c < in1) {
       Piece16<T, V> pp, qq;
@@ -240,15 +261,16 @@ __global__ void __launch_bounds__(VTHREADS) verify_kernel(const __grid_constant_
       ends<T, V>(p, c * V - off, a.vocab, x_p);
       if (how == OVER) ends<T, V>(q, c * V - off, a.vocab, x_q);
     }
-    weigh<V>(x_p, x_q, c * V - off, how, x, w, all);
+    weigh<V>(x_p, x_q, c * V - off, how, x, hi, lo, s);
   };
   if (lane < 2) {  // the piece before the whole ones, the one behind
     const int c = lane ? in1 : 0;
     if (c >= c0 && c < c1 && (lane ? in1 >= in0 : in0 > 0)) {
-      u64_t w[V];
-      any_piece(c, what, w, plain);
-#pragma unroll
-      for (int i = 0; i < V; ++i) sum += w[i];
+      int hi[V], lo[V];
+      Sums s{};
+      any_piece(c, what, hi, lo, s);
+      sum += joined(s.hi, s.lo);
+      plain += joined(s.p_hi, s.p_lo);
     }
   }
   sum = warp_sum64(sum);
@@ -256,7 +278,7 @@ __global__ void __launch_bounds__(VTHREADS) verify_kernel(const __grid_constant_
   if (lane == 0) warp_sums[warp][0] = sum, warp_sums[warp][1] = plain;
   __syncthreads();
   if (warp == 0) {
-    u64_t s = lane < VWARPS ? warp_sums[lane][0] : 0, t = lane < VWARPS ? warp_sums[lane][1] : 0;
+    u64_t s = lane < cta_warps ? warp_sums[lane][0] : 0, t = lane < cta_warps ? warp_sums[lane][1] : 0;
     s = warp_sum64(s);
     t = warp_sum64(t);
     if (lane == 0) cta_sum[0] = s, cta_sum[1] = t;
@@ -297,12 +319,12 @@ __global__ void __launch_bounds__(VTHREADS) verify_kernel(const __grid_constant_
   for (int w = 0; w < warp; ++w) before += warp_sums[w][col];
   if (!(before <= border && before + warp_sums[warp][col] > border)) return;
   for (int c = c0; c < c1; c += 32) {
-    u64_t w[V], mine = 0;
+    u64_t mine = 0;
+    int hi[V], lo[V];
     if (c + lane < c1) {
-      u64_t none = 0;
-      any_piece(c + lane, how, w, none);
-#pragma unroll
-      for (int i = 0; i < V; ++i) mine += w[i];
+      Sums s{};
+      any_piece(c + lane, how, hi, lo, s);
+      mine = joined(s.hi, s.lo);
     }
     u64_t pre = mine;
 #pragma unroll
@@ -317,7 +339,7 @@ __global__ void __launch_bounds__(VTHREADS) verify_kernel(const __grid_constant_
         int t = (c + lane) * V - off;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          at += w[i];
+          at += joined(hi[i], lo[i]);
           if (at <= border) ++t;
         }
         a.out_tokens[stop] = t;
@@ -332,7 +354,8 @@ template <typename T>
 cudaError_t launch_verify(const VerifyArgs& a, unsigned ctas, cudaStream_t s) {
   cudaLaunchConfig_t c{};
   cudaLaunchAttribute at[1];
-  c.gridDim = dim3(ctas * (unsigned)a.n_seqs), c.blockDim = dim3(VTHREADS), c.stream = s;
+  // (many sequences: smaller blocks, four an SM, go round it evenly)
+  c.gridDim = dim3(ctas * (unsigned)a.n_seqs), c.blockDim = dim3(ctas * (unsigned)a.n_seqs <= 152 ? kMostThreadsV : kMostThreadsV / 2), c.stream = s;
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = ctas, at[0].val.clusterDim.y = 1, at[0].val.clusterDim.z = 1;
   c.attrs = at, c.numAttrs = 1;
@@ -348,8 +371,8 @@ extern "C" int dls_verify_draft(const dls_verify_draft_desc* d, void* cuda_strea
   if (!d) return report_error(DLS_ERR_ARG, "verify_draft: desc=NULL");
   const int size = d->prob_type == DLS_F32 ? 4 : d->prob_type == DLS_F16 || d->prob_type == DLS_BF16 ? 2 : 0;
   if (!size) return report_error(DLS_ERR_ARG, "verify_draft: prob_type=%d", d->prob_type);
-  if (d->n_tokens < 0 || d->n_seqs < 0 || d->n_seqs > 1 << 24 || d->vocab < 1 || d->vocab > 1 << 30)
-    return report_error(DLS_ERR_ARG, "verify_draft: n_tokens=%d n_seqs=%d (at most 2^24) vocab=%d (1 to 2^30)", d->n_tokens, d->n_seqs, d->vocab);
+  if (d->n_tokens < 0 || d->n_seqs < 0 || d->n_seqs > 1 << 24 || d->vocab < 1 || d->vocab > 1 << 18)
+    return report_error(DLS_ERR_ARG, "verify_draft: n_tokens=%d n_seqs=%d (at most 2^24) vocab=%d (1 to 2^18)", d->n_tokens, d->n_seqs, d->vocab);
   if (d->target_stride < d->vocab || d->target_stride > 1ll << 32 || (d->draft && (d->draft_stride < d->vocab || d->draft_stride > 1ll << 32)))
     return report_error(DLS_ERR_ARG, "verify_draft: target_stride=%lld draft_stride=%lld (vocab=%d to 2^32)", (long long)d->target_stride,
                         (long long)d->draft_stride, d->vocab);
@@ -376,7 +399,7 @@ extern "C" int dls_verify_draft(const dls_verify_draft_desc* d, void* cuda_strea
   a.wide = !d->draft || (!((reinterpret_cast<uintptr_t>(d->target) ^ reinterpret_cast<uintptr_t>(d->draft)) & 15) &&
                          !(((d->target_stride - d->draft_stride) * size) & 15));
   unsigned ctas = kMaxCluster;
-  while (ctas > 1 && ((long long)ctas * d->n_seqs > 304 || d->vocab < 2048 * (int)ctas)) ctas /= 2;
+  while (ctas > 1 && ((long long)ctas * d->n_seqs > 608 || d->vocab < 2048 * (int)ctas)) ctas /= 2;
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
   cudaError_t e = cudaSuccess;
   if (a.status) e = cudaMemsetAsync(a.status, 0, sizeof(int32_t), s);

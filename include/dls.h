@@ -721,14 +721,15 @@ int dls_attention_chunk8(const dls_attention_chunk8_desc* d, void* cuda_stream);
  * all drafts stand, else from max(target - draft, 0) of the row of the first
  * that does not: the least t whose running sum exceeds pick[b] times the whole.
  * draft = NULL: the drafts were certain (greedy): x stands while accept < target[x], and
- * the residual is the target's without x.  Sums are exact in units of 2^-60, so
- * the token does not depend on how they are formed.  A residual without weight
+ * the residual is the target's without x.  For this each probability counts in
+ * whole numbers of 2^-45, to the nearest, and sums and their comparison with
+ * pick are exact, so the token does not depend on how they are formed.  A residual without weight
  * gives way to the target's row; a row without any gives -1 and status bit 2.
  *  out_tokens: the standing drafts from row cu_q[b] on, the token taken, -1 in
  *   the sequence's other rows; rows of no sequence are left as they are.
  *  n_accepted[b]: drafts that stand (0 for a sequence without rows).
  *  kv_len_out[b] = kv_len[b] less the drafts that do not (may be kv_len).
- * Probabilities count as 0..1 (NaN as 0), a row's sum should be at most 8;
+ * Probabilities count as 0..1 (NaN as 0), whatever their sum;
  * random numbers as 0 <= x < 1 (NaN as 0).  A drafted token outside
  * [0, vocab) does not stand and sets status bit 2; bit 4 marks a cu_q that does
  * not fit, whose sequence has n_accepted 0 and no out_tokens. */
@@ -747,7 +748,7 @@ typedef struct dls_verify_draft_desc {
   int64_t target_stride, draft_stride; /* elements from one row to the next */
   int32_t n_tokens;         /* rows, padding included */
   int32_t n_seqs;           /* 0..2^24 */
-  int32_t vocab;            /* 1..2^30 */
+  int32_t vocab;            /* 1..2^18 */
   int32_t prob_type;        /* dls_dtype */
 } dls_verify_draft_desc;
 int dls_verify_draft(const dls_verify_draft_desc* d, void* cuda_stream);

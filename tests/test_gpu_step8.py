@@ -964,13 +964,10 @@ def test_pools_of_more_than_two_to_the_31_codes(gpu_lib):
 
 # ---- drafted tokens ----------------------------------------------------------------------------------
 
-def fixed60(p):
-    """Probabilities (any float array) as whole numbers of 2^-60, cut off."""
+def units(p):
+    """Probabilities (any float array) in whole numbers of 2^-45, to the nearest: p 2^45 is exact in 64 bits, and below 2^53."""
     p = np.nan_to_num(np.asarray(p, dtype=np.float64), nan=0.0).clip(0.0, 1.0)
-    m, e = np.frexp(p)
-    n = (m * 2.0 ** 53).astype(np.int64)            # p = n 2^(e - 53), exactly
-    s = 60 + e - 53
-    return np.where(s >= 0, n << np.clip(s, 0, 62), n >> np.clip(-s, 0, 62))
+    return np.rint(p * 2.0 ** 45).astype(np.int64)
 
 
 def verify_plain(tokens, target, draft, cu, accept, pick, vocab):
@@ -991,11 +988,11 @@ def verify_plain(tokens, target, draft, cu, accept, pick, vocab):
             if not ok:
                 stop = r
                 break
-        p = fixed60(target[stop]).astype(object) if vocab < 50 else fixed60(target[stop])
+        p = units(target[stop])
         w = p
         if stop < e - 1:
             if draft is not None:
-                w = np.maximum(p - (fixed60(draft[stop]).astype(object) if vocab < 50 else fixed60(draft[stop])), 0)
+                w = np.maximum(p - units(draft[stop]), 0)
             else:
                 w = p.copy()
                 if 0 <= tokens[stop + 1] < vocab:

@@ -92,7 +92,7 @@ def test_attention_chunk8_refuses(lib, over, word):
 
 @pytest.mark.parametrize("over,word", [
     (dict(prob_type=4), "prob_type=4"), (dict(n_tokens=-1), "n_tokens=-1"), (dict(n_seqs=-1), "n_seqs=-1"),
-    (dict(n_seqs=(1 << 24) + 1), "n_seqs"), (dict(vocab=0), "vocab=0"), (dict(target_stride=1023), "target_stride=1023"),
+    (dict(n_seqs=(1 << 24) + 1), "n_seqs"), (dict(vocab=0), "vocab=0"), (dict(vocab=(1 << 18) + 1, target_stride=1 << 20, draft_stride=1 << 20), "vocab"), (dict(target_stride=1023), "target_stride=1023"),
     (dict(draft_stride=1000), "draft_stride=1000"), (dict(target_stride=(1 << 32) + 1), "target_stride"), (dict(cu_q=0), "cu_q"),
     (dict(n_accepted=0), "n_accepted"), (dict(kv_len=0), "both lengths"), (dict(kv_len_out=0), "both lengths"),
     (dict(tokens=0), "tokens"), (dict(target=0), "target"), (dict(accept=0), "accept"), (dict(pick=0), "pick"),
