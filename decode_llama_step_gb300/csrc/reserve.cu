@@ -17,7 +17,7 @@
 // itself, the cluster meets once (the state may be written only after all have
 // read it, the stack read only after the pages that come back are on it), then
 // each takes its share of the rows.
-#include <math.h>
+#include <type_traits>
 
 #include "../../include/dls.h"
 #include "kernels.h"
@@ -28,7 +28,6 @@ namespace {
 
 constexpr int kMostThreads = 1024;
 constexpr int kPerThread = DLS_MAX_CHUNK_SEQS / kMostThreads;  // sequences of a thread at most
-constexpr int kRowsLane = 4;                                   // rows of a lane at a time
 // Sums stop here, above every bound that they are held to (2^27 pages, 2^30 rows): sums cut off so stay a prefix sum,
 // and those that matter are exact.
 constexpr unsigned kCap = (1u << 30) + 1;
@@ -185,7 +184,9 @@ __global__ void __launch_bounds__(kMostThreads, 1) reserve_kernel(const __grid_c
       for (int j = lane; j < n; j += 32) a.free_pages[r.pop + j] = a.page_table[(size_t)s * a.max_pages + j];
     }
   }
-  cluster_meet();  // (the state is read, the stack is whole)
+  // (the state is read, the stack is whole; a cluster of one takes 2000 cycles for its barrier, a block 30)
+  if (ctas > 1) cluster_meet();
+  else __syncthreads();
 
   if (rank == 0) {
 #pragma unroll
@@ -204,11 +205,9 @@ __global__ void __launch_bounds__(kMostThreads, 1) reserve_kernel(const __grid_c
     }
   }
 
-  // Rows: a warp takes a run of them, a lane four neighbours at a time, which as a rule are of one sequence and
-  // one page.  (16-byte stores where the arrays allow.)
-  constexpr int kTurn = 32 * kRowsLane;
-  const int share = ((all + warps - 1) / warps + kRowsLane - 1) / kRowsLane * kRowsLane;
-  const int r0 = (int)min((long long)share * warp, (long long)all), r1 = min(r0 + share, all);
+  // Rows: a warp takes a run of them, a lane one at a time or, where there are
+  // many, four neighbours, which then as a rule are of one sequence and one page.
+  // (16-byte stores where the arrays allow.)
   bool bad_page = false;
   auto seq_from = [&](int lo, int row) {  // the sequence from lo on that holds the row: the last that begins there or before
     if (cu[lo + 1] > row) return lo;
@@ -226,6 +225,10 @@ __global__ void __launch_bounds__(kMostThreads, 1) reserve_kernel(const __grid_c
     if (first) a.page_table[(size_t)s * a.max_pages + j] = p;
     return p;
   };
+  auto run = [&](auto lane_rows) {
+  constexpr int kRowsLane = decltype(lane_rows)::value, kTurn = 32 * kRowsLane;
+  const int share = ((all + warps - 1) / warps + kRowsLane - 1) / kRowsLane * kRowsLane;
+  const int r0 = (int)min((long long)share * warp, (long long)all), r1 = min(r0 + share, all);
   int s = 0;
   for (int r = r0 + lane * kRowsLane; r < r1; r += kTurn) {
     int pos[kRowsLane], slot[kRowsLane], id[kRowsLane];
@@ -248,8 +251,8 @@ __global__ void __launch_bounds__(kMostThreads, 1) reserve_kernel(const __grid_c
     }
     auto put = [&](int32_t* to, const int (&v)[kRowsLane]) {
       if (!to) return;
-      if (n == kRowsLane && !(reinterpret_cast<uintptr_t>(to) & 15)) {
-        *reinterpret_cast<int4*>(to + r) = make_int4(v[0], v[1], v[2], v[3]);
+      if (kRowsLane == 4 && n == 4 && !(reinterpret_cast<uintptr_t>(to) & 15)) {
+        *reinterpret_cast<int4*>(to + r) = make_int4(v[0], v[kRowsLane > 1], v[kRowsLane / 2], v[kRowsLane - 1]);
       } else {
 #pragma unroll
         for (int i = 0; i < kRowsLane; ++i)
@@ -260,6 +263,9 @@ __global__ void __launch_bounds__(kMostThreads, 1) reserve_kernel(const __grid_c
     put(a.slots, slot);
     put(a.seq_ids, id);
   }
+  };
+  if (all > warps * 32) run(std::integral_constant<int, 4>());
+  else run(std::integral_constant<int, 1>());
   if (a.status && bad_page) atomicOr(a.status, kBadPage);
 }
 
@@ -299,14 +305,16 @@ extern "C" int dls_kv_reserve(const dls_kv_reserve_desc* d, void* cuda_stream) {
   cudaError_t e = cudaSuccess;
   if (a.status) e = cudaMemsetAsync(a.status, 0, sizeof(int32_t), s);
   const int smem = (a.n_seqs + 1) * 4 + a.n_seqs * (int)sizeof(SeqRow);
+  if (e == cudaSuccess && a.max_rows > 131072)  // a cluster of 16
+    e = cudaFuncSetAttribute(reserve_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e == cudaSuccess && smem > 40 * 1024)  // beyond what a launch may ask for unannounced (48 KB, the static part with it)
     e = cudaFuncSetAttribute(reserve_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (DLS_MAX_CHUNK_SEQS + 1) * 4 + DLS_MAX_CHUNK_SEQS * (int)sizeof(SeqRow));
   if (e == cudaSuccess) {
     cudaLaunchConfig_t c{};
     cudaLaunchAttribute at[1];
-    const unsigned ctas = a.max_rows <= 4096 ? 1 : a.max_rows <= 16384 ? 2 : a.max_rows <= 65536 ? 4 : 8;
-    const int wanted = std::max(a.n_seqs, a.max_rows / kRowsLane);
+    const unsigned ctas = a.max_rows <= 4096 ? 1 : a.max_rows <= 16384 ? 2 : a.max_rows <= 65536 ? 4 : a.max_rows <= 131072 ? 8 : 16;
+    const int wanted = std::max(a.n_seqs, a.max_rows / 4);
     int threads = 128;
     while (threads < kMostThreads && threads < wanted) threads *= 2;
     c.gridDim = dim3(ctas), c.blockDim = dim3(threads), c.dynamicSmemBytes = smem, c.stream = s;

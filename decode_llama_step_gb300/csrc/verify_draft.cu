@@ -63,12 +63,14 @@ __device__ __forceinline__ float saturated(float x) {
   asm("add.sat.f32 %0, %1, 0f00000000;" : "=f"(y) : "f"(x));
   return y;
 }
+// (as the bits of the sums: kHi and kLo more than the numbers)
+constexpr int kHi = 0x40000000, kLo = 0x34c00000;
 __device__ __forceinline__ void units2(float x, float y, int (&hi)[2], int (&lo)[2]) {
   const f2_t v = pk2(x, y), h = fadd2(v, pk2(2.f, 2.f));                // steps of 2^-22
   const f2_t rest = fadd2(v, ffma2(h, pk2(-1.f, -1.f), pk2(2.f, 2.f)));  // exact, at most 2^-23
   const f2_t l = fadd2(rest, pk2(0x1.8p-22f, 0x1.8p-22f));               // steps of 2^-45
-  hi[0] = __float_as_int(upk2(h).x) - 0x40000000, hi[1] = __float_as_int(upk2(h).y) - 0x40000000;
-  lo[0] = __float_as_int(upk2(l).x) - 0x34c00000, lo[1] = __float_as_int(upk2(l).y) - 0x34c00000;
+  hi[0] = __float_as_int(upk2(h).x), hi[1] = __float_as_int(upk2(h).y);
+  lo[0] = __float_as_int(upk2(l).x), lo[1] = __float_as_int(upk2(l).y);
 }
 __device__ __forceinline__ u64_t joined(int hi, int lo) { return (u64_t)((long long)hi * (1 << 23) + lo); }
 
@@ -120,31 +122,36 @@ __device__ __forceinline__ void ends(const T* row, int first, int vocab, float (
 // Weight of an element: of p alone, of p without token x, or of what p has over q.
 enum What { ALONE, WITHOUT, OVER };
 
-// Weights of V elements, hi and lo apart, and the sums of them and of p alone.
+// Sums of weights and of p alone, hi and lo apart, of few elements (hi is at
+// most 2^22, lo up to that either way; unsigned: what wraps on the way is gone
+// at the end).
 struct Sums {
-  int hi, lo, p_hi, p_lo;
+  unsigned hi, lo, p_hi, p_lo;
 };
-template <int V>
-__device__ __forceinline__ void weigh(const float (&p)[V], const float (&q)[V], int first, int what, int x, int (&hi)[V], int (&lo)[V], Sums& s) {
+// Adds V elements; `each` is told the weight of every one.
+template <int V, typename Each>
+__device__ __forceinline__ void weigh(const float (&p)[V], const float (&q)[V], int first, int what, int x, Sums& s, Each&& each) {
 #pragma unroll
   for (int i = 0; i < V; i += 2) {
     const float p0 = saturated(p[i]), p1 = V > 1 ? saturated(p[i + (V > 1)]) : 0.f;
     int h[2], l[2];
     units2(p0, p1, h, l);
-    s.p_hi += h[0] + h[1], s.p_lo += l[0] + l[1];
+    constexpr unsigned n = V > 1 ? 2 : 1;
+    s.p_hi += (unsigned)h[0] + (V > 1 ? (unsigned)h[1] : 0u) - n * kHi, s.p_lo += (unsigned)l[0] + (V > 1 ? (unsigned)l[1] : 0u) - n * kLo;
+    int g[2] = {kHi, kHi}, k[2] = {kLo, kLo};
+    bool in[2] = {true, V > 1};
     if (what == OVER) {
       const float q0 = saturated(q[i]), q1 = V > 1 ? saturated(q[i + (V > 1)]) : 0.f;
-      int g[2], k[2];
       units2(q0, q1, g, k);
-      h[0] = p0 > q0 ? h[0] - g[0] : 0, l[0] = p0 > q0 ? l[0] - k[0] : 0;
-      h[1] = p1 > q1 ? h[1] - g[1] : 0, l[1] = p1 > q1 ? l[1] - k[1] : 0;
+      in[0] = p0 > q0, in[1] = V > 1 && p1 > q1;
     } else if (what == WITHOUT) {
-      if (first + i == x) h[0] = l[0] = 0;
-      if (first + i + 1 == x) h[1] = l[1] = 0;
+      in[0] = first + i != x, in[1] = V > 1 && first + i + 1 != x;
     }
-    s.hi += h[0] + h[1], s.lo += l[0] + l[1];
-    hi[i] = h[0], lo[i] = l[0];
-    if (V > 1) hi[i + (V > 1)] = h[1], lo[i + (V > 1)] = l[1];
+#pragma unroll
+    for (int e = 0; e < (int)n; ++e) {
+      if (in[e]) s.hi += (unsigned)(h[e] - g[e]), s.lo += (unsigned)(l[e] - k[e]);
+      each(i + e, in[e] ? joined(h[e] - g[e], l[e] - k[e]) : 0);
+    }
   }
 }
 
@@ -157,8 +164,7 @@ __device__ __forceinline__ u64_t warp_sum64(u64_t v) {
 template <typename T, int V>
 __global__ void __launch_bounds__(kMostThreadsV, 2) verify_kernel(const __grid_constant__ VerifyArgs a) {
   __shared__ u64_t warp_sums[kMostThreadsV / 32][2];
-  __shared__ __align__(16) u64_t cta_sum[2];
-  __shared__ u64_t all[kMaxCluster][2];
+  __shared__ __align__(16) u64_t all[kMaxCluster][2];  // each CTA's sums
   __shared__ int s_stop;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cta_warps = blockDim.x >> 5;
   unsigned rank, ctas;
@@ -175,6 +181,7 @@ __global__ void __launch_bounds__(kMostThreadsV, 2) verify_kernel(const __grid_c
     }
     return;
   }
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   const T *target = static_cast<const T*>(a.target), *draft = static_cast<const T*>(a.draft);
 
   // the first row whose draft does not stand, or the last row
@@ -243,13 +250,12 @@ __global__ void __launch_bounds__(kMostThreadsV, 2) verify_kernel(const __grid_c
       float x_p[V], x_q[V];
       pp[k].get(x_p);
       if (what == OVER) qq[k].get(x_q);
-      int hi[V], lo[V];
-      weigh<V>(x_p, x_q, (c + 32 * k) * V - off, what, x, hi, lo, s);
+      weigh<V>(x_p, x_q, (c + 32 * k) * V - off, what, x, s, [](int, u64_t) {});
     }
-    sum += joined(s.hi, s.lo);  // (16 elements of at most 2^22 so far)
-    plain += joined(s.p_hi, s.p_lo);
+    sum += joined((int)s.hi, (int)s.lo);  // (16 elements)
+    plain += joined((int)s.p_hi, (int)s.p_lo);
   }
-  auto any_piece = [&](int c, int how, int (&hi)[V], int (&lo)[V], Sums& s) {
+  auto any_piece = [&](int c, int how, Sums& s, auto&& each) {
     float x_p[V], x_q[V];
     if (c >= in0 && c < in1) {
       Piece16<T, V> pp, qq;
@@ -261,16 +267,15 @@ __global__ void __launch_bounds__(kMostThreadsV, 2) verify_kernel(const __grid_c
       ends<T, V>(p, c * V - off, a.vocab, x_p);
       if (how == OVER) ends<T, V>(q, c * V - off, a.vocab, x_q);
     }
-    weigh<V>(x_p, x_q, c * V - off, how, x, hi, lo, s);
+    weigh<V>(x_p, x_q, c * V - off, how, x, s, each);
   };
   if (lane < 2) {  // the piece before the whole ones, the one behind
     const int c = lane ? in1 : 0;
     if (c >= c0 && c < c1 && (lane ? in1 >= in0 : in0 > 0)) {
-      int hi[V], lo[V];
       Sums s{};
-      any_piece(c, what, hi, lo, s);
-      sum += joined(s.hi, s.lo);
-      plain += joined(s.p_hi, s.p_lo);
+      any_piece(c, what, s, [](int, u64_t) {});
+      sum += joined((int)s.hi, (int)s.lo);
+      plain += joined((int)s.p_hi, (int)s.p_lo);
     }
   }
   sum = warp_sum64(sum);
@@ -278,20 +283,20 @@ __global__ void __launch_bounds__(kMostThreadsV, 2) verify_kernel(const __grid_c
   if (lane == 0) warp_sums[warp][0] = sum, warp_sums[warp][1] = plain;
   __syncthreads();
   if (warp == 0) {
-    u64_t s = lane < cta_warps ? warp_sums[lane][0] : 0, t = lane < cta_warps ? warp_sums[lane][1] : 0;
+    u64_t s = lane < cta_warps ? warp_sums[lane][0] : 0, u = lane < cta_warps ? warp_sums[lane][1] : 0;
     s = warp_sum64(s);
-    t = warp_sum64(t);
-    if (lane == 0) cta_sum[0] = s, cta_sum[1] = t;
+    u = warp_sum64(u);
+    // to every CTA of the cluster (all have begun: they arrived)
+    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+    if (lane < (int)ctas) {
+      uint32_t at;
+      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(&all[rank][0])), "r"(lane));
+      asm volatile("st.shared::cluster.v2.u64 [%0], {%1, %2};" ::"r"(at), "l"(s), "l"(u) : "memory");
+    }
+  } else {
+    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
   }
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-  if (tid < (int)ctas * 2) {
-    uint32_t at;
-    u64_t v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(&cta_sum[tid & 1])), "r"(tid >> 1));
-    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(at) : "memory");
-    all[tid >> 1][tid & 1] = v;
-  }
-  // (the sums of this CTA may be read until everyone has arrived here)
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
   u64_t total = 0, before = 0;
   int col = 0;
@@ -319,12 +324,11 @@ __global__ void __launch_bounds__(kMostThreadsV, 2) verify_kernel(const __grid_c
   for (int w = 0; w < warp; ++w) before += warp_sums[w][col];
   if (!(before <= border && before + warp_sums[warp][col] > border)) return;
   for (int c = c0; c < c1; c += 32) {
-    u64_t mine = 0;
-    int hi[V], lo[V];
+    u64_t mine = 0, w[V];
     if (c + lane < c1) {
       Sums s{};
-      any_piece(c + lane, how, hi, lo, s);
-      mine = joined(s.hi, s.lo);
+      any_piece(c + lane, how, s, [&](int i, u64_t x) { w[i] = x; });
+      mine = joined((int)s.hi, (int)s.lo);
     }
     u64_t pre = mine;
 #pragma unroll
@@ -339,7 +343,7 @@ __global__ void __launch_bounds__(kMostThreadsV, 2) verify_kernel(const __grid_c
         int t = (c + lane) * V - off;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          at += joined(hi[i], lo[i]);
+          at += w[i];
           if (at <= border) ++t;
         }
         a.out_tokens[stop] = t;
