@@ -86,9 +86,9 @@ namespace {
 constexpr int BK = 128;          // keys per tile
 constexpr int MAXC = 152;        // CTAs at most (one per SM)
 // Threads of a CTA: copies, products and the list (4 warps), softmax (8) and,
-// over codes, what makes them operands (4).
+// over codes, what makes them operands (8).
 template <int CODE>
-constexpr int kThreads = CODE ? 512 : 384;
+constexpr int kThreads = CODE ? 640 : 384;
 constexpr int kMostWarps = kThreads<DLS_E4M3> / 32;
 constexpr int QDEPTH = 4;        // pieces the list runs ahead
 // Units of a range at least: a key tile per slot of a split tile.  One token
@@ -134,13 +134,12 @@ struct CCfg {
   static constexpr bool kTogether = HDP == 64;
   static constexpr int kUses = kTogether ? 1 : 2;  // ring uses of a key tile
   static constexpr int kStage = kTogether ? 2 * kKV : kKV;
-  // Codes arrive in a ring of their own, half the size a use.  What is in
-  // flight from memory is what that ring holds, so it takes what operands can
-  // spare: two of their stages (one for K, one for V) are enough for the
-  // products of wide heads, which take as long as converting the next.
-  static constexpr int NST = !CODE ? 4 : kTogether ? 3 : 2;
+  // Codes arrive in a ring of their own, half the size a use.  Three stages of
+  // operands: with two (and five of wide heads' codes) the next K waits for the
+  // last product with this one, 609 us against 521 (2048 tokens over 16384, 32 heads of 128).
+  static constexpr int NST = !CODE ? 4 : 3;
   static constexpr int kRaw = CODE ? kStage / 2 : 0;
-  static constexpr int NRAW = 5;
+  static constexpr int NRAW = kTogether ? 5 : 3;
   static constexpr int kKVOff = 2 * kQ;
   static constexpr int kXOff = kKVOff + NST * kStage;  // 8 KB a slot: its output rows on their way out, or statistics being joined
   static constexpr int kRawOff = kXOff + 2 * 8192;
@@ -884,7 +883,7 @@ __global__ void __launch_bounds__(kThreads<CODE>, 1) chunk_kernel(const __grid_c
   // set up by warps 1 and 2 while the others begin on the plan
   if (tid == 64) {
     for (int i = 0; i < NST; ++i) {
-      mbar_init(smem_u32(&sh.full[i]), CODE ? 4 : 1);  // the copy, or the converting warps
+      mbar_init(smem_u32(&sh.full[i]), CODE ? 8 : 1);  // the copy, or the converting warps
       mbar_init(smem_u32(&sh.empty[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -899,14 +898,14 @@ __global__ void __launch_bounds__(kThreads<CODE>, 1) chunk_kernel(const __grid_c
     mbar_init(smem_u32(&sh.x_full), 4);
     for (int i = 0; i < QDEPTH; ++i) {
       mbar_init(smem_u32(&sh.pq_full[i]), 1);
-      mbar_init(smem_u32(&sh.pq_empty[i]), CODE ? 14 : 10);
+      mbar_init(smem_u32(&sh.pq_empty[i]), CODE ? 18 : 10);
     }
     if constexpr (CODE != 0) {
       for (int i = 0; i < C::NRAW; ++i) {
         mbar_init(smem_u32(&sh.raw_full[i]), 33);  // the copy's bytes, and each lane's scales
-        mbar_init(smem_u32(&sh.raw_empty[i]), 4);
+        mbar_init(smem_u32(&sh.raw_empty[i]), 8);
       }
-      mbar_init(smem_u32(&sh.q_ready), 4);
+      mbar_init(smem_u32(&sh.q_ready), 8);
     }
     sh.abort = 0;
     mbar_fence_init();
@@ -933,7 +932,7 @@ __global__ void __launch_bounds__(kThreads<CODE>, 1) chunk_kernel(const __grid_c
 
   if (warp < 4) {
     // (what the block was launched with, 168 or 128 a thread, is shared out anew)
-    if constexpr (CODE != 0) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if constexpr (CODE != 0) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     else asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == 0) {
       // ---------------- copies: Q tiles, and K/V tiles piece by piece of a page
@@ -1209,9 +1208,10 @@ __global__ void __launch_bounds__(kThreads<CODE>, 1) chunk_kernel(const __grid_c
   } else if (CODE != 0 && warp >= 12) {
     if constexpr (CODE != 0) {
       // ---------------- codes to halves (exact), in the layout that the copies of 16-bit pages have
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
       constexpr int NRAW = C::NRAW;
-      const int ct = tid - 12 * 32, nc = a.head_dim / 16;  // 16-byte pieces of a key
+      const int ct = tid - 12 * 32;
+      const int nc = a.head_dim / 16;  // 16-byte pieces of a key
       const unsigned inv_nc = (65536 + nc - 1) / nc;        // x / nc = x * inv_nc >> 16 for x < 1024
       const bool even = (nc & (nc - 1)) == 0;
       int u = 0, nt = 0, nq = 0;                            // ring uses, key tiles, Q tiles seen
@@ -1228,13 +1228,12 @@ __global__ void __launch_bounds__(kThreads<CODE>, 1) chunk_kernel(const __grid_c
           // value next to 2^15 is a row of halves, exactly but for what lies
           // 2^38 below that value; the softmax takes the power back
           if (!(ok = __all_sync(0xffffffffu, cwait(smem_u32(&sh.q_full), nq & 1, ab)))) break;
-          for (int s = 0; s < (mode == PAIR ? 2 : 1); ++s) {
-            const int rows = min(mode == PAIR ? tokens - s * a.tpq : tokens, a.tpq) * a.group;
-            if (ct >= rows) continue;
-            const uint32_t at = qbase + s * C::kQ + ct * 128;
+          const int s = ct >> 7, qr = ct & 127, rows = min(mode == PAIR ? tokens - s * a.tpq : tokens, a.tpq) * a.group;
+          if (qr < rows && (mode == PAIR || s == 0)) {
+            const uint32_t at = qbase + s * C::kQ + qr * 128;
             uint32_t most = 0;
             for (int j = 0; j < a.head_dim / 8; ++j) {
-              const uint4 w = lds128(at + (j >> 3) * (128 * 128) + (((j & 7) ^ (ct & 7)) << 4));
+              const uint4 w = lds128(at + (j >> 3) * (128 * 128) + (((j & 7) ^ (qr & 7)) << 4));
               const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
               for (int i = 0; i < 4; ++i) most = max(most, max(x[i] << 16 & 0x7fff0000u, x[i] & 0x7fff0000u));
@@ -1242,12 +1241,12 @@ __global__ void __launch_bounds__(kThreads<CODE>, 1) chunk_kernel(const __grid_c
             const int e = most >= 0x7f800000u || !most ? 0 : min(14 - ((int)(most >> 23) - 127), 100);
             const float f = __uint_as_float((unsigned)(e + 127) << 23);
             for (int j = 0; j < a.head_dim / 8; ++j) {
-              const uint32_t y = at + (j >> 3) * (128 * 128) + (((j & 7) ^ (ct & 7)) << 4);
+              const uint32_t y = at + (j >> 3) * (128 * 128) + (((j & 7) ^ (qr & 7)) << 4);
               const uint4 w = lds128(y);
               auto two = [&](uint32_t x) { return Kind<__half>::pack(__uint_as_float(x << 16) * f, __uint_as_float(x & 0xffff0000u) * f); };
               sts128(y, make_uint4(two(w.x), two(w.y), two(w.z), two(w.w)));
             }
-            sh.q_exp[nq & 1][s][ct] = (int8_t)e;
+            sh.q_exp[nq & 1][s][qr] = (int8_t)e;
           }
           fence_async_smem();
           __syncwarp();
@@ -1283,39 +1282,40 @@ __global__ void __launch_bounds__(kThreads<CODE>, 1) chunk_kernel(const __grid_c
           // the other order, so that eight lanes of a row of 128 meet eight different bank groups
           auto put = [&](uint32_t dst, int row, int c, const uint4& w, bool zero) {
             uint4 e[2];
-            codes_to_half<CODE>(w, e);
+            const bool swap = c >> 2 & 1;
+            codes_to_half<CODE>(make_uint4(swap ? w.z : w.x, swap ? w.w : w.y, swap ? w.x : w.z, swap ? w.y : w.w), e);
             if (zero) e[0] = e[1] = make_uint4(0, 0, 0, 0);
-            const uint32_t at = dst + (c >> 2) * (BK * 128) + row * 128;
-            const int swap = c >> 2 & 1, j0 = (2 * c + swap) & 7, j1 = (2 * c + 1 - swap) & 7;
-            sts128(at + ((j0 ^ (row & 7)) << 4), swap ? e[1] : e[0]);
-            sts128(at + ((j1 ^ (row & 7)) << 4), swap ? e[0] : e[1]);
+            const uint32_t at = dst + (c >> 2) * (BK * 128) + row * 128 + (((2 * c + (c >> 2 & 1)) & 7 ^ (row & 7)) << 4);
+            sts128(at, e[0]);
+            sts128(at ^ 16, e[1]);
           };
           // rows of V that no query may see can hold anything: 0 * NaN would reach every row through the product
           const bool ragged = (C::kTogether || r.is_v) && (key0 + BK > kl || key0 < lo);
           auto hidden = [&](int row) { return key0 + row >= kl || key0 + row < lo; };
           bool freed = false;
           if (even && !ragged) {
-            // a thread's pieces lie in one column, 128 / nc rows apart (a multiple of 8: the swizzle is the same for all)
-            const int row0 = ct / nc, c = ct - row0 * nc, step = 128 / nc;
-            constexpr int kAll = C::kTogether ? 2 : 1;  // K and V, one behind the other
-            uint4 w[8];
+            // a thread's pieces (K's and V's, one behind the other, or of wide heads one of them) lie in one column
+            const int all = C::kTogether ? nc : 4, c = ct & (nc - 1);
+            uint4 w[4];
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              if (i < kAll * nc) w[i] = lds128(from + (ct + 128 * i) * 16);
+            for (int i = 0; i < 4; ++i)
+              if (i < all) w[i] = lds128(from + (ct + 256 * i) * 16);
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&sh.raw_empty[rs]));
             freed = true;
             if (!(ok = __all_sync(0xffffffffu, stage_free()))) break;
-            scales();
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              if (i < kAll * nc) put(to + (i < nc ? 0 : C::kKV), row0 + step * (i < nc ? i : i - nc), c, w[i], false);
+            for (int i = 0; i < 4; ++i) {
+              const int at = (int)((unsigned)(ct + 256 * i) * inv_nc >> 16), second = at >= BK;  // the piece's row of both tiles
+              if (i < all) put(to + (second ? C::kKV : 0), at - second * BK, c, w[i], false);
+            }
+            scales();
           } else {
             if (!(ok = __all_sync(0xffffffffu, stage_free()))) break;
             scales();
             const int total = (C::kTogether ? 2 : 1) * BK * nc;
 #pragma unroll 1
-            for (int i = ct; i < total; i += 128) {
+            for (int i = ct; i < total; i += 256) {
               const bool second = i >= BK * nc;
               const int at = second ? i - BK * nc : i, row = (int)((unsigned)at * inv_nc >> 16);
               const bool v = C::kTogether ? second : r.is_v;
@@ -1334,7 +1334,7 @@ __global__ void __launch_bounds__(kThreads<CODE>, 1) chunk_kernel(const __grid_c
     }
   } else {
     // ---------------- softmax and epilogue: slot = warpgroup, thread = row (TMEM lane)
-    if constexpr (CODE != 0) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+    if constexpr (CODE != 0) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
     else asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     const int slot = (warp >> 2) - 1, quarter = warp & 3, tw = tid & 127;
     const uint32_t tl = (uint32_t)(quarter * 32) << 16;
