@@ -1214,6 +1214,11 @@ __global__ void __launch_bounds__(kThreads<CODE>, 1) chunk_kernel(const __grid_c
       const int nc = a.head_dim / 16;  // 16-byte pieces of a key
       const unsigned inv_nc = (65536 + nc - 1) / nc;        // x / nc = x * inv_nc >> 16 for x < 1024
       const bool even = (nc & (nc - 1)) == 0;
+      // where the thread's column begins in an operand tile (even): see put
+      const int own_c = ct & (nc - 1), own_row = (int)((unsigned)ct * inv_nc >> 16);
+      const uint32_t own_at = (own_c >> 2) * (BK * 128) + own_row * 128 + ((2 * own_c & 7 ^ (own_row & 7)) << 4);
+      const uint32_t own_step = C::kTogether ? 256 / nc * 128 : 4096;
+      static_assert(!C::kTogether || C::kKV == BK * 128, "V's rows follow K's");
       int u = 0, nt = 0, nq = 0;                            // ring uses, key tiles, Q tiles seen
       bool ok = true;
       for (int k = 0; ok; ++k) {
@@ -1278,14 +1283,13 @@ __global__ void __launch_bounds__(kThreads<CODE>, 1) chunk_kernel(const __grid_c
             }
             nt += keys;
           };
-          // 16-byte chunk j of a row lies at j ^ (row & 7) of its 128 bytes; the upper half's lanes store their two chunks in
-          // the other order, so that eight lanes of a row of 128 meet eight different bank groups
+          // 16-byte chunk j of a row lies at j ^ (row & 7) of its 128 bytes.  (A row of 128 meets four bank groups twice;
+          // storing the upper half's chunks in the other order, without conflicts, costs four selects a piece and 6 us of 484.)
           auto put = [&](uint32_t dst, int row, int c, const uint4& w, bool zero) {
             uint4 e[2];
-            const bool swap = c >> 2 & 1;
-            codes_to_half<CODE>(make_uint4(swap ? w.z : w.x, swap ? w.w : w.y, swap ? w.x : w.z, swap ? w.y : w.w), e);
+            codes_to_half<CODE>(w, e);
             if (zero) e[0] = e[1] = make_uint4(0, 0, 0, 0);
-            const uint32_t at = dst + (c >> 2) * (BK * 128) + row * 128 + (((2 * c + (c >> 2 & 1)) & 7 ^ (row & 7)) << 4);
+            const uint32_t at = dst + (c >> 2) * (BK * 128) + row * 128 + ((2 * c & 7 ^ (row & 7)) << 4);
             sts128(at, e[0]);
             sts128(at ^ 16, e[1]);
           };
@@ -1294,20 +1298,24 @@ __global__ void __launch_bounds__(kThreads<CODE>, 1) chunk_kernel(const __grid_c
           auto hidden = [&](int row) { return key0 + row >= kl || key0 + row < lo; };
           bool freed = false;
           if (even && !ragged) {
-            // a thread's pieces (K's and V's, one behind the other, or of wide heads one of them) lie in one column
-            const int all = C::kTogether ? nc : 4, c = ct & (nc - 1);
+            // a thread's pieces (K's and V's, one behind the other, or of wide heads one of them) lie in one column, the
+            // same distance apart in both forms (V's rows follow K's there too): addresses are sums
             uint4 w[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              if (i < all) w[i] = lds128(from + (ct + 256 * i) * 16);
+              if (!C::kTogether || i < nc) w[i] = lds128(from + ct * 16 + i * 4096);
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&sh.raw_empty[rs]));
             freed = true;
             if (!(ok = __all_sync(0xffffffffu, stage_free()))) break;
+            const uint32_t at = to + own_at;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const int at = (int)((unsigned)(ct + 256 * i) * inv_nc >> 16), second = at >= BK;  // the piece's row of both tiles
-              if (i < all) put(to + (second ? C::kKV : 0), at - second * BK, c, w[i], false);
+              if (C::kTogether && i >= nc) continue;
+              uint4 e[2];
+              codes_to_half<CODE>(w[i], e);
+              sts128(at + i * own_step, e[0]);
+              sts128((at ^ 16) + i * own_step, e[1]);
             }
             scales();
           } else {
