@@ -105,16 +105,19 @@ int attend(const dls_attention_chunk8_desc* d, const char* what, void* cuda_stre
   const CUtensorMapDataType dt = d->q_type == DLS_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const uint32_t pr = pt < BK ? pt : BK;
   CUtensorMap tq, tk, tv;
-  // Few rows a sequence: the kernel without operands of 128 rows.  The number
-  // of rows alone is known here, so a batch may hold a longer sequence all the
-  // same; its tiles then read their keys once for every sixteen rows, and all
+  // Few rows a sequence (two tiles of sixteen, on average): the kernel without
+  // operands of 128 rows.  4 heads a KV head of 128 and 8 sequences over 4096: 16
+  // rows 27 us (46 by the other), 32 rows 38 (47), 48 rows 52 (48); 64 over
+  // 2048: 76 (152), 132 (152), 187 (155); heads of 64 alike.  The number of rows
+  // alone is known here, so a batch may hold a longer sequence all the same;
+  // its tiles then read their keys once for every sixteen rows, and all
   // the batch's tiles are no more than those of equal sequences.
-  const bool few = d->code_type && (hd == 64 || hd == 128) && a.group <= kFewRows && (long long)d->n_tokens * a.group <= kFewRows * (long long)d->n_seqs;
+  const bool few = d->code_type && a.group <= kFewRows && (long long)d->n_tokens * a.group <= 2 * kFewRows * (long long)d->n_seqs;
   if (few) {
     const int rows = (long long)d->n_tokens * a.group <= 8 * (long long)d->n_seqs && a.group <= 8 ? 8 : kFewRows;
     a.tile_tokens = rows / a.group;
     a.small_plan = d->n_seqs <= 128 && d->n_tokens <= 128 * a.tile_tokens && (long long)d->max_pages * pt <= 1 << 24;
-    const CUtensorMapSwizzle sw = hd == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+    const CUtensorMapSwizzle sw = hd == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : hd == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE;
     if (!make_tmap_2d(&tk, CU_TENSOR_MAP_DATA_TYPE_UINT8, d->k_pages, hd, a.pool_rows, hd, hd, pr, sw) ||
         !make_tmap_2d(&tv, CU_TENSOR_MAP_DATA_TYPE_UINT8, d->v_pages, hd, a.pool_rows, hd, hd, pr, sw))
       return report_error(DLS_ERR_CUDA, "%s: tensor map (head_dim=%d)", what, hd);

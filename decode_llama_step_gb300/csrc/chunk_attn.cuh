@@ -1588,7 +1588,7 @@ cudaError_t chunk_codes_setup();
 cudaError_t launch_chunk_codes(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const ChunkArgs& a, int code, bool half,
                                int ctas, cudaStream_t s);
 
-// The same for tiles of few rows (few_attn8.cu): head_dim 64 or 128, at most 16 rows a tile, c's tile_tokens.
+// The same for tiles of few rows (few_attn8.cu): at most 16 rows a tile, c's tile_tokens.
 constexpr int kFewRows = 16;
 cudaError_t few_codes_setup();
 cudaError_t launch_few_codes(const CUtensorMap& tk, const CUtensorMap& tv, const ChunkArgs& c, const void* q, long long q_stride, bool half,

@@ -17,7 +17,10 @@
 //              codes of them are its part of a k-step, q's fragments follow
 //   O += P V   lane 4r + c holds dimensions [16 r, 16 r + 16) of keys 2c,
 //              2c + 1, 2c + 8, 2c + 9: byte permutes pair the keys
-// (head_dim 128; half of each at 64).  The scores' fragment is the weights'.
+// (head_dim 128; half of each at 64; other ones are read by words as they lie:
+// k-step s is dimensions [16 s, 16 s + 16), four of them a lane, and the lane's
+// dimensions of V are [32 i + 4 r, 32 i + 4 r + 4), and two of a last half).
+// The scores' fragment is the weights'.
 // Eight such warps work on 128 keys; each keeps its own (R, l, O), joined in
 // shared memory at the end of a piece and, where a tile was cut, through the
 // workspace in range order.
@@ -41,9 +44,13 @@ struct FCfg {
   static constexpr int kRows = WIDE ? 16 : 8;
   static constexpr int kPart = BK * HD;              // bytes of a key tile's K or V
   static constexpr int kStage = 2 * kPart;
-  static constexpr int NST = 131072 / kStage;        // 128 KB in flight an SM
+  static constexpr int NST = 131072 / kStage < 8 ? 131072 / kStage : 8;  // 128 KB in flight an SM
   static constexpr int kMergeOff = NST * kStage;
-  static constexpr int kMiscOff = kMergeOff + FWARPS * kRows * HD * 4;
+  static constexpr bool kWide16 = HD == 64 || HD == 128;      // read 16 bytes at a time, through a swizzle
+  static constexpr int kRowF = kWide16 ? HD : HD + 4;         // floats of a row where shares are joined
+  static constexpr int kMergeBytes = FWARPS * kRows * kRowF * 4;
+  static constexpr int kEnd = kMergeOff + (kMergeBytes < MAXC * 32 * 4 ? MAXC * 32 * 4 : kMergeBytes);  // (or a join's statistics)
+  static constexpr int kMiscOff = kEnd < DLS_MAX_CHUNK_SEQS * 16 ? DLS_MAX_CHUNK_SEQS * 16 : kEnd;        // (or the lengths being planned over)
 };
 struct FMisc {
   uint64_t full[8], empty[8], pq_full[QDEPTH], pq_empty[QDEPTH];
@@ -60,7 +67,6 @@ constexpr int few_smem() {
   return FCfg<HD, WIDE>::kMiscOff + (int)sizeof(FMisc) + 1024;
 }
 static_assert(few_smem<128, true>() <= 227 * 1024, "shared memory");
-static_assert(DLS_MAX_CHUNK_SEQS * 16 <= FCfg<64, false>::kMergeOff, "plan scratch");
 
 struct FewArgs {
   ChunkArgs c;
@@ -89,6 +95,17 @@ __device__ __forceinline__ uint32_t two_halves(uint32_t w) {
   return h;
 }
 
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t a) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
+  return v;
+}
+
 __device__ __forceinline__ bool all_warps(bool ok) {
   uint32_t r;
   asm volatile(
@@ -105,11 +122,21 @@ __device__ __forceinline__ void meet() { named_bar(1, FWARPS * 32); }
 // halves (see the converting warps of chunk_attn.cuh); cq takes it back.
 template <int HD>
 __device__ __forceinline__ void load_q(const FewArgs& a, bool live, size_t at, uint32_t (&w)[HD / 8], float& cq) {
-  const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at);
+  const uint16_t* const row = static_cast<const uint16_t*>(a.q) + at;
+  const int c = threadIdx.x & 3;
+  if constexpr (HD == 64 || HD == 128) {
+    const uint4* p = reinterpret_cast<const uint4*>(row + (HD / 4) * c);
 #pragma unroll
-  for (int i = 0; i < HD / 32; ++i) {
-    const uint4 x = live ? p[i] : make_uint4(0, 0, 0, 0);
-    w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
+    for (int i = 0; i < HD / 32; ++i) {
+      const uint4 x = live ? p[i] : make_uint4(0, 0, 0, 0);
+      w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
+    }
+  } else {
+#pragma unroll
+    for (int s = 0; s < HD / 16; ++s) {
+      const uint2 x = live ? *reinterpret_cast<const uint2*>(row + 16 * s + 4 * c) : make_uint2(0, 0);
+      w[2 * s] = x.x, w[2 * s + 1] = x.y;
+    }
   }
   cq = 1.f;
   if (a.q_bf16) {
@@ -130,7 +157,7 @@ template <int HD, int CODE, bool WIDE>
 __global__ void __launch_bounds__(FTHREADS, 1) few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                                                           const __grid_constant__ FewArgs fa) {
   using C = FCfg<HD, WIDE>;
-  constexpr int NST = C::NST, HDP = HD;
+  constexpr int NST = C::NST, HDP = HD <= 64 ? 64 : 128;  // HDP: as the workspace is laid out
   const ChunkArgs& a = fa.c;
   extern __shared__ __align__(1024) uint8_t fsm[];
   const uint32_t raw = smem_u32(fsm), pad = (1024u - (raw & 1023u)) & 1023u, base = raw + pad;
@@ -254,7 +281,7 @@ __global__ void __launch_bounds__(FTHREADS, 1) few_kernel(const __grid_constant_
       row[h].ok = x < n_rows;
       row[h].hi = !row[h].ok ? 0x7fffffff : a.causal ? min(max(pos + 1, 0), p.kl) : p.kl;
       row[h].lo = row[h].ok && a.window && pos >= a.window ? pos - a.window + 1 : 0;
-      const size_t qrow = row[h].ok ? (size_t)(p.row0 + tok) * fa.q_stride + (size_t)(p.kvh * G + x - tok * G) * HD + (HD / 4) * c : 0;
+      const size_t qrow = row[h].ok ? (size_t)(p.row0 + tok) * fa.q_stride + (size_t)(p.kvh * G + x - tok * G) * HD : 0;
       load_q<HD>(fa, row[h].ok, qrow, qa[h], cq[h]);
     }
     float o[HD / 8][4];
@@ -276,21 +303,29 @@ __global__ void __launch_bounds__(FTHREADS, 1) few_kernel(const __grid_constant_
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           const int key = 8 * t + r;
+          auto product = [&](int st, uint32_t x) {
+            const uint32_t qf[4] = {qa[0][2 * st], WIDE ? qa[WIDE][2 * st] : 0u, qa[0][2 * st + 1], WIDE ? qa[WIDE][2 * st + 1] : 0u};
+            mma16816(sc[t], qf, two_halves<CODE, false>(x), two_halves<CODE, true>(x));
+          };
+          if constexpr (C::kWide16) {
 #pragma unroll
-          for (int h = 0; h < HD / 64; ++h) {
-            const int chunk = HD == 128 ? (2 * c + h) ^ (key & 7) : c ^ (key >> 1 & 3);
-            const uint4 w = lds128(kt + key * HD + chunk * 16);
-            const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+            for (int h = 0; h < HD / 64; ++h) {
+              const int chunk = HD == 128 ? (2 * c + h) ^ (key & 7) : c ^ (key >> 1 & 3);
+              const uint4 w = lds128(kt + key * HD + chunk * 16);
+              const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int st = 4 * h + e;
-              const uint32_t qf[4] = {qa[0][2 * st], WIDE ? qa[WIDE][2 * st] : 0u, qa[0][2 * st + 1], WIDE ? qa[WIDE][2 * st + 1] : 0u};
-              mma16816(sc[t], qf, two_halves<CODE, false>(x[e]), two_halves<CODE, true>(x[e]));
+              for (int e = 0; e < 4; ++e) product(4 * h + e, x[e]);
             }
+          } else {
+            uint32_t x[HD / 16];
+#pragma unroll
+            for (int st = 0; st < HD / 16; ++st) x[st] = lds32(kt + key * HD + 16 * st + 4 * c);
+#pragma unroll
+            for (int st = 0; st < HD / 16; ++st) product(st, x[st]);
           }
         }
         // V's codes: keys 2c, 2c + 1, 2c + 8, 2c + 9
-        constexpr int VW = HD / 32;  // words of a lane's dimensions
+        constexpr int VW = (HD + 16) / 32;  // words of a lane's dimensions, the last one a half where HD / 16 is odd
         uint32_t v[4][VW];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -298,6 +333,10 @@ __global__ void __launch_bounds__(FTHREADS, 1) few_kernel(const __grid_constant_
           if constexpr (HD == 128) {
             const uint4 w = lds128(vt + key * HD + ((r ^ (key & 7)) << 4));
             v[e][0] = w.x, v[e][1] = w.y, v[e][2] = w.z, v[e][3] = w.w;
+          } else if constexpr (HD != 64) {
+#pragma unroll
+            for (int x = 0; x < HD / 32; ++x) v[e][x] = lds32(vt + key * HD + 32 * x + 4 * r);
+            if constexpr (HD % 32 != 0) v[e][VW - 1] = lds16(vt + key * HD + HD - 16 + 2 * r);
           } else {
             asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];"
                          : "=r"(v[e][0]), "=r"(v[e][1])
@@ -366,8 +405,10 @@ __global__ void __launch_bounds__(FTHREADS, 1) few_kernel(const __grid_constant_
           const uint32_t hi01 = __byte_perm(v[0][x], v[1][x], 0x7362), hi23 = __byte_perm(v[2][x], v[3][x], 0x7362);
           mma16816(o[4 * x], pa, two_halves<CODE, false>(lo01), two_halves<CODE, false>(lo23));
           mma16816(o[4 * x + 1], pa, two_halves<CODE, true>(lo01), two_halves<CODE, true>(lo23));
-          mma16816(o[4 * x + 2], pa, two_halves<CODE, false>(hi01), two_halves<CODE, false>(hi23));
-          mma16816(o[4 * x + 3], pa, two_halves<CODE, true>(hi01), two_halves<CODE, true>(hi23));
+          if (4 * x + 2 < HD / 8) {
+            mma16816(o[(4 * x + 2) % (HD / 8)], pa, two_halves<CODE, false>(hi01), two_halves<CODE, false>(hi23));
+            mma16816(o[(4 * x + 3) % (HD / 8)], pa, two_halves<CODE, true>(hi01), two_halves<CODE, true>(hi23));
+          }
         }
       } else {
         __syncwarp();
@@ -376,22 +417,34 @@ __global__ void __launch_bounds__(FTHREADS, 1) few_kernel(const __grid_constant_
     }
     u0 += n;
 
-    // ---- the warps' shares meet.  A lane's HD / 4 dimensions of a row lie in
-    // 16-byte pieces, moved by its number against bank conflicts.
-    constexpr int kPieces = HD / 16, kRowF = HD;  // 16-byte pieces of a lane, floats of a row
+    // ---- the warps' shares meet.  Where codes are read 16 bytes at a time a
+    // lane's HD / 4 dimensions of a row lie in 16-byte pieces, moved by its number
+    // against bank conflicts; else rows are four floats longer.
+    constexpr int kPieces = HD / 16, kRowF = C::kRowF;  // 16-byte pieces of a lane, floats of a row
 #pragma unroll
     for (int h = 0; h < (WIDE ? 2 : 1); ++h) {
       float s = l[h];
       s += __shfl_xor_sync(0xffffffffu, s, 1);
       s += __shfl_xor_sync(0xffffffffu, s, 2);
       if (c == 0) sh.R[warp][r + 8 * h] = R[h], sh.l[warp][r + 8 * h] = s;
-      float* const to = merge + (size_t)(warp * C::kRows + r + 8 * h) * kRowF + c * (HD / 4);
+      float* const to = merge + (size_t)(warp * C::kRows + r + 8 * h) * kRowF;
 #pragma unroll
       for (int x = 0; x < kPieces; ++x) {
-        // dimensions 4 x .. of the lane's: o[j][.] holds j and HD / 8 + j
-        const int up = x >= kPieces / 2, j = 4 * x - up * (HD / 8);
-        *reinterpret_cast<float4*>(to + ((x ^ (lane & (kPieces - 1))) << 2)) =
-            make_float4(o[j][2 * h + up], o[j + 1][2 * h + up], o[j + 2][2 * h + up], o[j + 3][2 * h + up]);
+        if constexpr (C::kWide16) {
+          // dimensions 4 x .. of the lane's: o[j][.] holds j and HD / 8 + j
+          const int up = x >= kPieces / 2, j = 4 * x - up * (HD / 8);
+          *reinterpret_cast<float4*>(to + c * (HD / 4) + ((x ^ (lane & (kPieces - 1))) << 2)) =
+              make_float4(o[j][2 * h + up], o[j + 1][2 * h + up], o[j + 2][2 * h + up], o[j + 3][2 * h + up]);
+        } else if (x < HD / 32 * 2) {
+          // eight dimensions from 32 i + 8 c on: o[4 i + e][.] holds e and 4 + e of them
+          const int up = x & 1, j = 4 * (x >> 1);
+          *reinterpret_cast<float4*>(to + 32 * (x >> 1) + 8 * c + 4 * up) =
+              make_float4(o[j][2 * h + up], o[j + 1][2 * h + up], o[(j + 2) % (HD / 8)][2 * h + up], o[(j + 3) % (HD / 8)][2 * h + up]);
+        } else {
+          // four of the last sixteen: o[j][.] holds 0 and 2, o[j + 1][.] 1 and 3
+          const int j = HD / 8 - 2;
+          *reinterpret_cast<float4*>(to + HD - 16 + 4 * c) = make_float4(o[j][2 * h], o[j + 1][2 * h], o[j][2 * h + 1], o[j + 1][2 * h + 1]);
+        }
       }
     }
     meet();
@@ -411,8 +464,11 @@ __global__ void __launch_bounds__(FTHREADS, 1) few_kernel(const __grid_constant_
     };
     for (int it = tid; it < n_rows * C4; it += FWARPS * 32) {
       const int x = it / C4, d = it - x * C4;
-      const int q = 4 * d / (HD / 4), piece = d - q * kPieces;
-      const int moved = (piece ^ ((4 * (x & 7) + q) & (kPieces - 1))) << 2;
+      int from = 4 * d;
+      if constexpr (C::kWide16) {
+        const int q = d / kPieces, piece = d - q * kPieces;
+        from = q * (HD / 4) + ((piece ^ ((4 * (x & 7) + q) & (kPieces - 1))) << 2);
+      }
       float M = -INFINITY, L = 0.f;
 #pragma unroll
       for (int w = 0; w < FWARPS; ++w) M = fmaxf(M, sh.R[w][x]);
@@ -420,7 +476,7 @@ __global__ void __launch_bounds__(FTHREADS, 1) few_kernel(const __grid_constant_
 #pragma unroll
       for (int w = 0; w < FWARPS; ++w) {
         const float f = weight(sh.R[w][x], M);
-        const float4 z = *reinterpret_cast<const float4*>(merge + (size_t)(w * C::kRows + x) * kRowF + q * (HD / 4) + moved);
+        const float4 z = *reinterpret_cast<const float4*>(merge + (size_t)(w * C::kRows + x) * kRowF + from);
         L = fmaf(f, sh.l[w][x], L);
         y.x = fmaf(f, z.x, y.x), y.y = fmaf(f, z.y, y.y), y.z = fmaf(f, z.z, y.z), y.w = fmaf(f, z.w, y.w);
       }
@@ -479,25 +535,36 @@ __global__ void __launch_bounds__(FTHREADS, 1) few_kernel(const __grid_constant_
 
 using FewFn = void (*)(const CUtensorMap, const CUtensorMap, const FewArgs);
 
+struct Few {
+  FewFn f;
+  int smem;
+};
 template <int HD, int CODE>
-FewFn few_fn(bool wide) {
-  return wide ? few_kernel<HD, CODE, true> : few_kernel<HD, CODE, false>;
+Few few_of(bool wide) {
+  if (wide) return {few_kernel<HD, CODE, true>, few_smem<HD, true>()};
+  return {few_kernel<HD, CODE, false>, few_smem<HD, false>()};
 }
-FewFn few_fn(int hd, int code, bool wide) {
-  if (hd == 128) return code == DLS_E4M3 ? few_fn<128, DLS_E4M3>(wide) : few_fn<128, DLS_I8>(wide);
-  return code == DLS_E4M3 ? few_fn<64, DLS_E4M3>(wide) : few_fn<64, DLS_I8>(wide);
+template <int CODE>
+Few few_of(int hd, bool wide) {
+  switch (hd) {
+    case 16: return few_of<16, CODE>(wide);
+    case 32: return few_of<32, CODE>(wide);
+    case 48: return few_of<48, CODE>(wide);
+    case 64: return few_of<64, CODE>(wide);
+    case 80: return few_of<80, CODE>(wide);
+    case 96: return few_of<96, CODE>(wide);
+    case 112: return few_of<112, CODE>(wide);
+    default: return few_of<128, CODE>(wide);
+  }
 }
-int few_bytes(int hd, bool wide) {
-  return hd == 128 ? (wide ? few_smem<128, true>() : few_smem<128, false>()) : (wide ? few_smem<64, true>() : few_smem<64, false>());
-}
+Few few_of(int hd, int code, bool wide) { return code == DLS_E4M3 ? few_of<DLS_E4M3>(hd, wide) : few_of<DLS_I8>(hd, wide); }
 
 }  // namespace
 
 cudaError_t few_codes_setup() {
-  for (int i = 0; i < 8; ++i) {
-    const int hd = i & 1 ? 64 : 128;
-    const cudaError_t e =
-        cudaFuncSetAttribute(few_fn(hd, i & 2 ? DLS_I8 : DLS_E4M3, i & 4), cudaFuncAttributeMaxDynamicSharedMemorySize, few_bytes(hd, i & 4));
+  for (int i = 0; i < 32; ++i) {
+    const Few k = few_of(16 + (i >> 2) * 16, i & 2 ? DLS_I8 : DLS_E4M3, i & 1);
+    const cudaError_t e = cudaFuncSetAttribute(k.f, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
@@ -507,7 +574,8 @@ cudaError_t launch_few_codes(const CUtensorMap& tk, const CUtensorMap& tv, const
                              int code, int ctas, cudaStream_t s) {
   FewArgs a{c, q, q_stride, !half};
   const bool wide = a.c.tile_tokens * a.c.group > 8;
-  few_fn(a.c.head_dim, code, wide)<<<ctas, FTHREADS, few_bytes(a.c.head_dim, wide), s>>>(tk, tv, a);
+  const Few k = few_of(a.c.head_dim, code, wide);
+  k.f<<<ctas, FTHREADS, k.smem, s>>>(tk, tv, a);
   return cudaGetLastError();
 }
 

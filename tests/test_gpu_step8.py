@@ -723,7 +723,9 @@ FEW = [  # few rows a sequence: heads x new tokens of a KV head's group up to ei
 
 @pytest.mark.parametrize("lengths,heads,kvh", FEW, ids=lambda x: f"{len(x)}seqs" if isinstance(x, list) else str(x))
 @pytest.mark.parametrize("hd,page,block,typ,code", [(128, 64, 64, "bf16", "e4m3"), (64, 16, 16, "f16", "i8"), (128, 16, 16, "f16", "e4m3"),
-                                                    (64, 256, 32, "bf16", "e4m3"), (128, 128, 32, "bf16", "i8")])
+                                                    (64, 256, 32, "bf16", "e4m3"), (128, 128, 32, "bf16", "i8"), (96, 64, 16, "f16", "e4m3"),
+                                                    (80, 16, 16, "bf16", "i8"), (112, 32, 32, "f16", "e4m3"), (48, 128, 64, "bf16", "e4m3"),
+                                                    (32, 64, 64, "f16", "i8"), (16, 16, 16, "bf16", "e4m3")])
 def test_attention8_few_rows(gpu_lib, lengths, heads, kvh, hd, page, block, typ, code):
     check_attend(lengths, heads, kvh, hd, page, block, typ, code, first=1, pad=2)
 
@@ -732,6 +734,7 @@ def test_attention8_few_rows(gpu_lib, lengths, heads, kvh, hd, page, block, typ,
 def test_attention8_few_rows_windows(gpu_lib, window):
     check_attend([(1, 1000), (2, 300), (1, 33), (3, 3), (1, 1)], 8, 2, 128, 32, 16, "f16", "e4m3", window=window)
     check_attend([(1, 1000), (2, 300), (1, 33), (3, 3), (1, 1)], 4, 2, 64, 16, 16, "bf16", "i8", window=window)
+    check_attend([(1, 1000), (2, 300), (1, 33), (3, 3), (1, 1)], 4, 2, 80, 64, 16, "bf16", "e4m3", window=window)
 
 
 def test_attention8_few_rows_without_keys_and_every_key(gpu_lib):
@@ -746,7 +749,7 @@ def test_attention8_few_rows_scales_of_scores(gpu_lib, scale):
     check_attend([(1, 777), (2, 400)], 4, 2, 128, 64, 32, "f16", "e4m3", scale=scale)
 
 
-@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("hd", [64, 112, 128])
 @pytest.mark.parametrize("lengths,heads", [([(1, 9000)], 16), ([(3, 5000), (1, 3001)], 16)])
 def test_attention8_rising_scores(gpu_lib, hd, lengths, heads):
     """Keys whose scores grow along the sequence: the running maximum moves at every step, by little and by much."""
