@@ -33,7 +33,7 @@ namespace dls {
 namespace {
 
 constexpr int FWARPS = 8;
-constexpr int FTHREADS = (FWARPS + 1) * 32;
+constexpr int FTHREADS = (FWARPS + 2) * 32;   // with one warp for the copies, one for the scales
 constexpr int FK = 16;             // keys of a warp's step; FWARPS * FK = BK
 static_assert(FWARPS * FK == BK, "a key tile is a round of the warps");
 constexpr int kFewCost = 1;        // what a tile of work costs beyond its key tiles, in key tiles
@@ -57,7 +57,7 @@ struct FMisc {
   Piece pq[QDEPTH];
   float scale[8][2][FWARPS];     // of a stage: K's and V's for each warp's keys
   float R[FWARPS][16], l[FWARPS][16];
-  long long scan[FWARPS + 1];
+  long long scan[FWARPS + 2];
   long long range0, range1, per;
   int b0, t0, off0, kvh0, start0, ql0, kl0;
   int abort, last;
@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(FTHREADS, 1) few_kernel(const __grid_constant_
   }
   if (warp == FWARPS && lane < QDEPTH) {
     mbar_init(smem_u32(&sh.pq_full[lane]), 1);
-    mbar_init(smem_u32(&sh.pq_empty[lane]), FWARPS);
+    mbar_init(smem_u32(&sh.pq_empty[lane]), FWARPS + 1);
   }
   if (tid == FTHREADS - 1) {
     prefetch_tmap(&tm_k);
@@ -237,24 +237,54 @@ __global__ void __launch_bounds__(FTHREADS, 1) few_kernel(const __grid_constant_
             tma_load_2d(dst + v * C::kPart + x * pr * HD, v ? &tm_v : &tm_k, 0, y, bar);
           }
         }
-        const int w = lane & 7, v = lane >> 3 & 1, key = j * BK + w * FK;
-        const int page = __shfl_sync(0xffffffffu, entry, ((key >> a.page_shift) - entries_at) & 31);
-        if (lane < 2 * FWARPS) {  // both scales of each warp's keys (no page: 0)
-          const float* from = v ? a.v_scales : a.k_scales;
-          int bytes = 0;
-          if (key < p.kl && key + FK > p.lo && page >= 0 && page < a.n_pages) {
-            from += ((size_t)(page * a.n_kv + p.kvh) << (a.page_shift - a.block_shift)) + ((key & ((1 << a.page_shift) - 1)) >> a.block_shift);
-            bytes = 4;
-          }
-          asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(&sh.scale[s][v][w])), "l"(from), "r"(bytes) : "memory");
-          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
-        }
       }
     }
     // no copy may be in flight when the CTA ends
     __syncwarp();
     for (int x = u > NST ? u - NST : 0; x < u; ++x) cwait(smem_u32(&sh.full[x % NST]), (x / NST) & 1, ab, false);
     if (!ok && a.status && lane == 0) atomicOr(a.status, kTimeout);
+    return;
+  }
+  if (warp == FWARPS + 1) {
+    // ---------------- both scales of each warp's keys (no page: 0).  A warp of its own: with the copies' they took
+    // 1250 cycles a key tile, which bounded narrow heads
+    bool ok = true;
+    int u = 0;
+    const int w = lane & 7, v = lane >> 3 & 1;
+    for (int k = 0; ok; ++k) {
+      if (!(ok = __all_sync(0xffffffffu, cwait(smem_u32(&sh.pq_full[k % QDEPTH]), (k / QDEPTH) & 1, ab)))) break;
+      const Piece p = sh.pq[k % QDEPTH];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sh.pq_empty[k % QDEPTH]));
+      if (p.mode == END) break;
+      const int32_t* table = a.page_table + (size_t)p.b * a.max_pages;
+      const int per_page = a.page_shift - a.block_shift;
+      int entries_at = -(1 << 30), entry = -1;
+#pragma unroll 1
+      for (int j = p.ja; j < p.jb; ++j, ++u) {
+        const int first = (j * BK) >> a.page_shift, last = ((j + 1) * BK - 1) >> a.page_shift;
+        if (last >= entries_at + 32) {
+          entries_at = first;
+          const int e = entries_at + lane;
+          entry = -1;
+          if ((long long)e << a.page_shift < p.kl && (long long)(e + 1) << a.page_shift > p.lo) entry = table[e];
+        }
+        const int s = u % NST, key = j * BK + w * FK;
+        const int page = __shfl_sync(0xffffffffu, entry, ((key >> a.page_shift) - entries_at) & 31);
+        const float* from = v ? a.v_scales : a.k_scales;
+        int bytes = 0;
+        if (key < p.kl && key + FK > p.lo && page >= 0 && page < a.n_pages) {
+          from += ((size_t)(page * a.n_kv + p.kvh) << per_page) + ((key & ((1 << a.page_shift) - 1)) >> a.block_shift);
+          bytes = 4;
+        }
+        if (u >= NST && !(ok = __all_sync(0xffffffffu, cwait(smem_u32(&sh.empty[s]), ((u / NST) - 1) & 1, ab)))) break;
+        if (lane < 2 * FWARPS) {
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(&sh.scale[s][v][w])), "l"(from), "r"(bytes) : "memory");
+          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&sh.full[s])) : "memory");
+        }
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");  // none in flight when the CTA ends
     return;
   }
 
