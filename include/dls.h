@@ -651,8 +651,11 @@ int dls_kv_reserve(const dls_kv_reserve_desc* d, void* cuda_stream);
  * (any positive one) unless the new rows need a larger one; then its earlier
  * codes are divided by the growth and rounded again.  NaN becomes NaN (e4m3) or 0 and does not count for
  * the scale, an infinity the largest code.  Codes and scales of blocks that
- * get no row are left as they are.  (dls_qk_norm_rope takes q, at
- * dls_kv_reserve's positions.) */
+ * get no row are left as they are.  A block belongs to one appending sequence: where two sequences
+ * append to the same block in one call, its codes and scale are undefined, and
+ * a growing scale changes the codes of its earlier tokens for everyone who
+ * shares them (copy a partly filled page before appending, as dls_kv_fork_shared
+ * does).  (dls_qk_norm_rope takes q, at dls_kv_reserve's positions.) */
 typedef struct dls_kv_append8_desc {
   const void* k;            /* in_type [n_tokens][n_kv_heads][head_dim] */
   const void* v;
@@ -729,9 +732,9 @@ int dls_attention_chunk8(const dls_attention_chunk8_desc* d, void* cuda_stream);
  *   the sequence's other rows; rows of no sequence are left as they are.
  *  n_accepted[b]: drafts that stand (0 for a sequence without rows).
  *  kv_len_out[b] = kv_len[b] less the drafts that do not (may be kv_len).
- * Probabilities count as 0..1 (NaN as 0), whatever their sum;
- * random numbers as 0 <= x < 1 (NaN as 0).  A drafted token outside
- * [0, vocab) does not stand and sets status bit 2; bit 4 marks a cu_q that does
+ * In the sums probabilities count as 0..1 (NaN as 0), whatever they add up to, and
+ * pick as 0 <= x < 1 (NaN as 0); a comparison with a NaN says that the draft does
+ * not stand.  A drafted token outside [0, vocab) does not stand and sets status bit 2; bit 4 marks a cu_q that does
  * not fit, whose sequence has n_accepted 0 and no out_tokens. */
 typedef struct dls_verify_draft_desc {
   const int32_t* tokens;    /* device [n_tokens] */

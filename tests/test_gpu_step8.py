@@ -107,7 +107,7 @@ class Requests:
         self.stack = free[:self.count] + [-9] * (pages - self.count)
         self.page, self.r = page, r
 
-    def run(self, new, max_rows, pad=0, alias=False, arrays=True, stream=None):
+    def run(self, new, max_rows, pad=0, alias=False, arrays=True, stream=None, skew=0):
         want = reserve_plain(new, self.kv, self.held, self.table, self.stack, self.count, self.page, max_rows)
         n = len(new)
         kv, held, count = ints(self.kv), ints(self.held), ints([self.count])
@@ -115,7 +115,8 @@ class Requests:
         table, stack = ints(self.table).reshape(n, self.most), ints(self.stack)
         cu = torch.full((n + 1,), 77, dtype=I32, device="cuda")
         status = ints([99])
-        got = [torch.full((max_rows + pad,), 77, dtype=I32, device="cuda") for _ in range(3)] if arrays else [None] * 3
+        # skew: the arrays begin between two 16-byte boundaries
+        got = [torch.full((max_rows + pad + skew,), 77, dtype=I32, device="cuda")[skew:] for _ in range(3)] if arrays else [None] * 3
         dls.kv_reserve(ints(new), kv, held, table, stack, count, *out, cu, self.page, positions=got[0], slots=got[1],
                        seq_ids=got[2], max_rows=max_rows, status=status, stream=stream)
         torch.cuda.synchronize()
@@ -138,7 +139,7 @@ def test_reserve_single_tokens(gpu_lib, n, page):
     r.run([random.Random(b).choice([1, 1, 1, 0, -1]) for b in range(n)], n, pad=5, alias=True)
 
 
-@pytest.mark.parametrize("n,page,rows", [(1, 16, 1), (1, 64, 5000), (5, 32, 700), (64, 16, 300), (211, 16, 90), (7, 256, 20000)])
+@pytest.mark.parametrize("n,page,rows", [(1, 16, 1), (1, 64, 5000), (5, 32, 700), (64, 16, 300), (211, 16, 90), (7, 256, 20000), (13, 64, 20000)])
 def test_reserve_prompts(gpu_lib, n, page, rows):
     r = Requests(n, page, 7 * n + rows, spare=n * (rows // page + 2), most=rows // page + 30)
     new = [r.r.choice([rows, rows // 2 + 1, 1, 0]) for _ in range(n)]
@@ -159,6 +160,7 @@ def test_reserve_when_pages_or_rows_run_out(gpu_lib, seed):
     r.run(new, 0)
     r.run(new, total, alias=True)
     r.run(new, total, arrays=False)
+    r.run(new, total, skew=1, stream=torch.cuda.current_stream())
 
 
 def test_reserve_states_that_cannot_be(gpu_lib):
@@ -396,6 +398,9 @@ def check_append(lengths, kvh, hd, rot, page, block, tin, code, norm, pairing, f
     ([(700, 1700), (1, 300), (40, 41)], 3, 128, 128, 256, 128, "f32", "e4m3", True, "adjacent", 0, 0),
     ([(31, 1000), (1, 1), (9, 77), (8, 64), (65, 65)], 5, 48, 32, 128, 64, "bf16", "i8", True, "adjacent", 3, 40),
     ([(1, 60)] * 63 + [(2048, 2048)], 2, 64, 64, 64, 64, "bf16", "e4m3", False, "halves", 0, 0),
+    # blocks whose angles are too many to be held
+    ([(300, 700), (1, 5), (256, 256)], 1, 256, 256, 256, 256, "bf16", "e4m3", True, "halves", 0, 0),
+    ([(700, 1700), (2, 900)], 2, 128, 128, 256, 256, "f16", "i8", True, "adjacent", 1, 1),
 ])
 def test_append8(gpu_lib, lengths, kvh, hd, rot, page, block, tin, code, norm, pairing, first, pad):
     check_append(lengths, kvh, hd, rot, page, block, tin, code, norm, pairing, first, pad)
@@ -1165,6 +1170,43 @@ def test_verify_agrees_with_the_distribution(gpu_lib):
                      torch.rand(n, generator=g, device="cuda"), out, acc, draft=q.expand(2 * n, vocab).contiguous())
     share = torch.bincount(out[::2].long(), minlength=vocab).double() / n
     assert bool(((share - p.double()).abs() <= 5 * (p.double() * (1 - p.double()) / n).sqrt()).all())  # five standard deviations
+
+
+def test_verify_on_streams_and_in_a_graph(gpu_lib):
+    """Two calls at once on two streams, and a captured one replayed with other inputs, give what each gives alone."""
+    made = []
+    for seed, n, vocab in ((1, 9, 128256), (2, 40, 5003)):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        rows = 4 * n
+        s = dict(tokens=torch.randint(0, vocab, (rows,), generator=g, device="cuda", dtype=I32),
+                 target=torch.softmax(2 * torch.randn(rows, vocab, generator=g, device="cuda"), -1),
+                 draft=torch.softmax(2 * torch.randn(rows, vocab, generator=g, device="cuda"), -1), cu=torch.arange(n + 1, device="cuda", dtype=I32) * 4,
+                 accept=torch.rand(rows, generator=g, device="cuda") * 0.01, pick=torch.rand(n, generator=g, device="cuda"))
+        made.append((s, [(torch.full((rows,), 7, dtype=I32, device="cuda"), torch.full((n,), 7, dtype=I32, device="cuda")) for _ in range(2)], torch.cuda.Stream()))
+
+    def call(s, out, stream):
+        dls.verify_draft(s["tokens"], s["target"], s["cu"], s["accept"], s["pick"], *out, draft=s["draft"], stream=stream)
+
+    for s, out, _ in made:
+        call(s, out[0], None)
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s, out, stream in made:
+            call(s, out[1], stream)
+    torch.cuda.synchronize()
+    for s, out, _ in made:
+        assert torch.equal(out[0][0], out[1][0]) and torch.equal(out[0][1], out[1][1])
+    s, out, stream = made[1]
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr, stream=stream):
+        call(s, out[1], torch.cuda.current_stream())
+    s["target"].copy_(s["draft"].flip(0))
+    s["pick"].mul_(0.5)
+    call(s, out[0], None)
+    torch.cuda.synchronize()
+    gr.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out[0][0], out[1][0]) and torch.equal(out[0][1], out[1][1])
 
 
 def test_verify_flags_rows_that_do_not_fit(gpu_lib):
