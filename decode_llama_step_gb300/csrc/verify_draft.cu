@@ -235,26 +235,33 @@ __global__ void __launch_bounds__(kMostThreadsV, 2) verify_kernel(const __grid_c
   const int in0 = off ? 1 : 0, in1 = (a.vocab + off) / V;  // whole pieces
   u64_t sum = 0, plain = 0;
   constexpr int U = V == 8 ? 2 : 4;  // pieces in flight
-  for (int c = max(c0, in0) + lane; c < min(c1, in1); c += 32 * U) {
-    Piece16<T, V> pp[U], qq[U];
+  // (a loop for each kind: asked at every pair of elements, the kind took as many instructions as the sums)
+  auto add_up = [&](auto kind) {
+    constexpr int WHAT = decltype(kind)::value;
+    for (int c = max(c0, in0) + lane; c < min(c1, in1); c += 32 * U) {
+      Piece16<T, V> pp[U], qq[U];
 #pragma unroll
-    for (int k = 0; k < U; ++k) {
-      const int at = min(c + 32 * k, in1 - 1) * V - off;
-      pp[k].load(p, at);
-      if (what == OVER) qq[k].load(q, at);
-    }
-    Sums s{};
+      for (int k = 0; k < U; ++k) {
+        const int at = min(c + 32 * k, in1 - 1) * V - off;
+        pp[k].load(p, at);
+        if (WHAT == OVER) qq[k].load(q, at);
+      }
+      Sums s{};
 #pragma unroll
-    for (int k = 0; k < U; ++k) {
-      if (c + 32 * k >= min(c1, in1)) continue;
-      float x_p[V], x_q[V];
-      pp[k].get(x_p);
-      if (what == OVER) qq[k].get(x_q);
-      weigh<V>(x_p, x_q, (c + 32 * k) * V - off, what, x, s, [](int, u64_t) {});
+      for (int k = 0; k < U; ++k) {
+        if (c + 32 * k >= min(c1, in1)) continue;
+        float x_p[V], x_q[V];
+        pp[k].get(x_p);
+        if (WHAT == OVER) qq[k].get(x_q);
+        weigh<V>(x_p, x_q, (c + 32 * k) * V - off, WHAT, x, s, [](int, u64_t) {});
+      }
+      sum += joined((int)s.hi, (int)s.lo);  // (16 elements)
+      plain += joined((int)s.p_hi, (int)s.p_lo);
     }
-    sum += joined((int)s.hi, (int)s.lo);  // (16 elements)
-    plain += joined((int)s.p_hi, (int)s.p_lo);
-  }
+  };
+  if (what == OVER) add_up(std::integral_constant<int, OVER>());
+  else if (what == WITHOUT) add_up(std::integral_constant<int, WITHOUT>());
+  else add_up(std::integral_constant<int, ALONE>());
   auto any_piece = [&](int c, int how, Sums& s, auto&& each) {
     float x_p[V], x_q[V];
     if (c >= in0 && c < in1) {
