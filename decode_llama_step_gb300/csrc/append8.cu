@@ -24,8 +24,10 @@
 // the largest magnitude, and again (from L1 or L2) for the codes, but for the
 // last few, which it still has.  The norm's factor of a row is taken into both
 // at the end.  All warps on one unit, rows in registers in between: a third
-// fewer instructions, half the warps, a barrier a unit, 44 us against 2x for
-// the chunks of a prefill batch.
+// fewer instructions, half the warps, a barrier a unit, 44 us for the chunks of
+// a prefill batch (9762 tokens, 8 heads of 128, bf16) against 32.
+// Measured (GPU time): those 31.9 us (9.0 at the copy rate; 68% of the issue
+// slots busy, instructions bound it), 64 single tokens 5.0 us.
 #include "kernels.h"
 #include "rope.cuh"
 

@@ -18,14 +18,16 @@
 // in any order give the same bits, and v sum w is compared exactly (its floor,
 // against whole sums).  u q(x) < p(x) is exact in a double.  The conversion
 // takes two additions: p + 2 holds p's first 22 bits in its mantissa, and what
-// is left, added to 3 2^-23, the next 23 (units of 2^-60 by shifts took three times
-// the instructions, which is what bounded the call: 24 us for 64 sequences).
+// is left, added to 3 2^-23, the next 23 (units of 2^-60 by shifts: 24 us for 64
+// sequences where this took 21, both with the kind of weight asked at every pair).
 //
 // What bounds it: the bytes of one row of p and one of q a sequence; the rows
 // of drafts that stand are never read but at one token.  A cluster of CTAs
 // takes a sequence, each a slice of the vocabulary: sums, exchanged through
 // distributed shared memory, then the CTA whose slice holds the border finds
 // the warp, the lane and the token by prefix sums of the (cached) slice.
+// Measured (GPU time; 128256 tokens, fp32): one sequence 6.9 us, 64 sequences
+// 16.9 us (9.8 at the copy rate), 22.7 with the rows in HBM.
 #include <cuda_bf16.h>
 #include <math.h>
 
