@@ -330,7 +330,8 @@ __global__ void __launch_bounds__(ATHREADS, 4) append8_kernel(const __grid_const
             amax = fmaxf(amax, most * r);
             if (s == last) break;
           } else {
-            const float f = r * inv;
+            // (lanes without elements keep their zeros, which every row's sum of squares takes in, also where r is no number)
+            const float f = live ? r * inv : 0.f;
             const f2_t f2 = pk2(f, f);
 #pragma unroll
             for (int e = 0; e < 8; e += 2) scale2(xa[e], xa[e + 1], f2), scale2(xb[e], xb[e + 1], f2);
