@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(kMostThreads, 1) reserve_kernel(const __grid_c
   const int per = (a.n_seqs + threads - 1) / threads, b0 = min(tid * per, a.n_seqs), b1 = min(b0 + per, a.n_seqs);
 
   int fresh[kPerThread], kv[kPerThread], held[kPerThread], need[kPerThread];
-  bool grant[kPerThread];
+  bool grant[kPerThread], lost[kPerThread];  // lost: over, in a state that cannot be
   int flags = 0;
   if (tid == 0) s_flags = s_used = s_end = 0;
   const int count_in = *a.free_count;
@@ -120,7 +120,8 @@ __global__ void __launch_bounds__(kMostThreads, 1) reserve_kernel(const __grid_c
     if (bad || far) flags |= kBadPos;
     grant[i] = !bad && !far && fresh[i] > 0;
     need[i] = grant[i] ? max(0, (int)(((long long)kv[i] + fresh[i] + page - 1) >> a.page_shift) - held[i]) : 0;
-    if (fresh[i] < 0 && bad) held[i] = 0;
+    lost[i] = bad && fresh[i] < 0;
+    if (lost[i]) held[i] = 0;
     if (fresh[i] < 0) give_sum = capped(give_sum, held[i]);
     need_sum = capped(need_sum, need[i]);
   }
@@ -196,8 +197,9 @@ __global__ void __launch_bounds__(kMostThreads, 1) reserve_kernel(const __grid_c
       const int b = b0 + i;
       if (b >= b1) continue;
       const bool over = fresh[i] < 0;
-      a.kv_len_out[b] = over ? 0 : kv[i] + cu[b + 1] - cu[b];
-      a.held_out[b] = over ? 0 : held[i] + need[i];
+      // (in place, what is there is the only record of pages that were not given back: it stays)
+      if (!lost[i] || a.kv_len_out != a.kv_len) a.kv_len_out[b] = over ? 0 : kv[i] + cu[b + 1] - cu[b];
+      if (!lost[i] || a.held_out != a.held) a.held_out[b] = over ? 0 : held[i] + need[i];
       a.cu_q[b + 1] = cu[b + 1];
     }
     if (tid == 0) {

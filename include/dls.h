@@ -618,9 +618,13 @@ uint64_t dls_attention_chunk_workspace_bytes(int32_t head_dim);
  * needs (dls_verify_draft takes tokens back, never pages).
  * status: bit 4 for lengths that do not fit (kv_len, held or free_count outside
  * their range, held below what kv_len needs, kv_len + new_len above page_tokens *
- * max_pages; such a request is left out, and is not given back if over; or more
- * pages coming back than the stack holds, of which the rest is dropped), bit 16 when a
- * request was left out for want of pages or rows, bit 1 for a slot of -1. */
+ * max_pages; such a request is left out; or more pages coming back than the stack
+ * holds, of which the rest is dropped), bit 16 when a request was left out for want
+ * of pages or rows, bit 1 for a slot of -1.
+ * A request that is over with a state that cannot be gives no page back.  Where
+ * kv_len_out is kv_len, and held_out held, its entries stay as they are, so that the
+ * caller still has what names its pages (with the table, whose row stays too) and
+ * can end it again once they are put right; in arrays of their own they are 0. */
 typedef struct dls_kv_reserve_desc {
   const int32_t* new_len;    /* device [n_seqs] */
   const int32_t* kv_len;     /* device [n_seqs]: cached tokens */

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from decode_llama_step_gb300 import dls
-from test_gpu_step8 import Batch8, CODES, ints, scale_of, turned
+from test_gpu_step8 import Batch8, CODES, Requests, ints, scale_of, turned
 
 pytestmark = pytest.mark.gpu
 
@@ -65,3 +65,38 @@ def test_append8_a_row_that_is_no_number_reaches_no_other(gpu_lib, code, hd, rot
             assert torch.equal(got[b][0][keep], first[b][0][keep])
             codes = got[b][0][mine].view(CODES[code]).float()
             assert bool((codes == 0).all()) if code == "i8" else bool(codes.isnan().all())
+
+
+@pytest.mark.parametrize("n,rows", [(6, 50), (40, 20000), (300, 4000)])
+def test_reserve_keeps_the_record_of_pages_that_it_cannot_take_back(gpu_lib, n, rows):
+    """Requests that are over with a state that cannot be, in place: length and held pages stay, for the caller to put right
+    and end again; arrays of their own hold 0."""
+    page = 16
+    r = Requests(n, page, 50 + n, spare=4 * n)
+    bad = {1: (-7, None), 2: (page * r.most + 1, None), 4: (5 + page * max(r.held[4], 1), max(r.held[4], 1)), n - 1: (0, r.most + 1)}
+    pages = {}
+    for b, (kv, held) in bad.items():
+        pages[b] = r.held[b]
+        r.kv[b] = kv
+        r.held[b] = r.held[b] if held is None else held
+    new = [-1 if b in bad else 1 for b in range(n)]
+    for inside in (False, True):
+        kv, held, count, table, stack = ints(r.kv), ints(r.held), ints([r.count]), ints(r.table), ints(r.stack)
+        kv_out, held_out = (kv, held) if inside else (torch.full_like(kv, 77), torch.full_like(held, 77))
+        cu, status = ints([0] * (n + 1)), ints([0])
+        dls.kv_reserve(ints(new), kv, held, table, stack, count, kv_out, held_out, count, cu, page, max_rows=rows, status=status)
+        assert status.item() == 4
+        taken = sum(r.kv[b] == page * r.held[b] for b in range(n) if b not in bad)
+        assert count.item() == r.count - taken
+        for b in range(n):
+            want = (r.kv[b] + 1, r.held[b] + (r.kv[b] == page * r.held[b])) if b not in bad else (r.kv[b], r.held[b]) if inside else (0, 0)
+            assert (kv_out[b].item(), held_out[b].item()) == want, b
+    # the lengths put right, the same requests end: their pages are on the stack
+    for b in bad:
+        kv[b], held[b] = 0, pages[b]
+    before = count.item()
+    dls.kv_reserve(ints([-1 if b in bad else 0 for b in range(n)]), kv, held, table, stack, count, kv, held, count, cu, page,
+                   max_rows=rows, status=status)
+    assert status.item() == 0 and count.item() == before + sum(pages.values())
+    back = stack.tolist()[before:count.item()]
+    assert sorted(back) == sorted(p for b in bad for p in r.table[b][:pages[b]])
