@@ -286,6 +286,14 @@ __global__ void __launch_bounds__(ATHREADS, 4) append8_kernel(const __grid_const
         }
       };
 
+      auto store = [&](int s) {
+        uint8_t* const p = out + (size_t)(off + s + sub) * hd;
+        *reinterpret_cast<uint2*>(p + ea) = make_uint2(Coder<CODE>::four(xa[0], xa[1], xa[2], xa[3]),
+                                                       Coder<CODE>::four(xa[4], xa[5], xa[6], xa[7]));
+        *reinterpret_cast<uint2*>(p + eb) = make_uint2(Coder<CODE>::four(xb[0], xb[1], xb[2], xb[3]),
+                                                       Coder<CODE>::four(xb[4], xb[5], xb[6], xb[7]));
+      };
+
       float amax = 0.f, scale = 0.f, inv = 0.f;
       const int last = (m - 1) / rps * rps;
       fetch(0);
@@ -317,6 +325,21 @@ __global__ void __launch_bounds__(ATHREADS, 4) append8_kernel(const __grid_const
           }
           if (lane == 0) *scale_at = scale;
           inv = 1.f / scale;
+          if (__builtin_expect((__float_as_uint(scale) & 0x7fffffu) != 0, 0)) {
+            // kept from elsewhere and no power of two, so the reciprocal is rounded: divisions, by themselves, since a
+            // choice between the two in the loop below costs 2% of the time
+#pragma unroll 1
+            for (int s = 0; s < m; s += rps) {
+              fetch(s);
+              values(s, m);
+              if (live && s + sub < m) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) xa[e] = __fdiv_rn(xa[e] * r, scale), xb[e] = __fdiv_rn(xb[e] * r, scale);
+                store(s);
+              }
+            }
+            break;
+          }
         }
 #pragma unroll 1
         for (int s = turn_no ? last : 0;;) {
@@ -336,11 +359,7 @@ __global__ void __launch_bounds__(ATHREADS, 4) append8_kernel(const __grid_const
 #pragma unroll
             for (int e = 0; e < 8; e += 2) scale2(xa[e], xa[e + 1], f2), scale2(xb[e], xb[e + 1], f2);
             if (live && s + sub < m) {
-              uint8_t* const p = out + (size_t)(off + s + sub) * hd;
-              *reinterpret_cast<uint2*>(p + ea) = make_uint2(Coder<CODE>::four(xa[0], xa[1], xa[2], xa[3]),
-                                                             Coder<CODE>::four(xa[4], xa[5], xa[6], xa[7]));
-              *reinterpret_cast<uint2*>(p + eb) = make_uint2(Coder<CODE>::four(xb[0], xb[1], xb[2], xb[3]),
-                                                             Coder<CODE>::four(xb[4], xb[5], xb[6], xb[7]));
+              store(s);
             }
             if (next == last) break;
             if (s == last) fetch(0);

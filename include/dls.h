@@ -648,12 +648,13 @@ typedef struct dls_kv_reserve_desc {
 int dls_kv_reserve(const dls_kv_reserve_desc* d, void* cuda_stream);
 
 /* dls_kv_append into pools of codes: K normed (where k_norm is given) and
- * rotated, V as it is, both divided by their block's scale and rounded once
- * (to the nearest, ties to even).  The scale is a power of two, 2^-64 to 2^64:
+ * rotated, V as it is, both divided by their block's scale in fp32 and the
+ * quotient rounded to the nearest code (ties to even).  The scale is a power of two, 2^-64 to 2^64:
  * the least under which the largest magnitude of the block's rows fits the
  * codes.  A block that already holds earlier tokens of the sequence keeps its scale
- * (any positive one) unless the new rows need a larger one; then its earlier
- * codes are divided by the growth and rounded again.  NaN becomes NaN (e4m3) or 0 and does not count for
+ * (any from 2^-64 to 2^64; others, and NaN, become the nearer end, as which
+ * dls_attention_chunk8 takes them) unless the new rows need a larger one; then its
+ * earlier codes are multiplied by old / new in fp32 and rounded again.  NaN becomes NaN (e4m3) or 0 and does not count for
  * the scale, an infinity the largest code.  Codes and scales of blocks that
  * get no row are left as they are.  A block belongs to one appending sequence: where two sequences
  * append to the same block in one call, its codes and scale are undefined, and

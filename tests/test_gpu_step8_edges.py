@@ -100,3 +100,76 @@ def test_reserve_keeps_the_record_of_pages_that_it_cannot_take_back(gpu_lib, n, 
     assert status.item() == 0 and count.item() == before + sum(pages.values())
     back = stack.tolist()[before:count.item()]
     assert sorted(back) == sorted(p for b in bad for p in r.table[b][:pages[b]])
+
+
+def kept_scale(had, code):
+    """What a scale that is there counts as: 2^-64 to 2^64, the nearer end where it lies outside or is none."""
+    return had.nan_to_num(0.0, math.inf, 0.0).clamp(2.0 ** -64, 2.0 ** 64)
+
+
+def coded(x, code):
+    return x.round().clamp(-127, 127).to(torch.int8) if code == "i8" else x.clamp(-448, 448).to(CODES["e4m3"])
+
+
+@pytest.mark.parametrize("code", ["e4m3", "i8"])
+@pytest.mark.parametrize("grows", [False, True])
+@pytest.mark.parametrize("typ", ["f32", "bf16"])
+def test_append8_into_blocks_of_any_scale(gpu_lib, code, grows, typ):
+    """Blocks filled elsewhere, whose scales are no powers of two: new rows are divided by the scale that stays, codes of one
+    that grows multiplied by old / new, both in fp32, and rounded to the nearest code."""
+    kvh, hd, page, block = 2, 128, 64, 64
+    lengths = [(9, 20 + b % 30) for b in range(64)]
+    B = Batch8(lengths, kvh, hd, page, block, code, 23)
+    B.fill(upto=[kl - ql for ql, kl in lengths])
+    x = torch.empty(B.rows, 2 * kvh, hd, device="cuda")
+    for b, (ql, kl) in enumerate(lengths):
+        p = int(B.table[b, 0])
+        if b == 0:
+            B.vs[p, 0, 0] = 0.010002499
+        size = torch.cat([B.ks[p, :, 0], B.vs[p, :, 0]])[None, :, None]
+        # halves of codes, times the scale, rounded: quotients on and next to the borders between codes
+        unit = (torch.randint(-126, 127, (ql, 2 * kvh, hd), generator=B.g, device="cuda") / 2) if code == "i8" else (
+            torch.randn(ql, 2 * kvh, hd, generator=B.g, device="cuda") * 60).clamp(-220, 220)
+        x[b * ql:(b + 1) * ql] = unit * size * (3.0 if grows else 1.0)
+    x = x.to({"f32": torch.float32, "bf16": torch.bfloat16}[typ])
+    if code == "i8" and typ == "f32" and not grows:
+        x[0, kvh, 0] = 0.02500625   # 2.5 times its scale in fp32, a tie: 2; times the reciprocal it is more
+    old = [t.clone() for t in (B.k, B.v, B.ks, B.vs)]
+    dls.kv_append8(x[:, :kvh], x[:, kvh:], B.k, B.v, B.ks, B.vs, B.table, B.cu_q, B.kv_len, None)
+    grown = 0
+    for b, (ql, kl) in enumerate(lengths):
+        p = int(B.table[b, 0])
+        for src, pool, scales, op, os_ in ((x[:, :kvh], B.k, B.ks, old[0], old[2]), (x[:, kvh:], B.v, B.vs, old[1], old[3])):
+            mine = src[b * ql:(b + 1) * ql].float()
+            most = mine.abs().amax((0, 2))
+            had = os_[p, :, 0]
+            want = torch.maximum(had, scale_of(most, code).float())
+            assert torch.equal(scales[p, :, 0], want)
+            grown += int((want > had).sum())
+            got = pool.view(torch.uint8)[p, :, kl - ql:kl].view(CODES[code])
+            assert torch.equal(got.view(torch.uint8), coded(mine / want[:, None], code).transpose(0, 1).contiguous().view(torch.uint8))
+            was = op.view(torch.uint8)[p, :, :kl - ql].view(CODES[code]).float()
+            f = (had / want)[:, None, None]
+            then = torch.where(f < 1, coded(was * f, code).float(), was)
+            assert torch.equal(pool.view(torch.uint8)[p, :, :kl - ql].view(CODES[code]).float(), then)
+    assert (grown > 100) == grows
+
+
+@pytest.mark.parametrize("code", ["e4m3", "i8"])
+def test_append8_into_blocks_whose_scale_is_none(gpu_lib, code):
+    """A scale of 0, a negative one, NaN or one outside 2^-64..2^64 counts as the nearer end, codes as they are, as the
+    attention takes it."""
+    odd = [0.0, -3.0, math.nan, 2.0 ** -80, 2.0 ** 70, math.inf, 2.0 ** 64, 2.0 ** -64]
+    lengths = [(1, 10)] * len(odd)
+    B = Batch8(lengths, 1, 64, 16, 16, code, 29)
+    B.fill(upto=[9] * len(odd))
+    p = B.table[:, 0].long()
+    had = torch.tensor(odd, device="cuda")
+    B.ks[p, 0, 0], B.vs[p, 0, 0] = had, had
+    old = B.v.clone()
+    x = torch.zeros(B.rows, 1, 64, device="cuda")
+    dls.kv_append8(x, x, B.k, B.v, B.ks, B.vs, B.table, B.cu_q, B.kv_len, None)
+    for scales in (B.ks, B.vs):
+        assert torch.equal(scales[p, 0, 0], kept_scale(had, code))
+    assert torch.equal(B.v.view(torch.uint8)[p, :, :9], old.view(torch.uint8)[p, :, :9])
+    assert not bool(B.v.view(torch.uint8)[p, :, 9].any())
