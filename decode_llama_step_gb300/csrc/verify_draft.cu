@@ -188,9 +188,9 @@ __global__ void __launch_bounds__(kMostThreadsV, 2) verify_kernel(const __grid_c
 
   // the first row whose draft does not stand, or the last row
   if (warp == 0) {
-    int stop = end - 1;
+    int stop = end - 1, r = start;
     bool strange = false;
-    for (int r = start; r < end - 1; r += 32) {
+    for (; r < end - 1; r += 32) {
       const int row = r + lane;
       bool falls = false;
       if (row < end - 1) {
@@ -211,6 +211,8 @@ __global__ void __launch_bounds__(kMostThreadsV, 2) verify_kernel(const __grid_c
       }
     }
     if (lane == 0) s_stop = stop;
+    if (rank == 0 && a.status)  // tokens behind the 32 that were looked at last
+      for (r += 32 + lane; r < end - 1; r += 32) strange |= a.tokens[r + 1] < 0 || a.tokens[r + 1] >= a.vocab;
     if (strange && rank == 0 && a.status) atomicOr(a.status, kBadToken);
   }
   __syncthreads();

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from decode_llama_step_gb300 import dls
-from test_gpu_step8 import Batch8, CODES, Requests, ints, scale_of, turned
+from test_gpu_step8 import Batch8, CODES, Requests, check_verify, ints, scale_of, turned
 
 pytestmark = pytest.mark.gpu
 
@@ -173,3 +173,16 @@ def test_append8_into_blocks_whose_scale_is_none(gpu_lib, code):
         assert torch.equal(scales[p, 0, 0], kept_scale(had, code))
     assert torch.equal(B.v.view(torch.uint8)[p, :, :9], old.view(torch.uint8)[p, :, :9])
     assert not bool(B.v.view(torch.uint8)[p, :, 9].any())
+
+
+@pytest.mark.parametrize("drawn", [False, True])
+def test_verify_flags_a_strange_token_anywhere(gpu_lib, drawn):
+    """A drafted token outside the vocabulary sets its bit also far behind the first draft that does not stand."""
+    for at in (3, 31, 32, 33, 68):
+        for token in (-1, 777, 1 << 30):
+            def edit(s, cu):
+                s["accept"][cu[1]] = 1e30       # the second sequence's first draft does not stand
+                s["tokens"][cu[1] + at] = token
+
+            want = check_verify([4, 70, 2], 777, "f32", drawn, 13, edit=edit, expect=2)
+            assert want[1][1] == 0
