@@ -9,10 +9,12 @@ namespace dls {
 
 namespace {
 
-// SMs of the current device, with the kernels' attributes set on it; 0 on an error.
-int device_ready(cudaError_t* err) {
+// SMs of the current device, with the attributes of the kernels over 16-bit pages, or over codes, set on it; 0 on an
+// error.  Each kind by itself: an attribute loads its kernel, and the 40 over codes took three quarters of the 3.2 ms
+// that the first call over 16-bit pages then was.
+int device_ready(bool codes, cudaError_t* err) {
   static std::mutex mu;
-  static int sms[64];
+  static int sms[64][2];
   int dev = 0;
   if ((*err = cudaGetDevice(&dev)) != cudaSuccess) return 0;
   if (dev < 0 || dev >= 64) {
@@ -20,17 +22,20 @@ int device_ready(cudaError_t* err) {
     return 0;
   }
   std::lock_guard<std::mutex> g(mu);
-  if (sms[dev]) return sms[dev];
+  if (sms[dev][codes]) return sms[dev][codes];
   int n = 0;
   if ((*err = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return 0;
+  if (codes) {
+    if ((*err = chunk_codes_setup()) != cudaSuccess || (*err = few_codes_setup()) != cudaSuccess) return 0;
+    return sms[dev][1] = n;
+  }
   const ChunkFn f[2] = {chunk_kernel<__half, 128, 0>, chunk_kernel<__nv_bfloat16, 128, 0>};
   const ChunkFn h[2] = {chunk_kernel<__half, 64, 0>, chunk_kernel<__nv_bfloat16, 64, 0>};
   for (int i = 0; i < 2; ++i) {
     if ((*err = cudaFuncSetAttribute(f[i], cudaFuncAttributeMaxDynamicSharedMemorySize, chunk_smem<128, 0>())) != cudaSuccess) return 0;
     if ((*err = cudaFuncSetAttribute(h[i], cudaFuncAttributeMaxDynamicSharedMemorySize, chunk_smem<64, 0>())) != cudaSuccess) return 0;
   }
-  if ((*err = chunk_codes_setup()) != cudaSuccess || (*err = few_codes_setup()) != cudaSuccess) return 0;
-  return sms[dev] = n;
+  return sms[dev][0] = n;
 }
 
 bool rows_ok(const void* p, long long stride, long long width) {
@@ -83,7 +88,7 @@ int attend(const dls_attention_chunk8_desc* d, const char* what, void* cuda_stre
                         (unsigned long long)d->workspace_bytes, (unsigned long long)dls_attention_chunk_workspace_bytes(hd));
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
   cudaError_t e = cudaSuccess;
-  const int sms = device_ready(&e);
+  const int sms = device_ready(d->code_type != 0, &e);
   if (e != cudaSuccess) return report_error(DLS_ERR_CUDA, "%s: cuda=%s", what, cudaGetErrorString(e));
   ChunkArgs a{};
   a.o = d->o, a.lse = d->lse;

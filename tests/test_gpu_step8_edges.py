@@ -1,6 +1,9 @@
 """Edges of the calls around the 8-bit paged cache, each against the definition: inputs that are no numbers, states that
 cannot be, scales of any size, lengths past a look of 32."""
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -186,3 +189,30 @@ def test_verify_flags_a_strange_token_anywhere(gpu_lib, drawn):
 
             want = check_verify([4, 70, 2], 777, "f32", drawn, 13, edit=edit, expect=2)
             assert want[1][1] == 0
+
+
+FIRST_CALLS = """
+import sys, time, torch
+sys.path.insert(0, sys.argv[1])
+from decode_llama_step_gb300 import dls
+z = lambda *s, t=torch.float16: torch.zeros(*s, dtype=t, device="cuda")
+i = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+q, k, k8, sc = z(1, 8, 64), z(2, 2, 16, 64), z(2, 2, 16, 64, t=torch.int8), torch.ones(2, 2, 1, device="cuda")
+rest = i([[0, 1]]), i([0, 1]), i([5]), torch.empty_like(q), z(dls.attention_chunk_workspace_bytes(64), t=torch.uint8)
+for f, a in ((dls.attention_chunk, (q, k, k)), (dls.attention_chunk8, (q, k8, k8, sc, sc))):
+    torch.cuda.synchronize()
+    t = time.perf_counter()
+    f(*a, *rest)
+    torch.cuda.synchronize()
+    print(time.perf_counter() - t)
+"""
+
+
+def test_a_call_over_16_bit_pages_loads_no_kernel_over_codes(gpu_lib):
+    """In a process of its own the first call over 16-bit pages is short beside the first one over codes, which has ten
+    times the kernels: each pays for its own."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    runs = [subprocess.run([sys.executable, "-c", FIRST_CALLS, root], capture_output=True, text=True, check=True).stdout.split()
+            for _ in range(3)]
+    pages, codes = (min(float(r[x]) for r in runs) for x in (0, 1))
+    assert codes > pages, (pages, codes)
