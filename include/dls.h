@@ -690,9 +690,23 @@ int dls_kv_append8(const dls_kv_append8_desc* d, void* cuda_stream);
 
 /* dls_attention_chunk over pools of codes: the same rows, masks, guarantees
  * and workspace (one serves both calls, not at the same time).  q and o are
- * q_type.  Scales may be any from 2^-64 to 2^64 (others, and NaN, count as the nearer end);
- * codes enter the products exactly, the softmax weights times V's scale are
- * rounded to q_type.  NaN codes count as the other call's NaN. */
+ * q_type.  Scales may be any from 2^-64 to 2^64 (others, and NaN, count as the nearer end).
+ * Products are of halves (fp16) whatever q_type is: codes are halves exactly; a bf16
+ * row of q times the power of two that puts its largest value next to 2^15 is one
+ * but for what lies 2^38 below that value; the softmax weights times V's scale are
+ * rounded to eleven bits (those below 2^-21 of the row's largest to steps of 2^-31
+ * of it), in the sum of weights they are not.  A weight times V's scale below 2^-118
+ * of the row's largest may count as 0, in that sum too.  NaN codes count as the
+ * other call's NaN.
+ * There are two kernels, and the one for few rows is taken where n_tokens * (n_heads
+ * / n_kv_heads) is at most 32 * n_seqs and a KV head has at most 16 query heads: what
+ * the host knows, which does not see the lengths.  A long chunk in such a batch (among
+ * single tokens, or sequences without rows) reads its keys once for every eight or
+ * sixteen query rows, and takes up to six times as long as alone; single tokens take
+ * twice as long in a batch that goes to the other kernel, for its chunks or its padding rows.
+ * A caller whose sequences are ordered by kind does better with a call for each
+ * kind: n_seqs, and cu_q, kv_len and page_table from its first sequence on; q and o
+ * stay whole, n_tokens is the last row's number and one. */
 typedef struct dls_attention_chunk8_desc {
   const void* q;            /* q_type [n_tokens][n_heads][head_dim], rotated */
   const void* k_pages;      /* pools of codes */
@@ -740,7 +754,10 @@ int dls_attention_chunk8(const dls_attention_chunk8_desc* d, void* cuda_stream);
  * In the sums probabilities count as 0..1 (NaN as 0), whatever they add up to, and
  * pick as 0 <= x < 1 (NaN as 0); a comparison with a NaN says that the draft does
  * not stand.  A drafted token outside [0, vocab) does not stand and sets status bit 2; bit 4 marks a cu_q that does
- * not fit, whose sequence has n_accepted 0 and no out_tokens. */
+ * not fit, whose sequence has n_accepted 0 and no out_tokens.
+ * A prompt's rows in the same batch are taken for drafts too, and have rows of target (and draft) like them, though only
+ * the last one's probabilities matter: an accept below 0 keeps the next token where either probability is above 0
+ * (draft = NULL: always), so the prompt goes through whole and its length stays. */
 typedef struct dls_verify_draft_desc {
   const int32_t* tokens;    /* device [n_tokens] */
   const void* target;       /* prob_type [n_tokens][vocab] */

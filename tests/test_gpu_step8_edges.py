@@ -9,7 +9,7 @@ import pytest
 import torch
 
 from decode_llama_step_gb300 import dls
-from test_gpu_step8 import Batch8, CODES, Requests, check_verify, ints, scale_of, turned
+from test_gpu_step8 import Batch8, CODES, Requests, TYPES, attend64, check_verify, close_attend, ints, rounding, scale_of, turned, workspace
 
 pytestmark = pytest.mark.gpu
 
@@ -216,3 +216,92 @@ def test_a_call_over_16_bit_pages_loads_no_kernel_over_codes(gpu_lib):
             for _ in range(3)]
     pages, codes = (min(float(r[x]) for r in runs) for x in (0, 1))
     assert codes > pages, (pages, codes)
+
+
+# ---- what the header says of weights, scales and prompts in a batch --------------------------------------
+
+def near_cancelling(lengths, kvh, hd, code, seed):
+    """A batch whose values cancel: neighbours' V are each other's negatives, keys nearly alike."""
+    B = Batch8(lengths, kvh, hd, 32, 32, code, seed)
+    B.fill()
+    for b, (_, kl) in enumerate(lengths):
+        p, s = B.slots(b, 0, kl)
+        sign = 1 - 2 * (torch.arange(kl, device="cuda") % 2)
+        v = B.v.view(torch.uint8)[p, :, s].view(CODES[code]).float()
+        v = v[:1].clamp(min=-127) * sign[:, None, None]
+        B.v.view(torch.uint8)[p, :, s] = v.to(CODES[code]).view(torch.uint8)
+    B.ks.mul_(0.05)
+    return B
+
+
+@pytest.mark.parametrize("typ", ["f16", "bf16"])
+@pytest.mark.parametrize("code", ["e4m3", "i8"])
+@pytest.mark.parametrize("hd,lengths", [(128, [(1, 2), (1, 3), (1, 4), (1, 6)] * 20), (64, [(1, 2), (1, 3), (1, 5)] * 20),
+                                        (128, [(40, 42), (50, 51), (45, 49)] * 4), (64, [(40, 42), (50, 51), (45, 49)] * 4)])
+def test_attention8_weights_are_halves(gpu_lib, typ, code, hd, lengths):
+    """Weights are rounded to eleven bits whatever q's type: few keys, whose values cancel, so that the output is small beside
+    what it is summed from and its own rounding hides nothing."""
+    B = near_cancelling(lengths, 2, hd, code, 37)
+    q = torch.randn(B.rows, 4, hd, generator=B.g, device="cuda").to(TYPES[typ])
+    o, ws = torch.empty_like(q), workspace(hd)
+    dls.attention_chunk8(q, B.k, B.v, B.ks, B.vs, B.table, B.cu_q, B.kv_len, o, ws)
+    want, _, mag, dot = attend64(B, q, 4, hd ** -0.5, True, 0)
+    # as close_attend, with a half's half step for the weights, below its normal range 2^-32 of the largest V
+    ds = (hd + 8) * 2.0 ** -23 * dot + 2.0 ** -16
+    top = 128.0 if code == "i8" else 448.0
+    lim = (2.0 ** -11 * (1 + 2.0 ** -6) + 2 * ds[..., None] + 2 * 66 * 2.0 ** -23) * mag + rounding(want, TYPES[typ]) * (1 + 2.0 ** -6)
+    lim = lim + 64 * 2.0 ** -32 * top * float(B.vs.nan_to_num(0.0).max())
+    err = (o.double() - want).abs()
+    assert bool((err <= lim).all()), float((err / lim).max())
+    if typ == "bf16":  # the test would see weights of eight bits
+        assert float((lim / (mag * 2.0 ** -9).clamp(min=1e-30))[..., 0].median()) < 1
+
+
+@pytest.mark.parametrize("typ", ["f16", "bf16"])
+@pytest.mark.parametrize("rows", [1, 40])
+def test_attention8_scales_2_to_the_110_apart(gpu_lib, typ, rows):
+    """Keys of equal weight whose V scales are 2^-50 and 2^60: all count in the sum of weights."""
+    B = Batch8([(rows, 300), (rows, 64)], 2, 64, 32, 16, "e4m3", 41)
+    B.fill()
+    for b, (_, kl) in enumerate(B.lengths):
+        p, s = B.slots(b, 0, kl)
+        small = torch.arange(kl, device="cuda") // 16 % 2 == 0
+        B.vs[p, :, s // 16] = torch.where(small, 2.0 ** -50, 2.0 ** 60)[:, None].expand(-1, 2)
+    q = torch.randn(B.rows, 4, 64, generator=B.g, device="cuda").to(TYPES[typ])
+    out = torch.empty_like(q)
+    lse = torch.empty(B.rows, 4, device="cuda")
+    B.v.view(torch.uint8).bitwise_and_(0x80)   # (values of 2^60 do not fit the output: zeros, the sum is what is looked at)
+    dls.attention_chunk8(q, B.k, B.v, B.ks, B.vs, B.table, B.cu_q, B.kv_len, out, workspace(64), lse=lse)
+    close_attend(B, out, lse, attend64(B, q, 4, 0.125, True, 0))
+
+
+@pytest.mark.parametrize("typ,heads,hd", [("bf16", 8, 128), ("f16", 4, 64)])
+def test_attention8_a_call_for_each_kind_of_sequence(gpu_lib, typ, heads, hd):
+    """Single tokens first, chunks behind: two calls over parts of the same lengths, tables and rows are one over all, and
+    the first leaves the other's rows alone."""
+    n, chunks = 30, [(200, 700), (90, 90)]
+    B = Batch8([(1, 50 + 40 * b) for b in range(n)] + chunks, 2, hd, 32, 32, "e4m3", 47, first=2, pad=3)
+    B.fill()
+    q = torch.randn(B.rows, heads, hd, generator=B.g, device="cuda").to(TYPES[typ])
+    o, ws, status = torch.full_like(q, 7.0), workspace(hd), ints([9])
+    pools = B.k, B.v, B.ks, B.vs
+    rows = B.starts[n]
+    dls.attention_chunk8(q[:rows], *pools, B.table[:n], B.cu_q[:n + 1], B.kv_len[:n], o[:rows], ws, status=status)
+    dls.attention_status(status)
+    assert bool((o[rows:] == 7).all()) and bool((o[:2] == 7).all()) and not bool((o[2:rows] == 7).all())
+    dls.attention_chunk8(q, *pools, B.table[n:], B.cu_q[n:], B.kv_len[n:], o, ws, status=status)
+    dls.attention_status(status)
+    close_attend(B, o, None, attend64(B, q, heads, hd ** -0.5, True, 0))
+    assert bool((o[B.starts[-1]:] == 7).all())
+
+
+def test_verify_of_a_batch_with_prompts(gpu_lib):
+    """accept below 0 keeps a row's next token where its probabilities are above 0: a prompt's rows go through whole, its
+    length stays, and the token after it comes from its last row."""
+    def prompts(s, cu):
+        s["accept"][cu[1]:cu[2]] = -1.0
+        s["tokens"][cu[1]:cu[2]] = torch.randint(0, 500, (cu[2] - cu[1],), device="cuda", dtype=torch.int32)
+
+    for drawn in (False, True):
+        want = check_verify([4, 90, 1, 3], 500, "f32", drawn, 43, edit=prompts)
+        assert want[1][1] == 89 and want[1][0][-1] >= 0
