@@ -102,7 +102,7 @@ int attend(const dls_attention_chunk8_desc* d, const char* what, void* cuda_stre
   a.causal = d->causal, a.window = d->window;
   a.tpq = tpq, a.tile_tokens = 2 * tpq, a.inv_group = (65536 + a.group - 1) / a.group;
   a.c = (d->scale > 0.f ? d->scale : 1.0f / sqrtf((float)hd)) * 1.4426950408889634f;
-  // a lane of the planning warp walks at most 4 sequences and 8 more tiles; its sums fit 32 bits.
+  // A lane of the planning warp walks at most 4 sequences and 8 more tiles; its sums fit 32 bits.
   // One token over 2048: 15.5 us with the warp's plan, 16.2 with the block's; 64 over up to 8192 (5301 on average) 218 and 220 us.
   a.small_plan = d->n_seqs <= 128 && d->n_tokens <= 8 * 2 * a.tpq && (long long)d->max_pages * pt <= 1 << 24;
   a.k_scales = d->k_scales, a.v_scales = d->v_scales;
@@ -114,13 +114,21 @@ int attend(const dls_attention_chunk8_desc* d, const char* what, void* cuda_stre
   // operands of 128 rows.  4 heads a KV head of 128 and 8 sequences over 4096: 16
   // rows 27 us (46 by the other), 32 rows 38 (47), 48 rows 52 (48); 64 over
   // 2048: 76 (152), 132 (152), 187 (155); heads of 64 alike.  The number of rows
-  // alone is known here, so a batch may hold a longer sequence all the same;
-  // its tiles then read their keys once for every sixteen rows, and all
-  // the batch's tiles are no more than those of equal sequences.
+  // alone is known here, and batches of unequal sequences are not served well
+  // (32/8 heads of 128, bf16, e4m3): a long chunk taken this way reads its keys
+  // once for every eight or sixteen rows (256 tokens over 16384 beside 64 single
+  // ones over 2048: 471 us, 232 by the other kernel, 160 as a call for each kind;
+  // 512 over 16384 among 63 sequences without rows: 752, 151 by the other), and
+  // single tokens taken the other way work on tiles of 256 rows (64 over 2048
+  // with 2048 over 16384: 657, 545 as two calls; with 2000 rows of padding: 130,
+  // 70 this way).
   const bool few = d->code_type && a.group <= kFewRows && (long long)d->n_tokens * a.group <= 2 * kFewRows * (long long)d->n_seqs;
   if (few) {
     const int rows = (long long)d->n_tokens * a.group <= 8 * (long long)d->n_seqs && a.group <= 8 ? 8 : kFewRows;
     a.tile_tokens = rows / a.group;
+    // Here the warp plans up to 128 tiles' worth of rows (its sums still fit 32 bits).  Single tokens over 2048, 32/8 heads
+    // of 128: one 10.1 us (10.5 with the block's plan), 16 22.8 (23.6), 128 104.3 (104.9).  Where one sequence has
+    // most of the tiles, one lane walks them all: 385 tokens beside 127 single ones 225 (217), 512 over 1000 alone 97 (81).
     a.small_plan = d->n_seqs <= 128 && d->n_tokens <= 128 * a.tile_tokens && (long long)d->max_pages * pt <= 1 << 24;
     const CUtensorMapSwizzle sw = hd == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : hd == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE;
     if (!make_tmap_2d(&tk, CU_TENSOR_MAP_DATA_TYPE_UINT8, d->k_pages, hd, a.pool_rows, hd, hd, pr, sw) ||

@@ -945,7 +945,7 @@ __global__ void __launch_bounds__(kThreads<CODE>, 1) chunk_kernel(const __grid_c
   int* const ab = &sh.abort;
 
   if (warp < 4) {
-    // (what the block was launched with, 168 or 128 a thread, is shared out anew)
+    // (what the block was launched with, 168 or 96 a thread, is shared out anew)
     if constexpr (CODE != 0) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     else asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == 0) {

@@ -26,7 +26,7 @@
 // workspace in range order.
 //
 // What bounds it, measured (GPU time): 64 single tokens of 64 heads over up to
-// 8192 cached (0.7 GB of codes) 121 us, 5.8 TB/s of 6.7 (374 us through the
+// 8192 cached (0.7 GB of codes) 121 us, 5.8 TB/s of 6.7 (272 us through the
 // tensor-memory kernel): HBM, with a warp's step of 1450 cycles for 1310 of
 // HBM's close behind it.  One token over 2048, 32 heads: 9.4 us, a chain of launch, plan, page table, copy,
 // step and join.  Sixteen warps of 96 registers in place of eight: 202 us (their
