@@ -436,10 +436,10 @@ def kv_reserve(new_len, kv_len, held, page_table, free_pages, free_count, kv_len
                page_tokens, *, positions=None, slots=None, seq_ids=None, max_rows=None, status=None, stream=None):
     """Pages and rows of a batch from its requests' lengths (device int32 [sequences]): new_len tokens join kv_len ones
     (negative: the request is over, its pages go back on the stack free_pages, whose free_count lowest entries are
-    free).  Fresh pages go into page_table [sequences, pages], rows into cu_q [sequences + 1] and, where given,
-    positions, slots (page * page_tokens + offset) and seq_ids [rows].  kv_len_out, held_out and free_count_out may be
-    their inputs.  max_rows: the arrays' length where one is given.  stream None is the default stream, as in
-    qk_norm_rope."""
+    free; in place, one in a state that cannot be keeps it).  Fresh pages go into page_table [sequences, pages], rows into
+    cu_q [sequences + 1] and, where given, positions, slots (page * page_tokens + offset) and seq_ids [rows].  kv_len_out,
+    held_out and free_count_out may be their inputs.  max_rows: the arrays' length where one is given.  stream None is
+    the default stream, as in qk_norm_rope."""
     _dtypes or _types()
     i32_, device = _torch.int32, new_len.get_device()
     if page_table.dim() != 2:
@@ -494,7 +494,9 @@ def kv_append8(k, v, k_pages, v_pages, k_scales, v_scales, page_table, cu_q, kv_
 def attention_chunk8(q, k_pages, v_pages, k_scales, v_scales, page_table, cu_q, kv_len, o, workspace, *, lse=None, scale=0.0,
                      causal=True, window=0, status=None, stream=None):
     """attention_chunk over pages of codes (float8_e4m3fn or int8) with a scale for each block of tokens and head; q and
-    o [tokens, heads, head_dim] in float16 or bfloat16.  workspace: as attention_chunk's, which may be the same one."""
+    o [tokens, heads, head_dim] in float16 or bfloat16.  workspace: as attention_chunk's, which may be the same one.  A
+    batch of single tokens and long chunks does better as a call for each kind of sequence (parts of page_table, cu_q and
+    kv_len; q and o up to the kind's last row)."""
     typ, device = _dtype(q, "q"), q.get_device()
     code, block, ksp, vsp = _codes(k_pages, v_pages, k_scales, v_scales, device)
     pages, kvh, pt, hd, kpp, vpp, table, most, cu, kl, seqs = _pools(k_pages, v_pages, page_table, cu_q, kv_len, device)

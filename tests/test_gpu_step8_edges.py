@@ -212,7 +212,8 @@ def test_a_call_over_16_bit_pages_loads_no_kernel_over_codes(gpu_lib):
     """In a process of its own the first call over 16-bit pages is short beside the first one over codes, which has ten
     times the kernels: each pays for its own."""
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
-    runs = [subprocess.run([sys.executable, "-c", FIRST_CALLS, root], capture_output=True, text=True, check=True).stdout.split()
+    runs = [subprocess.run([sys.executable, "-c", FIRST_CALLS, root], capture_output=True, text=True, check=True,
+                           env={**os.environ, "CUDA_MODULE_LOADING": "LAZY"}).stdout.split()
             for _ in range(3)]
     pages, codes = (min(float(r[x]) for r in runs) for x in (0, 1))
     assert codes > pages, (pages, codes)
